@@ -363,6 +363,43 @@ int moe_layer_noalloc(const moe_shape* s, const void* x, int x_dtype, const void
                       int32_t* row_token, int32_t* row_slot, int32_t* slot_row, void* stream);
 
 /*
+ * moe_layer_few_tokens -- the layer share for a few tokens (0 <= T <=
+ * MOE_FEW_TOKENS_MAX, a decode step), bound by reading the chosen experts'
+ * weights once.  Same routing rule, weights and shard semantics as
+ * moe_layer(), from the same packed weights, with two differences:
+ *   - logits are summed in double precision (moe_route: a float32 fma chain).
+ *     Where two experts' logits are closer than the chain's rounding, the two
+ *     may choose differently; exactly equal double sums go to the lower index.
+ *   - nothing between x and out is rounded below 22 bits: SwiGLU activations
+ *     and expert outputs are not rounded to fp16, so out is a float32 result.
+ *   Arguments as in moe_layer(); topk_idx [T, K] int32 and topk_w [T, K]
+ *   float32 are optional outputs.  Rows of tokens with no local expert are
+ *   written as zeros.  float32 x saturates at 65504 (fp16 parts), as in
+ *   moe_layer(); so do the weighted SwiGLU activations.
+ *   ws: moe_layer_few_tokens_workspace_bytes(s) bytes of device scratch, any
+ *   contents; calls that overlap in time need workspaces of their own.
+ *   T > MOE_FEW_TOKENS_MAX, or T * K * I or T * H beyond 2^31 / 6:
+ *   MOE_ERR_UNSUPPORTED (the size query returns 0).
+ */
+#define MOE_FEW_TOKENS_MAX 32
+size_t moe_layer_few_tokens_workspace_bytes(const moe_shape* s);
+int moe_layer_few_tokens(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
+                         const float* bias, const void* packed, float* out, int32_t* topk_idx, float* topk_w,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_layer_few_tokens_mxfp8 -- moe_layer_few_tokens() on the MXFP8 weights of
+ * moe_pack_weights_mxfp8() (H and I multiples of 256).  The weights' values
+ * are used exactly; x and the SwiGLU activations are NOT quantised (unlike
+ * moe_layer_mxfp8(), whose matrix instruction takes both operands in MXFP8):
+ * at this size the weights' bytes are the cost, and unquantised rows add none.
+ */
+size_t moe_layer_few_tokens_workspace_bytes_mxfp8(const moe_shape* s);
+int moe_layer_few_tokens_mxfp8(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
+                               const float* bias, const void* packed, float* out, int32_t* topk_idx, float* topk_w,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Measurement helpers (not part of the layer).  moe_probe_mfma_bf16 launches
  * `blocks` workgroups of 8 waves, each wave issuing `iters` rounds of eight
  * independent v_mfma_f32_32x32x16_bf16 with no memory traffic, and writes one

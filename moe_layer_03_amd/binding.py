@@ -45,7 +45,11 @@ EXPORTED = [
     "moe_probe_mfma_bf16_flops", "moe_probe_mfma_bf16", "moe_layer_noalloc",
     "moe_packed_weight_bytes_mxfp8", "moe_pack_weights_mxfp8", "moe_quantize_mxfp8", "moe_grouped_gemm_mxfp8",
     "moe_layer_workspace_bytes_mxfp8", "moe_layer_mxfp8",
+    "moe_layer_few_tokens_workspace_bytes", "moe_layer_few_tokens",
+    "moe_layer_few_tokens_workspace_bytes_mxfp8", "moe_layer_few_tokens_mxfp8",
 ]
+
+MOE_FEW_TOKENS_MAX = 32
 
 MOE_LAYER_NOALLOC_MAX_WS_BYTES = 64 << 20
 
@@ -136,6 +140,10 @@ def load() -> ctypes.CDLL:
         "moe_grouped_gemm_mxfp8": (i32, [_S, _P, _P, _P, _P, _P, i32, i32, _P, i32, _P, _P]),
         "moe_layer_workspace_bytes_mxfp8": (sz, [_S]),
         "moe_layer_mxfp8": (i32, [_S, _P, i32, _P, i32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]),
+        "moe_layer_few_tokens_workspace_bytes": (sz, [_S]),
+        "moe_layer_few_tokens": (i32, [_S, _P, i32, _P, i32, _P, _P, _P, _P, _P, _P, sz, _P]),
+        "moe_layer_few_tokens_workspace_bytes_mxfp8": (sz, [_S]),
+        "moe_layer_few_tokens_mxfp8": (i32, [_S, _P, i32, _P, i32, _P, _P, _P, _P, _P, _P, sz, _P]),
         "moe_probe_mfma_bf16_flops": (ctypes.c_int64, [i32, i32]),
         "moe_probe_mfma_bf16": (i32, [i32, i32, _P, _P]),
     }
@@ -507,3 +515,49 @@ def moe_layer_mxfp8(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed: t
                                 _ptr(ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream))
     _check("moe_layer_mxfp8", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# the layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def moe_layer_few_tokens_workspace_bytes(s: Shape) -> int:
+    return int(load().moe_layer_few_tokens_workspace_bytes(ctypes.byref(s.c())))
+
+
+def moe_layer_few_tokens_workspace_bytes_mxfp8(s: Shape) -> int:
+    return int(load().moe_layer_few_tokens_workspace_bytes_mxfp8(ctypes.byref(s.c())))
+
+
+def _layer_few_tokens(mx: bool, s: Shape, x, w_router, packed, bias, out, ws, topk_idx, topk_w, stream):
+    name = "moe_layer_few_tokens_mxfp8" if mx else "moe_layer_few_tokens"
+    need = (moe_layer_few_tokens_workspace_bytes_mxfp8 if mx else moe_layer_few_tokens_workspace_bytes)(s)
+    weights = (moe_packed_weight_bytes_mxfp8 if mx else moe_packed_weight_bytes)(s)
+    if packed.numel() < weights:
+        raise ValueError(f"packed must hold {weights} bytes, got {packed.numel()}")
+    if out is None:
+        out = _empty((s.T, s.H), torch.float32, x.device)
+    if ws is None:
+        ws = _empty(max(need, 16), torch.uint8, x.device)
+    st = getattr(load(), name)(
+        ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x), _ptr(w_router, None, s.H * s.E, "w_router"),
+        _dt(w_router), _ptr(bias, torch.float32, s.E, "bias"), _ptr(packed, torch.uint8, None, "packed"),
+        _ptr(out, torch.float32, s.T * s.H, "out"), _ptr(topk_idx, torch.int32, s.T * s.K, "topk_idx"),
+        _ptr(topk_w, torch.float32, s.T * s.K, "topk_w"), _ptr(ws, torch.uint8, None, "ws"), ws.numel(),
+        _stream(stream))
+    _check(name, st)
+    return out
+
+
+def moe_layer_few_tokens(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed: torch.Tensor,
+                         bias: Optional[torch.Tensor] = None, out=None, ws=None, *, topk_idx=None, topk_w=None,
+                         stream=None) -> torch.Tensor:
+    """The layer share for at most MOE_FEW_TOKENS_MAX tokens (packed from moe_pack_weights)."""
+    return _layer_few_tokens(False, s, x, w_router, packed, bias, out, ws, topk_idx, topk_w, stream)
+
+
+def moe_layer_few_tokens_mxfp8(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed: torch.Tensor,
+                               bias: Optional[torch.Tensor] = None, out=None, ws=None, *, topk_idx=None, topk_w=None,
+                               stream=None) -> torch.Tensor:
+    """The layer share for a few tokens with MXFP8 weights (packed from moe_pack_weights_mxfp8)."""
+    return _layer_few_tokens(True, s, x, w_router, packed, bias, out, ws, topk_idx, topk_w, stream)

@@ -182,6 +182,26 @@ int check_mx_shape(const moe_shape* s) {
     return MOE_OK;
 }
 
+// moe_layer_few_tokens: the layer's limits, and a batch the kernels are sized for.
+int check_few_shape(const moe_shape* s, bool mx) {
+    MOE_TRY(mx ? check_mx_shape(s) : check_shape(s));
+    return few_tokens_fits(*s) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+int layer_few_tokens(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
+                     const float* bias, const void* packed, bool mx, float* out, int32_t* topk_idx, float* topk_w,
+                     void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_few_shape(s, mx));
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return MOE_ERR_UNSUPPORTED;
+    if (x_dtype != w_dtype) return MOE_ERR_UNSUPPORTED;
+    if (!opt4(topk_idx) || !opt4(topk_w) || !opt4(bias)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < few_tokens_workspace(*s, nullptr, nullptr)) return MOE_ERR_WORKSPACE;
+    if (s->T == 0) return MOE_OK;   // no tokens; empty tensors may have null pointers
+    if (!ok16(ws) || !ok16(x) || !ok16(w_router) || !ok16(packed) || !ok16(out)) return MOE_ERR_INVALID_ARG;
+    return launch_few_tokens(*s, x, x_dtype, w_router, bias, packed, mx, out, topk_idx, topk_w, ws,
+                             static_cast<hipStream_t>(stream));
+}
+
 }  // namespace
 
 void set_last_hip_error(hipError_t e) { g_last_hip_error = static_cast<int32_t>(e); }
@@ -472,6 +492,30 @@ int moe_layer_noalloc(const moe_shape* s, const void* x, int x_dtype, const void
     MOE_TRY(scratch_of_current_device(&ws));
     return moe_layer(s, x, x_dtype, w_router, w_dtype, bias, packed, out, topk_idx, topk_w, counts, offsets,
                      row_token, row_slot, slot_row, ws, MOE_LAYER_NOALLOC_MAX_WS_BYTES, stream);
+}
+
+size_t moe_layer_few_tokens_workspace_bytes(const moe_shape* s) {
+    if (check_few_shape(s, false) != MOE_OK) return 0;
+    return few_tokens_workspace(*s, nullptr, nullptr);
+}
+
+size_t moe_layer_few_tokens_workspace_bytes_mxfp8(const moe_shape* s) {
+    if (check_few_shape(s, true) != MOE_OK) return 0;
+    return few_tokens_workspace(*s, nullptr, nullptr);
+}
+
+int moe_layer_few_tokens(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
+                         const float* bias, const void* packed, float* out, int32_t* topk_idx, float* topk_w, void* ws,
+                         size_t ws_bytes, void* stream) {
+    return layer_few_tokens(s, x, x_dtype, w_router, w_dtype, bias, packed, false, out, topk_idx, topk_w, ws, ws_bytes,
+                            stream);
+}
+
+int moe_layer_few_tokens_mxfp8(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
+                               const float* bias, const void* packed, float* out, int32_t* topk_idx, float* topk_w,
+                               void* ws, size_t ws_bytes, void* stream) {
+    return layer_few_tokens(s, x, x_dtype, w_router, w_dtype, bias, packed, true, out, topk_idx, topk_w, ws, ws_bytes,
+                            stream);
 }
 
 const char* moe_status_string(int status) {

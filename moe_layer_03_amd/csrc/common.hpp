@@ -178,4 +178,19 @@ int launch_mx_grouped_gemm(const moe_shape& s, const uint8_t* a, const uint8_t* 
                            const int32_t* offsets, const uint8_t* packed, int which, int epilogue, void* c,
                            int c_dtype, uint8_t* c_scales, hipStream_t st);
 
+// The layer for a few tokens (few.hip)
+struct FewWs {
+    double* part;      // partial logits
+    int32_t* idx;
+    float* w;
+    uint16_t* x;       // parts of float32 rows
+    uint16_t* h;       // parts of the weighted SwiGLU rows
+};
+// Whether the shape is within the few-token layer's limits.
+bool few_tokens_fits(const moe_shape& s);
+// Bytes of its workspace; with w, carves it from base.
+size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w);
+int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void* w_router, const float* bias,
+                      const void* packed, bool mx, float* out, int32_t* idx, float* tw, void* ws, hipStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,606 @@
+// The whole layer for a few tokens (at most MOE_FEW_TOKENS_MAX).
+//
+// Mathematics, for token t:
+//   l[t,e] = sum_h x[t,h] Wr[h,e] + b[e], summed in double precision;
+//   the K largest, ties to the lower index; w_j = exp(l_j - l_0) / sum_i exp(l_i - l_0);
+//   a_{t,j} = w_j silu(x_t Wg_e) (x_t Wu_e), e the expert of slot j;
+//   out_t = sum over local slots of a_{t,j} Wd_e.
+// With so few rows the layer is bound by reading the chosen experts' weights
+// once: 6 H I bytes per expert (16-bit) against 6 H I operations per row.
+//
+// Three steps:
+//   route    partial logits over slices of H, double-precision MFMA;
+//   gate/up  every workgroup sums the partials and selects the experts itself
+//            (T rows of E values, cheaper than another launch), then takes
+//            (chosen expert, 16 columns) units; its waves share the unit's H;
+//   down     the weights w_j are folded into the rows a, so the down product
+//            and the weighted combination over experts are ONE product with a
+//            long reduction: out[T, n] = [rows of every chosen expert] x
+//            [their down weights stacked], where row t of an expert's slice is
+//            zero if token t did not choose it.  A workgroup owns 16 output
+//            columns and the whole reduction: no scatter, no atomics, and the
+//            summation order does not depend on timing.
+// An MFMA row is a token in both products (no packing): rows of tokens that
+// did not choose the expert load zeros through an out-of-range buffer offset,
+// without memory traffic.
+//
+// Precision: the rows a are kept to 22 bits (two fp16 parts) or 24 (three bf16
+// parts, MXFP8), and nothing else is rounded below float32, so the float32
+// output is a float32 result, not an fp16 one (stream.hpp).
+#include "stream.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kNW = 8;                                 // waves per workgroup of the two products
+constexpr int kRouteNW = 8;
+constexpr int kMaxSlices = 16;
+
+typedef double doublex4 __attribute__((ext_vector_type(4)));
+
+struct FewArgs {
+    const uint16_t* a;         // gate/up rows: parts [NP][T][H]
+    int64_t a_part;            // elements per part
+    const uint8_t* gu;         // packed gate/up weights (16-bit or MXFP8 codes)
+    const uint8_t* gu_scales;
+    const uint8_t* dn;
+    const uint8_t* dn_scales;
+    const double* part;        // [S][T][E] partial logits
+    const float* bias;
+    uint16_t* h;               // rows a_{t,j}: parts [NPH][T * K][I]
+    int32_t* idx;              // [T][K]
+    float* w;                  // [T][K]
+    float* out;                // [T][H]
+    int S, T, H, E, K, I, e_begin, E_loc;
+};
+
+// ---- route -------------------------------------------------------------------
+
+template <typename XT> __device__ __forceinline__ double widen(XT v);
+template <> __device__ __forceinline__ double widen<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
+template <> __device__ __forceinline__ double widen<float>(float v) { return v; }
+
+// One workgroup: 16 experts x 16 tokens x one slice of H; its waves take 32-h
+// groups in turn.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and
+// k = l / 16; the four k of a group's step j are h = 8 (l / 16) + j.  The products
+// of bf16 (float32) inputs are exact in double, so only the additions round.
+// NPX > 0: the first expert column also writes the rows' parts for the gate/up product.
+template <typename XT, int NPX, bool F16>
+__global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __restrict__ x, const XT* __restrict__ w,
+                                                                  int T, int H, int E, double* __restrict__ part,
+                                                                  uint16_t* __restrict__ xp, int64_t xp_part) {
+    __shared__ double s_red[kRouteNW][4][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, kq = lane >> 4;
+    const int t = blockIdx.y * kRowTile + r, e = blockIdx.x * kRowTile + r;
+    const int groups = H / 32, step = gridDim.z * kRouteNW;
+    doublex4 acc = {0.0, 0.0, 0.0, 0.0};
+    for (int g = blockIdx.z * kRouteNW + wave; g < groups; g += step) {
+        const int h0 = g * 32 + kq * 8;
+        XT xv[8], wv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            xv[j] = t < T ? x[static_cast<int64_t>(t) * H + h0 + j] : XT(0);
+            wv[j] = e < E ? w[static_cast<int64_t>(h0 + j) * E + e] : XT(0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(widen<XT>(xv[j]), widen<XT>(wv[j]), acc, 0, 0, 0);
+        if constexpr (NPX > 0) {
+            if (blockIdx.x == 0 && t < T) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint16_t p[NPX];
+                    split_parts<NPX, F16>(static_cast<float>(widen<XT>(xv[j])), p);
+#pragma unroll
+                    for (int q = 0; q < NPX; ++q) xp[q * xp_part + static_cast<int64_t>(t) * H + h0 + j] = p[q];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) s_red[wave][v][lane] = acc[v];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+        const int v = threadIdx.x >> 6;
+        double s = 0.0;
+#pragma unroll
+        for (int q = 0; q < kRouteNW; ++q) s += s_red[q][v][lane];
+        // register v of lane l: row 4 v + l / 16, column l % 16
+        const int tt = blockIdx.y * kRowTile + 4 * v + kq;
+        if (tt < T && e < E) part[(static_cast<int64_t>(blockIdx.z) * T + tt) * E + e] = s;
+    }
+}
+
+// ---- selection ------------------------------------------------------------------
+
+// Maximum over the wave (DPP row shifts, then the four rows' results).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x111, 0xf, 0xf, false)));
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x112, 0xf, 0xf, false)));
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x114, 0xf, 0xf, false)));
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x118, 0xf, 0xf, false)));
+    return max(max(static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 15)),
+                   static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 31))),
+               max(static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 47)),
+                   static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 63))));
+}
+
+// One wave: token t's logits summed over the slices, its K best in order (larger
+// first, equal ones by index) and their weights, to LDS.  A lane holds experts
+// 64 g + lane.  A double is compared by its ordered bits, upper word first; the
+// lower word is looked at only where upper words are equal.
+template <int NE>
+__device__ __forceinline__ void select_token(const FewArgs& p, int t, int* s_idx, float* s_w, double* s_val) {
+    const int lane = threadIdx.x & (kWave - 1);
+    double val[NE];
+    uint32_t hi[NE], lo[NE];
+    uint32_t dead = 0u;
+#pragma unroll
+    for (int g = 0; g < NE; ++g) {
+        const int e = g * kWave + lane;
+        val[g] = 0.0;
+        if (e < p.E) {
+            for (int s = 0; s < p.S; ++s) val[g] += p.part[(static_cast<int64_t>(s) * p.T + t) * p.E + e];
+            if (p.bias != nullptr) val[g] += p.bias[e];
+            val[g] += 0.0;                             // -0 and +0 compare equal
+        }
+        uint64_t u = __builtin_bit_cast(uint64_t, val[g]);
+        u ^= (u >> 63) ? ~0ull : (1ull << 63);
+        hi[g] = e < p.E ? static_cast<uint32_t>(u >> 32) : 0u;
+        lo[g] = static_cast<uint32_t>(u);
+        dead |= e < p.E ? 0u : (1u << g);
+    }
+    for (int k = 0; k < p.K; ++k) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int g = 0; g < NE; ++g) m = max(m, hi[g]);
+        m = wave_max(m);
+        int many = 0;
+#pragma unroll
+        for (int g = 0; g < NE; ++g) many += __popcll(__ballot(hi[g] == m && !((dead >> g) & 1u)));
+        uint32_t m2 = 0u;
+        if (many > 1) {                                // uniform
+#pragma unroll
+            for (int g = 0; g < NE; ++g) m2 = max(m2, hi[g] == m && !((dead >> g) & 1u) ? lo[g] : 0u);
+            m2 = wave_max(m2);
+        }
+        int best = -1;
+#pragma unroll
+        for (int g = 0; g < NE; ++g) {
+            const uint64_t b = __ballot(hi[g] == m && !((dead >> g) & 1u) && (many == 1 || lo[g] == m2));
+            if (best < 0 && b != 0ull) best = g * kWave + __builtin_ctzll(b);
+        }
+#pragma unroll
+        for (int g = 0; g < NE; ++g)
+            if (g * kWave + lane == best) {
+                s_val[k] = val[g];
+                hi[g] = 0u;
+                dead |= 1u << g;
+            }
+        if (lane == 0) s_idx[t * p.K + k] = best;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const float ex = lane < p.K ? expf(static_cast<float>(s_val[lane] - s_val[0])) : 0.0f;
+    float sum = 0.0f;
+    for (int k = 0; k < p.K; ++k)
+        sum += __uint_as_float(__builtin_amdgcn_readlane(__builtin_bit_cast(int, ex), k));
+    if (lane < p.K) s_w[t * p.K + lane] = ex / sum;
+}
+
+// LDS tables of the routing, sized by the call (T K pairs, at most `amax` chosen
+// local experts).
+struct Tables {
+    int* idx;          // [T K] expert of (t, j)
+    float* w;          // [T K]
+    int* act;          // [amax] local index of the a-th chosen expert, ascending
+    int* pos;          // [E_loc] 0 or 1 + its place in act
+    int8_t* slot;      // [amax][T] slot of token t that chose expert a, or -1
+    int* count;        // number of chosen local experts
+};
+
+struct TableSizes {
+    size_t idx, w, act, pos, slot, count, total;
+};
+
+__host__ __device__ inline TableSizes table_sizes(int T, int K, int E_loc) {
+    const int pairs = T * K, amax = pairs < E_loc ? pairs : E_loc;
+    TableSizes z;
+    z.idx = 0;
+    z.w = z.idx + 4 * static_cast<size_t>(pairs);
+    z.act = z.w + 4 * static_cast<size_t>(pairs);
+    z.pos = z.act + 4 * static_cast<size_t>(amax);
+    z.count = z.pos + 4 * static_cast<size_t>(E_loc);
+    z.slot = z.count + 4;
+    z.total = (z.slot + static_cast<size_t>(amax) * T + 15) & ~size_t(15);
+    return z;
+}
+
+__device__ __forceinline__ Tables carve_tables(char* base, const FewArgs& p) {
+    const TableSizes z = table_sizes(p.T, p.K, p.E_loc);
+    Tables s;
+    s.idx = reinterpret_cast<int*>(base + z.idx);
+    s.w = reinterpret_cast<float*>(base + z.w);
+    s.act = reinterpret_cast<int*>(base + z.act);
+    s.pos = reinterpret_cast<int*>(base + z.pos);
+    s.count = reinterpret_cast<int*>(base + z.count);
+    s.slot = reinterpret_cast<int8_t*>(base + z.slot);
+    return s;
+}
+
+// From idx (complete, synchronised): the chosen local experts and who chose them.
+// Every thread of the workgroup takes part.
+__device__ __forceinline__ void build_tables(const Tables& s, const FewArgs& p) {
+    const int tid = threadIdx.x, n = blockDim.x, pairs = p.T * p.K;
+    const int amax = min(pairs, p.E_loc);
+    for (int i = tid; i < p.E_loc; i += n) s.pos[i] = 0;
+    for (int i = tid; i < amax * p.T; i += n) s.slot[i] = -1;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += n) {
+        const int e = s.idx[i] - p.e_begin;
+        if (e >= 0 && e < p.E_loc) s.pos[e] = 1;
+    }
+    __syncthreads();
+    if (tid < kWave) {
+        int run = 0;
+        for (int b = 0; b < p.E_loc; b += kWave) {
+            const int e = b + tid;
+            const bool on = e < p.E_loc && s.pos[e] != 0;
+            const uint64_t m = __ballot(on);
+            if (on) {
+                const int a = run + __popcll(m & ((1ull << tid) - 1ull));
+                s.act[a] = e;
+                s.pos[e] = 1 + a;
+            }
+            run += __popcll(m);
+        }
+        if (tid == 0) *s.count = run;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += n) {
+        const int e = s.idx[i] - p.e_begin;
+        if (e >= 0 && e < p.E_loc) {
+            const int t = i / p.K;
+            s.slot[(s.pos[e] - 1) * p.T + t] = static_cast<int8_t>(i - t * p.K);
+        }
+    }
+    __syncthreads();
+}
+
+// ---- gate and up ------------------------------------------------------------------
+
+// Steps wave, wave + kNW, ... of a gate/up unit.
+template <int NP, bool MX, int MT>
+struct GateUpCursor {
+    const uint8_t* b;          // this lane's gate bytes of the step
+    const uint8_t* sc;         // its scale bytes (MXFP8): gate, and `sc_up` further the up column's
+    int sc_up;
+    __amdgpu_buffer_rsrc_t rows;
+    uint32_t off[MT];          // byte offset of this lane's k group in part 0 of its row, or out of range
+    uint32_t part_bytes;
+    int left;                  // steps after this one
+
+    __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 2>& s) {
+        constexpr int half = MX ? 2048 : 1024;         // up columns: the other half of the pair
+        s.b[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
+        s.b[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + half));
+        if constexpr (MX) {
+            s.sc[0] = sc[0];
+            s.sc[1] = sc[sc_up];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+#pragma unroll
+                for (int l = 0; l < (MX ? 2 : 1); ++l)
+                    s.a[m][q][l] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off[m] + q * part_bytes + l * 16, 0, 0));
+        const int go = left > 0 ? 1 : 0;               // uniform
+        left -= go;
+        b += go * (kNW * kStepBytes);
+        if constexpr (MX) sc += go * (kNW * 2);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) off[m] += go * (kNW * (MX ? 128 : 64));
+    }
+};
+
+template <int NP, bool F16, bool MX, int MT, int NPH, bool F16H>
+__global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][2][4][kWave];
+    __shared__ double s_val[kNW][kWave];
+    const Tables tb = carve_tables(smem, p);
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    for (int t = wave; t < p.T; t += kNW) {
+        if (p.E <= 128) select_token<2>(p, t, tb.idx, tb.w, s_val[wave]);
+        else if (p.E <= 256) select_token<4>(p, t, tb.idx, tb.w, s_val[wave]);
+        else select_token<16>(p, t, tb.idx, tb.w, s_val[wave]);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = tid; i < p.T * p.K; i += kNW * 64) {
+            p.idx[i] = tb.idx[i];
+            p.w[i] = tb.w[i];
+        }
+    build_tables(tb, p);
+
+    const int nb = p.I / kRowTile;                     // units per expert
+    const int units = *tb.count * nb;
+    const int nk = p.H / (MX ? 64 : 32);               // steps of a unit
+    const __amdgpu_buffer_rsrc_t rows =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.a), 0, kBufferRange, kBufferFlags);
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int a = unit / nb, u = unit - a * nb;
+        const int e = __builtin_amdgcn_readfirstlane(tb.act[a]);
+        const int pair = u >> 1, c0 = (u & 1) * 16;
+        const int8_t* slot = tb.slot + a * p.T;
+
+        GateUpCursor<NP, MX, MT> cur;
+        const int64_t first = (static_cast<int64_t>(e) * (p.I >> 5) + pair) * nk + wave;
+        cur.b = p.gu + first * kStepBytes + step_lane_offset<MX>(0, c0);
+        if constexpr (MX) {
+            const int64_t col = static_cast<int64_t>(e) * 2 * p.I + pair * 64 + c0 + (lane & 15);
+            cur.sc = p.gu_scales + col * (p.H / 32) + wave * 2 + (lane >> 5);
+            cur.sc_up = p.H;                           // 32 columns further, H / 32 bytes each
+        }
+        cur.rows = rows;
+        cur.part_bytes = static_cast<uint32_t>(p.a_part * 2);
+        cur.left = (nk - wave + kNW - 1) / kNW - 1;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int t = m * kRowTile + (lane & 15);
+            const bool on = t < p.T && slot[t < p.T ? t : 0] >= 0;
+            cur.off[m] = on ? static_cast<uint32_t>(t * p.H + (wave * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2 : kOutOfRange;
+        }
+        Acc<NP, F16, MX, MT, 2> acc;
+        acc.clear();
+        stream_steps<4>(cur.left + 1, cur, acc);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) s_red[wave][m][c][v][lane] = acc.value(m, c, v);
+        __syncthreads();
+        // thread -> (row tile, register, lane): row 4 (lane / 16) + register, column lane % 16
+        if (tid < MT * 256) {
+            const int m = tid >> 8, v = (tid >> 6) & 3;
+            const int t = m * kRowTile + (lane >> 4) * 4 + v;
+            float g = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kNW; ++q) {
+                g += s_red[q][m][0][v][lane];
+                up += s_red[q][m][1][v][lane];
+            }
+            const int j = t < p.T ? slot[t] : -1;
+            if (j >= 0) {
+                const int row = t * p.K + j;
+                const float act = g / (1.0f + expf(-g)) * up * tb.w[row];
+                uint16_t part[NPH];
+                split_parts<NPH, F16H>(act, part);
+                const int64_t pairs = static_cast<int64_t>(p.T) * p.K;
+#pragma unroll
+                for (int q = 0; q < NPH; ++q)
+                    p.h[(q * pairs + row) * p.I + u * kRowTile + (lane & 15)] = part[q];
+            }
+        }
+        __syncthreads();                               // s_red is free
+    }
+}
+
+// ---- down and combine -----------------------------------------------------------------
+
+// Steps wave, wave + kNW, ... of the reduction over every chosen expert's I.
+template <int NP, bool MX, int MT>
+struct DownCursor {
+    const FewArgs* p;
+    const Tables* tb;
+    const uint8_t* b;          // this lane's bytes of expert 0's step 0
+    const uint8_t* sc;         // this lane's scale byte of expert 0's step 0
+    int64_t b_expert, sc_expert;   // bytes per expert
+    __amdgpu_buffer_rsrc_t rows;
+    uint32_t part_bytes;
+    int nk, count;             // steps per expert, chosen experts
+    int a, ks;                 // current step
+
+    __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 1>& s) {
+        const int lane = threadIdx.x & (kWave - 1);
+        const int e = __builtin_amdgcn_readfirstlane(tb->act[a]);
+        s.b[0] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(b + e * b_expert + static_cast<int64_t>(ks) * kStepBytes));
+        if constexpr (MX) s.sc[0] = sc[e * sc_expert + ks * 2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int t = m * kRowTile + (lane & 15);
+            const int j = t < p->T ? tb->slot[a * p->T + t] : -1;
+            const uint32_t off =
+                j >= 0 ? (static_cast<uint32_t>((t * p->K + j) * p->I) + (ks * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2
+                       : kOutOfRange;
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+#pragma unroll
+                for (int l = 0; l < (MX ? 2 : 1); ++l)
+                    s.a[m][q][l] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off + q * part_bytes + l * 16, 0, 0));
+        }
+        // advance, staying on this wave's last step at the end
+        int na = a, nks = ks + kNW;
+        while (nks >= nk) {
+            nks -= nk;
+            ++na;
+        }
+        if (na < count) {
+            a = na;
+            ks = nks;
+        }
+    }
+};
+
+template <int NP, bool F16, bool MX, int MT>
+__global__ __launch_bounds__(kNW * 64, 2) void few_down_kernel(FewArgs p) {
+    constexpr int D = MX ? 2 : 4;                      // an MXFP8 step is 64 k of up to 3 parts
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][4][kWave];
+    const Tables tb = carve_tables(smem, p);
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    for (int i = tid; i < p.T * p.K; i += kNW * 64) tb.idx[i] = p.idx[i];
+    __syncthreads();
+    build_tables(tb, p);
+
+    const int unit = blockIdx.x;                       // 16 output columns
+    const int n64 = unit >> 2, half = (unit >> 1) & 1, c0 = (unit & 1) * 16;
+    DownCursor<NP, MX, MT> cur;
+    cur.p = &p;
+    cur.tb = &tb;
+    cur.nk = p.I / (MX ? 64 : 32);
+    cur.count = __builtin_amdgcn_readfirstlane(*tb.count);
+    const int total = cur.count * cur.nk;
+    cur.b_expert = static_cast<int64_t>(p.H >> 6) * cur.nk * kStepBytes;
+    cur.b = p.dn + static_cast<int64_t>(n64) * cur.nk * kStepBytes + step_lane_offset<MX>(half, c0);
+    if constexpr (MX) {
+        cur.sc_expert = static_cast<int64_t>(p.H) * (p.I / 32);
+        cur.sc = p.dn_scales + static_cast<int64_t>(unit * kRowTile + (lane & 15)) * (p.I / 32) + (lane >> 5);
+    }
+    cur.rows = __builtin_amdgcn_make_buffer_rsrc(p.h, 0, kBufferRange, kBufferFlags);
+    cur.part_bytes = static_cast<uint32_t>(static_cast<int64_t>(p.T) * p.K * p.I * 2);
+    cur.a = wave / cur.nk;
+    cur.ks = wave - cur.a * cur.nk;
+    Acc<NP, F16, MX, MT, 1> acc;
+    acc.clear();
+    stream_steps<D>(total > wave ? (total - wave + kNW - 1) / kNW : 0, cur, acc);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s_red[wave][m][v][lane] = acc.value(m, 0, v);
+    __syncthreads();
+    if (tid < MT * 256) {
+        const int m = tid >> 8, v = (tid >> 6) & 3;
+        const int t = m * kRowTile + (lane >> 4) * 4 + v;
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kNW; ++q) s += s_red[q][m][v][lane];
+        if (t < p.T) p.out[static_cast<int64_t>(t) * p.H + unit * kRowTile + (lane & 15)] = s;
+    }
+}
+
+// ---- host -----------------------------------------------------------------------------
+
+// Slices of H in the route step: enough workgroups for the few (16 expert x 16
+// token) tiles, few enough partials for every gate/up workgroup to add.
+int route_slices(int T, int H) {
+    int S = T <= 2 ? kMaxSlices : 32 / T;
+    if (S < 2) S = 2;
+    const int most = (H / 32 + kRouteNW - 1) / kRouteNW;
+    return S < most ? S : most;
+}
+
+// parts of the gate/up rows that the route step writes (0: the rows are read from x)
+int x_parts(int x_dtype, bool mx) { return x_dtype == MOE_BF16 ? 0 : (mx ? 3 : 2); }
+int h_parts(bool mx) { return mx ? 3 : 2; }
+
+template <int MT>
+int launch_products(const FewArgs& p, int x_dtype, bool mx, hipStream_t st) {
+    const int64_t experts = p.T * p.K < p.E_loc ? p.T * p.K : p.E_loc;
+    const int64_t most = experts * (p.I / kRowTile);
+    const dim3 g(static_cast<unsigned>(most < 512 ? most : 512)), block(kNW * 64), d(p.H / kRowTile);
+    const size_t lds = table_sizes(p.T, p.K, p.E_loc).total;
+    if (mx) {
+        if (x_dtype == MOE_BF16)
+            hipLaunchKernelGGL((few_gate_up_kernel<1, false, true, MT, 3, false>), g, block, lds, st, p);
+        else
+            hipLaunchKernelGGL((few_gate_up_kernel<3, false, true, MT, 3, false>), g, block, lds, st, p);
+        MOE_CHECK_LAUNCH();
+        hipLaunchKernelGGL((few_down_kernel<3, false, true, MT>), d, block, lds, st, p);
+    } else {
+        if (x_dtype == MOE_BF16)
+            hipLaunchKernelGGL((few_gate_up_kernel<1, false, false, MT, 2, true>), g, block, lds, st, p);
+        else
+            hipLaunchKernelGGL((few_gate_up_kernel<2, true, false, MT, 2, true>), g, block, lds, st, p);
+        MOE_CHECK_LAUNCH();
+        hipLaunchKernelGGL((few_down_kernel<2, true, false, MT>), d, block, lds, st, p);
+    }
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+}  // namespace
+
+bool few_tokens_fits(const moe_shape& s) {
+    const int64_t rows = static_cast<int64_t>(s.T) * s.K * s.I * 2 * 3, x = static_cast<int64_t>(s.T) * s.H * 2 * 3;
+    const size_t lds = table_sizes(s.T, s.K, s.e_end - s.e_begin).total;
+    return s.T <= MOE_FEW_TOKENS_MAX && rows <= kBufferRange && x <= kBufferRange && lds <= 64 * 1024;
+}
+
+size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w) {
+    char* p = static_cast<char*>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) -> char* {
+        char* r = p ? p + off : nullptr;
+        off += up256(bytes);
+        return r;
+    };
+    const size_t pairs = static_cast<size_t>(s.T) * s.K;
+    FewWs z;
+    z.part = reinterpret_cast<double*>(take(static_cast<size_t>(kMaxSlices) * s.T * s.E * 8));
+    z.idx = reinterpret_cast<int32_t*>(take(pairs * 4));
+    z.w = reinterpret_cast<float*>(take(pairs * 4));
+    z.x = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * s.T * s.H * 2));
+    z.h = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * pairs * s.I * 2));
+    if (w != nullptr) *w = z;
+    return off;
+}
+
+int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void* w_router, const float* bias,
+                      const void* packed, bool mx, float* out, int32_t* idx, float* tw, void* ws, hipStream_t st) {
+    FewWs z;
+    few_tokens_workspace(s, ws, &z);
+    FewArgs p{};
+    p.T = s.T;
+    p.H = s.H;
+    p.E = s.E;
+    p.K = s.K;
+    p.I = s.I;
+    p.e_begin = s.e_begin;
+    p.E_loc = s.e_end - s.e_begin;
+    p.S = route_slices(s.T, s.H);
+    p.part = z.part;
+    p.bias = bias;
+    p.h = z.h;
+    p.idx = idx ? idx : z.idx;
+    p.w = tw ? tw : z.w;
+    p.out = out;
+    p.a = x_dtype == MOE_BF16 ? static_cast<const uint16_t*>(x) : z.x;
+    p.a_part = static_cast<int64_t>(s.T) * s.H;
+    const uint8_t* b = static_cast<const uint8_t*>(packed);
+    p.gu = b;
+    if (mx) {
+        p.dn = p.gu + mx_packed_gate_up_code_bytes(s);
+        p.gu_scales = p.dn + mx_packed_down_code_bytes(s);
+        p.dn_scales = p.gu_scales + mx_packed_gate_up_code_bytes(s) / 32;
+    } else {
+        p.dn = p.gu + packed_gate_up_elems(s) * 2;
+    }
+    const dim3 g((s.E + kRowTile - 1) / kRowTile, (s.T + kRowTile - 1) / kRowTile, p.S), block(kRouteNW * 64);
+    if (x_dtype == MOE_BF16)
+        hipLaunchKernelGGL((few_route_kernel<uint16_t, 0, false>), g, block, 0, st, static_cast<const uint16_t*>(x),
+                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+    else if (mx)
+        hipLaunchKernelGGL((few_route_kernel<float, 3, false>), g, block, 0, st, static_cast<const float*>(x),
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+    else
+        hipLaunchKernelGGL((few_route_kernel<float, 2, true>), g, block, 0, st, static_cast<const float*>(x),
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+    MOE_CHECK_LAUNCH();
+    return s.T <= kRowTile ? launch_products<1>(p, x_dtype, mx, st) : launch_products<2>(p, x_dtype, mx, st);
+}
+
+}  // namespace moe

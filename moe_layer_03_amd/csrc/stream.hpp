@@ -1,0 +1,152 @@
+// Weight-streaming products of a few rows: the building blocks shared by the
+// few-token layer and the dense product.
+//
+// A wave multiplies up to MT * 16 rows by CT tiles of 16 columns with
+// v_mfma_f32_16x16x32: every weight element passes through the wave's
+// registers exactly once, so the product runs at the rate the weights arrive.
+// Weights come in the packed layouts of the grouped GEMMs.  Both keep a
+// 64-column pair's reduction contiguous, 4 KiB per step:
+//   16-bit:  a step is 32 k, [2 k blocks][2 column halves][64 lanes][16 bytes],
+//   MXFP8:   a step is 64 k, [2 column halves][2 scale blocks][64 lanes][16 bytes],
+// and in both a lane slot is (column c of 32) + 32 * (k half of the block).  The
+// 16 columns c0 .. c0 + 15 of a half are four 256-byte pieces of a step, one per
+// k group of a lane: lane l holds column l % 16 and k group l / 16 (8 k of a
+// 16-bit step, 16 k of an MXFP8 step, as two MFMA operands of 8).
+//
+// Rows are held as NP 16-bit parts whose sum is the row's value:
+//   1 part: the value itself;
+//   2 parts (fp16): v = p0 + 2^-11 p1, |error| <= 2^-22 |v| for 2^-14 <= |v| <=
+//     65504 (p1 is scaled up so that it stays a normal fp16 number); the parts
+//     have their own accumulators, joined at the end;
+//   3 parts (bf16): v = p0 + p1 + p2, exact to 2^-24 |v|; one accumulator.
+// The MFMAs of the extra parts are free here: the weights' arrival bounds the
+// product, and a row held to 22 bits or more keeps the float32 output's digits.
+#pragma once
+
+#include "gemm_common.hpp"
+
+namespace moe {
+namespace {
+
+constexpr float kLoScale = 2048.0f;                    // 2^11, the second fp16 part's scale
+constexpr int kStepBytes = 4096;                       // packed weights of a 64-column pair per step
+constexpr int kRowTile = 16;                           // rows (and columns) of an MFMA tile
+
+__device__ __forceinline__ floatx4 mfma16(bool f16, const u32x4& a, const u32x4& b, floatx4 c) {
+    if (f16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8_t, a),
+                                                      __builtin_bit_cast(halfx8_t, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+}
+
+// Eight E4M3 codes (two words) times 2^(scale byte - 127), as bf16: exact, a code has 4 significant bits.
+__device__ __forceinline__ u32x4 mx_to_bf16(uint32_t w0, uint32_t w1, uint32_t scale_byte) {
+    const float s = __uint_as_float(scale_byte << 23);
+    u32x4 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true));
+    return r;
+}
+
+// Parts of v (see above); fp16 saturates at 65504.
+template <int NP, bool F16>
+__device__ __forceinline__ void split_parts(float v, uint16_t (&p)[NP]) {
+    if constexpr (F16) {
+        p[0] = f32_to_f16_sat(v);
+        if constexpr (NP == 2) {
+            const float c = fminf(fmaxf(v, -65504.0f), 65504.0f);
+            p[1] = f32_to_f16_sat((c - f16_to_f32(p[0])) * kLoScale);
+        }
+    } else {
+        float rest = v;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            p[i] = f32_to_bf16(rest);
+            rest -= bf16_to_f32(p[i]);                 // exact
+        }
+    }
+}
+
+// One step's operands of a wave: CT column tiles, MT row tiles of NP parts.
+template <int NP, bool MX, int MT, int CT>
+struct StepRegs {
+    static constexpr int AL = MX ? 2 : 1;              // MFMA operands of 8 k per lane and step
+    u32x4 b[CT];
+    uint32_t sc[MX ? CT : 1];
+    u32x4 a[MT][NP][AL];
+};
+
+template <int NP, bool F16, bool MX, int MT, int CT>
+struct Acc {
+    static constexpr int NA = (F16 && NP == 2) ? 2 : 1;
+    floatx4 v[NA][MT][CT];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) v[n][m][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void add(const StepRegs<NP, MX, MT, CT>& s) {
+#pragma unroll
+        for (int q = 0; q < StepRegs<NP, MX, MT, CT>::AL; ++q)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                u32x4 b;
+                if constexpr (MX) b = mx_to_bf16(s.b[c][2 * q], s.b[c][2 * q + 1], s.sc[c]);
+                else b = s.b[c];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const int n = NA == 2 ? p : 0;
+                        v[n][m][c] = mfma16(F16, s.a[m][p][q], b, v[n][m][c]);
+                    }
+            }
+    }
+    __device__ __forceinline__ float value(int m, int c, int i) const {
+        if constexpr (NA == 2) return v[0][m][c][i] + v[1][m][c][i] * (1.0f / kLoScale);
+        else return v[0][m][c][i];
+    }
+};
+
+// Byte offset of this lane's 16 bytes within a 4 KiB step: column half `half`,
+// columns c0 .. c0 + 15 of it (c0 0 or 16).
+template <bool MX>
+__device__ __forceinline__ int step_lane_offset(int half, int c0) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int col = lane & 15, kq = lane >> 4;
+    const int slot = ((kq & 1) * 32 + c0 + col) * 16;
+    return MX ? half * 2048 + (kq >> 1) * 1024 + slot : (kq >> 1) * 2048 + half * 1024 + slot;
+}
+
+// Adds n steps to acc.  cur.load(regs) issues the loads of the next step (the
+// last step again once there are no more) into a register ring D steps deep;
+// whole turns of the ring have no branch inside, so the wait before a step
+// leaves the younger D - 1 steps' loads in flight.
+template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
+__device__ __forceinline__ void stream_steps(int n, Cursor& cur, Acc<NP, F16, MX, MT, CT>& acc) {
+    if (n <= 0) return;                                // uniform over the wave
+    StepRegs<NP, MX, MT, CT> ring[D];
+#pragma unroll
+    for (int j = 0; j < D; ++j) cur.load(ring[j]);
+    int i = 0;
+    for (; i + D <= n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            acc.add(ring[j]);
+            cur.load(ring[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (i + j < n) acc.add(ring[j]);               // uniform
+}
+
+}  // namespace
+}  // namespace moe
