@@ -59,6 +59,11 @@ extern "C" {
 #define MOE_GEMM_DOWN    1   /* A = SwiGLU activations [*, I], B = down weights of each expert    */
 #define MOE_EPI_NONE     0   /* C = A.B (gate/up: columns 0..I-1 gate, I..2I-1 up)                 */
 #define MOE_EPI_SWIGLU   1   /* C = silu(A.Wg) * (A.Wu), silu(z) = z / (1 + exp(-z)); gate/up only */
+/* Further epilogues of moe_dense_gemm() (not of the grouped GEMMs). */
+#define MOE_EPI_SILU      2  /* z / (1 + exp(-z))                                                  */
+#define MOE_EPI_GELU      3  /* z (1 + erf(z / sqrt(2))) / 2                                       */
+#define MOE_EPI_GELU_TANH 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2                  */
+#define MOE_EPI_RELU      5  /* max(z, 0)                                                          */
 
 /*
  * Problem shape of one rank.
@@ -398,6 +403,59 @@ size_t moe_layer_few_tokens_workspace_bytes_mxfp8(const moe_shape* s);
 int moe_layer_few_tokens_mxfp8(const moe_shape* s, const void* x, int x_dtype, const void* w_router, int w_dtype,
                                const float* bias, const void* packed, float* out, int32_t* topk_idx, float* topk_w,
                                void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dense products around the experts (a shared expert, a dense MLP layer, an
+ * output projection), from one token to a prefill batch, with the epilogue
+ * fused:
+ *   C = act(A W + bias) + R                          (gated == 0)
+ *   C = silu(A Wg + bias_g) * (A Wu + bias_u) + R    (gated == 1)
+ * M rows, N output columns, K the reduction; W (Wg, Wu) [K, N].  Any sizes with
+ * 0 <= M <= MOE_DENSE_MAX_ROWS (M == 0: a no-op) and
+ * 1 <= N, K <= MOE_DENSE_MAX_COLS, else MOE_ERR_UNSUPPORTED.
+ */
+#define MOE_DENSE_MAX_ROWS (1 << 21)
+#define MOE_DENSE_MAX_COLS (1 << 18)
+typedef struct moe_dense_shape {
+    int32_t M, N, K;
+    int32_t gated;       /* 1: gate and up weights, MOE_EPI_SWIGLU; 0: one weight, any other epilogue */
+} moe_dense_shape;
+
+/* Bytes of the packed weights of (N, K, gated); M does not matter (host-only). */
+size_t moe_packed_dense_bytes(const moe_dense_shape* s);
+
+/*
+ * moe_pack_dense -- static conversion of w [K, N] (gated: the gate weight, with
+ * w_up [K, N]; else w_up is NULL), contiguous, MOE_BF16, MOE_F16 or MOE_F32, into
+ * the layout moe_dense_gemm() reads.  16-bit weights keep their type, float32
+ * weights are rounded to fp16 (saturating at 65504).  packed:
+ * moe_packed_dense_bytes(s) bytes, 16-byte aligned, written; opaque.  w needs
+ * its element's alignment only.
+ */
+int moe_pack_dense(const moe_dense_shape* s, const void* w, const void* w_up, int dtype, void* packed, void* stream);
+
+/*
+ * moe_dense_gemm -- the product on packed weights.
+ *   a: rows of K values, lda >= K elements apart; a_dtype MOE_BF16 for weights
+ *       packed from bf16, MOE_F16 for weights packed from fp16 or float32.
+ *   epilogue: MOE_EPI_SWIGLU exactly if s->gated, else MOE_EPI_NONE or one of
+ *       MOE_EPI_SILU .. MOE_EPI_RELU.
+ *   bias: float32 [N] (gated: [2][N], gate then up) or NULL.
+ *   residual: rows of N values, ldr >= N apart, r_dtype MOE_F32, MOE_BF16 or
+ *       MOE_F16, or NULL (r_dtype and ldr then do not matter).  It may be c
+ *       itself (same type and ldc: C += ...); any other overlap of c with an
+ *       input is undefined.
+ *   c (output): rows of N values, ldc >= N apart, c_dtype as r_dtype; elements
+ *       between the rows are not touched.
+ *   Products accumulate in float32, bias, activation and residual are applied
+ *   in float32, and the result is rounded once (16-bit: to nearest even; fp16
+ *   saturates at 65504).
+ *   a, residual and c need their element's alignment only; rows of A that all
+ *   start on 16 bytes (with K a multiple of 8) take the fast paths.
+ */
+int moe_dense_gemm(const moe_dense_shape* s, const void* a, int a_dtype, int64_t lda, const void* packed, int epilogue,
+                   const float* bias, const void* residual, int r_dtype, int64_t ldr, void* c, int c_dtype,
+                   int64_t ldc, void* stream);
 
 /*
  * Measurement helpers (not part of the layer).  moe_probe_mfma_bf16 launches

@@ -35,6 +35,10 @@ MOE_GEMM_GATE_UP = 0
 MOE_GEMM_DOWN = 1
 MOE_EPI_NONE = 0
 MOE_EPI_SWIGLU = 1
+MOE_EPI_SILU = 2
+MOE_EPI_GELU = 3
+MOE_EPI_GELU_TANH = 4
+MOE_EPI_RELU = 5
 
 EXPORTED = [
     "moe_dispatch_workspace_bytes", "moe_route_workspace_bytes", "moe_route_screen_layout",
@@ -47,6 +51,7 @@ EXPORTED = [
     "moe_layer_workspace_bytes_mxfp8", "moe_layer_mxfp8",
     "moe_layer_few_tokens_workspace_bytes", "moe_layer_few_tokens",
     "moe_layer_few_tokens_workspace_bytes_mxfp8", "moe_layer_few_tokens_mxfp8",
+    "moe_packed_dense_bytes", "moe_pack_dense", "moe_dense_gemm",
 ]
 
 MOE_FEW_TOKENS_MAX = 32
@@ -96,9 +101,26 @@ class Shape:
         return Shape(wl.T, wl.H, wl.E, wl.K, wl.I, wl.e_begin, wl.e_end)
 
 
+class _CDenseShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "gated")]
+
+
+@dataclasses.dataclass(frozen=True)
+class DenseShape:
+    """C [M, N] = A [M, K] times W [K, N]; gated: a gate and an up weight (SwiGLU)."""
+    M: int
+    N: int
+    K: int
+    gated: bool = False
+
+    def c(self) -> _CDenseShape:
+        return _CDenseShape(self.M, self.N, self.K, int(self.gated))
+
+
 _lib = None
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(_CShape)
+_D = ctypes.POINTER(_CDenseShape)
 
 
 def lib_path() -> str:
@@ -144,6 +166,10 @@ def load() -> ctypes.CDLL:
         "moe_layer_few_tokens": (i32, [_S, _P, i32, _P, i32, _P, _P, _P, _P, _P, _P, sz, _P]),
         "moe_layer_few_tokens_workspace_bytes_mxfp8": (sz, [_S]),
         "moe_layer_few_tokens_mxfp8": (i32, [_S, _P, i32, _P, i32, _P, _P, _P, _P, _P, _P, sz, _P]),
+        "moe_packed_dense_bytes": (sz, [_D]),
+        "moe_pack_dense": (i32, [_D, _P, _P, i32, _P, _P]),
+        "moe_dense_gemm": (i32, [_D, _P, i32, ctypes.c_int64, _P, i32, _P, _P, i32, ctypes.c_int64, _P, i32,
+                                 ctypes.c_int64, _P]),
         "moe_probe_mfma_bf16_flops": (ctypes.c_int64, [i32, i32]),
         "moe_probe_mfma_bf16": (i32, [i32, i32, _P, _P]),
     }
@@ -561,3 +587,65 @@ def moe_layer_few_tokens_mxfp8(s: Shape, x: torch.Tensor, w_router: torch.Tensor
                                stream=None) -> torch.Tensor:
     """The layer share for a few tokens with MXFP8 weights (packed from moe_pack_weights_mxfp8)."""
     return _layer_few_tokens(True, s, x, w_router, packed, bias, out, ws, topk_idx, topk_w, stream)
+
+
+# ---------------------------------------------------------------------------
+# dense products with a fused epilogue
+# ---------------------------------------------------------------------------
+
+def moe_packed_dense_bytes(d: DenseShape) -> int:
+    return int(load().moe_packed_dense_bytes(ctypes.byref(d.c())))
+
+
+def moe_pack_dense(d: DenseShape, w: torch.Tensor, w_up: Optional[torch.Tensor] = None,
+                   packed: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Pack w [K, N] (gated: the gate weight, with w_up [K, N]), bf16, fp16 or fp32; M does not matter."""
+    need = moe_packed_dense_bytes(d)
+    if packed is None:
+        packed = _empty(max(need, 16), torch.uint8, w.device)
+    if packed.dtype != torch.uint8 or packed.numel() < need:
+        raise ValueError(f"packed must be a uint8 buffer of at least {need} bytes")
+    n = d.N * d.K
+    st = load().moe_pack_dense(ctypes.byref(d.c()), _ptr(w, None, n, "w"), _ptr(w_up, w.dtype, n, "w_up"), _dt(w),
+                               _ptr(packed, torch.uint8, None, "packed"), _stream(stream))
+    _check("moe_pack_dense", st)
+    return packed
+
+
+def _rows(t: Optional[torch.Tensor], m: int, n: int, name: str):
+    """(pointer, row stride) of an [m, n] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if tuple(t.shape) != (m, n):
+        raise ValueError(f"{name} must be [{m}, {n}], got {list(t.shape)}")
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if m > 1 else n
+    if ld < n:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr() or None, ld
+
+
+def moe_dense_gemm(d: DenseShape, a: torch.Tensor, packed: torch.Tensor, epilogue: int = MOE_EPI_NONE, *,
+                   bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   c: Optional[torch.Tensor] = None, c_dtype: Optional[torch.dtype] = None,
+                   stream=None) -> torch.Tensor:
+    """act(a @ W + bias) + residual on moe_pack_dense weights (gated: MOE_EPI_SWIGLU, bias [2, N]).
+
+    a [M, K], residual and c [M, N] may have any row stride; c may be residual.  c_dtype defaults to a's."""
+    need = moe_packed_dense_bytes(d)
+    if packed.numel() < need:
+        raise ValueError(f"packed must hold {need} bytes, got {packed.numel()}")
+    if c is None:
+        c = _empty((d.M, d.N), c_dtype or a.dtype, a.device)
+    pa, lda = _rows(a, d.M, d.K, "a")
+    pr, ldr = _rows(residual, d.M, d.N, "residual")
+    pc, ldc = _rows(c, d.M, d.N, "c")
+    st = load().moe_dense_gemm(ctypes.byref(d.c()), pa, _dt(a), lda, _ptr(packed, torch.uint8, None, "packed"), epilogue,
+                               _ptr(bias, torch.float32, d.N * (2 if d.gated else 1), "bias"), pr,
+                               _dt(residual) if residual is not None else MOE_F32, ldr, pc, _dt(c), ldc,
+                               _stream(stream))
+    _check("moe_dense_gemm", st)
+    return c

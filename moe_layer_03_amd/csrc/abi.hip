@@ -202,6 +202,14 @@ int layer_few_tokens(const moe_shape* s, const void* x, int x_dtype, const void*
                              static_cast<hipStream_t>(stream));
 }
 
+// Dense products: the grid's limits are 2^31 - 1 column pairs and 65535 x 64 rows.
+int check_dense_shape(const moe_dense_shape* s) {
+    if (s == nullptr || s->M < 0 || s->N < 1 || s->K < 1) return MOE_ERR_INVALID_ARG;
+    if (s->gated != 0 && s->gated != 1) return MOE_ERR_INVALID_ARG;
+    if (s->M > MOE_DENSE_MAX_ROWS || s->N > MOE_DENSE_MAX_COLS || s->K > MOE_DENSE_MAX_COLS) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
 }  // namespace
 
 void set_last_hip_error(hipError_t e) { g_last_hip_error = static_cast<int32_t>(e); }
@@ -516,6 +524,39 @@ int moe_layer_few_tokens_mxfp8(const moe_shape* s, const void* x, int x_dtype, c
                                void* ws, size_t ws_bytes, void* stream) {
     return layer_few_tokens(s, x, x_dtype, w_router, w_dtype, bias, packed, true, out, topk_idx, topk_w, ws, ws_bytes,
                             stream);
+}
+
+size_t moe_packed_dense_bytes(const moe_dense_shape* s) {
+    if (check_dense_shape(s) != MOE_OK) return 0;
+    return dense_packed_bytes(*s);
+}
+
+int moe_pack_dense(const moe_dense_shape* s, const void* w, const void* w_up, int dtype, void* packed, void* stream) {
+    MOE_TRY(check_dense_shape(s));
+    if (!out_dtype_ok(dtype)) return MOE_ERR_UNSUPPORTED;
+    const size_t align = dtype == MOE_F32 ? 4 : 2;
+    if (w == nullptr || !aligned(w, align) || !ok16(packed)) return MOE_ERR_INVALID_ARG;
+    if (s->gated ? (w_up == nullptr || !aligned(w_up, align)) : w_up != nullptr) return MOE_ERR_INVALID_ARG;
+    return launch_pack_dense(*s, w, w_up, dtype, static_cast<uint16_t*>(packed), static_cast<hipStream_t>(stream));
+}
+
+int moe_dense_gemm(const moe_dense_shape* s, const void* a, int a_dtype, int64_t lda, const void* packed, int epilogue,
+                   const float* bias, const void* residual, int r_dtype, int64_t ldr, void* c, int c_dtype,
+                   int64_t ldc, void* stream) {
+    MOE_TRY(check_dense_shape(s));
+    if (epilogue < MOE_EPI_NONE || epilogue > MOE_EPI_RELU) return MOE_ERR_INVALID_ARG;
+    if ((epilogue == MOE_EPI_SWIGLU) != (s->gated == 1)) return MOE_ERR_INVALID_ARG;
+    if (a_dtype != MOE_BF16 && a_dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+    if (!out_dtype_ok(c_dtype) || (residual != nullptr && !out_dtype_ok(r_dtype))) return MOE_ERR_UNSUPPORTED;
+    if (lda < s->K || ldc < s->N || (residual != nullptr && ldr < s->N)) return MOE_ERR_INVALID_ARG;
+    if (s->M == 0) return MOE_OK;   // no rows; empty tensors may have null pointers
+    if (a == nullptr || !aligned(a, 2) || !ok16(packed) || !opt4(bias)) return MOE_ERR_INVALID_ARG;
+    if (c == nullptr || !aligned(c, c_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    if (residual != nullptr && !aligned(residual, r_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    if (residual == c && (r_dtype != c_dtype || ldr != ldc)) return MOE_ERR_INVALID_ARG;
+    return launch_dense_gemm(*s, static_cast<const uint16_t*>(a), a_dtype, lda, static_cast<const uint16_t*>(packed),
+                             epilogue, bias, residual, r_dtype, ldr, c, c_dtype, ldc,
+                             static_cast<hipStream_t>(stream));
 }
 
 const char* moe_status_string(int status) {

@@ -178,6 +178,14 @@ int launch_mx_grouped_gemm(const moe_shape& s, const uint8_t* a, const uint8_t* 
                            const int32_t* offsets, const uint8_t* packed, int which, int epilogue, void* c,
                            int c_dtype, uint8_t* c_scales, hipStream_t st);
 
+// Dense products with a fused epilogue (dense.hip)
+size_t dense_packed_bytes(const moe_dense_shape& s);
+int launch_pack_dense(const moe_dense_shape& s, const void* w, const void* w_up, int dtype, uint16_t* packed,
+                      hipStream_t st);
+int launch_dense_gemm(const moe_dense_shape& s, const uint16_t* a, int a_dtype, int64_t lda, const uint16_t* packed,
+                      int epilogue, const float* bias, const void* r, int r_dtype, int64_t ldr, void* c, int c_dtype,
+                      int64_t ldc, hipStream_t st);
+
 // The layer for a few tokens (few.hip)
 struct FewWs {
     double* part;      // partial logits
