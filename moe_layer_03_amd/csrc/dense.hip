@@ -20,6 +20,7 @@ struct DenseArgs {
     int64_t lda, ldr, ldc;
     int M, N, K, Kp;
     int gated, act, r_dtype, c_dtype;
+    int r_vec, c_vec;          // rows of R (C) start on four elements: four columns move at once
 };
 
 // ---- epilogue ------------------------------------------------------------------
@@ -60,6 +61,55 @@ __device__ __forceinline__ void finish(const DenseArgs& p, int row, int col, flo
     }
     if (p.r != nullptr) v += load_as(p.r, row * p.ldr + col, p.r_dtype);
     store_as(p.c, row * p.ldc + col, p.c_dtype, v);
+}
+
+// Four columns col .. col + 3 of a row at once (bias already loaded: b0 the
+// gate's or the only one, b1 the up's).
+__device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, floatx4 v, const floatx4& u,
+                                        const floatx4& b0, const floatx4& b1) {
+    if (row >= p.M || col >= p.N) return;
+    v += b0;
+    if (p.gated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * (u[i] + b1[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], p.act);
+    }
+    const bool whole = col + 4 <= p.N;
+    if (p.r != nullptr) {
+        const int64_t at = row * p.ldr + col;
+        if (whole && p.r_vec) {
+            if (p.r_dtype == MOE_F32) {
+                v += *reinterpret_cast<const floatx4*>(static_cast<const float*>(p.r) + at);
+            } else {
+                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.r) + at);
+                const uint16_t h[4] = {static_cast<uint16_t>(r.x), static_cast<uint16_t>(r.x >> 16),
+                                       static_cast<uint16_t>(r.y), static_cast<uint16_t>(r.y >> 16)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += p.r_dtype == MOE_BF16 ? bf16_to_f32(h[i]) : f16_to_f32(h[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < p.N) v[i] += load_as(p.r, at + i, p.r_dtype);
+        }
+    }
+    const int64_t at = row * p.ldc + col;
+    if (whole && p.c_vec) {
+        if (p.c_dtype == MOE_F32)
+            *reinterpret_cast<floatx4*>(static_cast<float*>(p.c) + at) = v;
+        else if (p.c_dtype == MOE_BF16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
+                make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < p.N) store_as(p.c, at + i, p.c_dtype, v[i]);
+    }
 }
 
 // ---- any alignment -----------------------------------------------------------------
@@ -207,11 +257,22 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
 }
 
 // ---- many rows: LDS tiles --------------------------------------------------------------
-// A workgroup of 8 waves owns um <= 256 rows x 256 packed columns; a wave owns one
-// of two row halves (up to 128 rows) x one 64-column pair: up to 4 x 2 tiles of
-// v_mfma_f32_32x32x16.  Both operands reach LDS by direct copies into a ring of
-// NB = 4 stages of 32 k, read one k-step of 16 ahead of the MFMAs; waits are
-// explicit and the once-per-stage barrier sits between a stage's two k-steps.
+// A workgroup of 8 waves owns MW * NA * 32 rows x (8 / MW) 64-column pairs; a wave
+// owns NA * 32 rows x one pair, NA x 2 tiles of v_mfma_f32_32x32x16.  Both
+// operands reach LDS by direct copies into a ring of kTileNB stages of 32 k.
+//
+// The two waves of a SIMD (w and w + 4) alternate: while one runs a stage's MFMAs
+// from registers, the other reads its next stage's fragments from LDS and issues
+// copies; a barrier ends each phase and the roles swap.  So the matrix unit
+// always has a wave whose operands are ready, and one register set of fragments
+// suffices (128 accumulators + 48 fragment registers at NA = 4).
+//   phase 2s:     waves 0-3 read stage s, waves 4-7 multiply stage s - 1
+//   phase 2s + 1: waves 0-3 multiply stage s, waves 4-7 read stage s
+// Stage s is read in phases 2s and 2s + 1, so from phase 2s + 2 on its buffer may be
+// refilled: a wave reading stage s issues k-tile s + NB - 1 into the buffer of
+// stage s - 1.  At the end of phase 2s + 1 every wave has issued k-tiles up to
+// s + NB - 1 and waits until its copies of k-tile s + 1 have landed.
+//
 // A's rows go through a buffer resource based at the tile's first row: rows past
 // M and k past K copy zeros.
 constexpr int kTileNB = 4;
@@ -231,15 +292,30 @@ __device__ __forceinline__ floatx16 mfma32d(bool f16, const u32x4& a, const u32x
                                                    0, 0, 0);
 }
 
-template <bool F16>
-__global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int um, int mtiles, int ntiles, int pairs) {
-    __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][256 * kTileBK];
-    __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][4][4][512];
+// End of a phase: nothing moves across it, and this wave's LDS reads are done.
+__device__ __forceinline__ void phase_end() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool F16, int MW, int NA>
+__global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+    constexpr int WN = 8 / MW;                         // column pairs of the tile
+    constexpr int UM = MW * NA * 32;                   // rows of the tile
+    constexpr int AC = (UM / 16 + 7) / 8;              // 16-row copy blocks per wave and stage
+    constexpr int BD = WN * 4 / 8;                     // 1 KiB weight blocks per wave and stage
+    constexpr int LOADS = AC + BD;
+    __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][AC * 128 * kTileBK];
+    __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][WN * 4][512];
+    __shared__ __attribute__((aligned(16))) float s_e[8][16][64];   // epilogue: 16 rows of each wave
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int mh = wave >> 2, nq = wave & 3;
-    const int hm = (um / 2 + 31) & ~31;                // rows of the first half
-    const int nk = p.Kp / kTileBK;
+    const bool late = wave >= 4;                       // reads in odd phases
+    const int mh = wave / WN, nq = wave % WN;
+    const int nk = p.Kp / kTileBK;                     // even
     const int total = mtiles * ntiles;
     const int G = gridDim.x, b = blockIdx.x;
     // one contiguous range of tiles per XCD and round, 8 row tiles x 4 column tiles of it at a time
@@ -250,126 +326,135 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int um,
         const int group = tile / (kGroup * ntiles), in = tile - group * kGroup * ntiles;
         const int gm = min(kGroup, mtiles - group * kGroup);
         const int n_tile = in / gm, m_tile = group * kGroup + in - n_tile * gm;
-        const int row0 = m_tile * um;
-        const int rows_valid = min(um, p.M - row0);
-        const int half0 = mh * hm;                     // first row of this wave's half
-        const int my_rows = min(rows_valid - half0, mh == 0 ? hm : um - hm);
-        const int na = my_rows > 0 ? (my_rows + 31) >> 5 : 0;
+        const int row0 = m_tile * UM;
 
         const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint16_t*>(p.a) + static_cast<int64_t>(row0) * p.lda, 0, kBufferRange, kBufferFlags);
-        // copy i of column quarter nq: 16-row block i * 4 + nq of the half
-        uint32_t a_off[2];
-        int a_k[2];
+        uint32_t a_off[AC];                            // block i * 8 + wave: row (lane / 4), granule position lane % 4
+        int a_k[AC];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = (i * 4 + nq) * 16 + (lane >> 2);
+        for (int i = 0; i < AC; ++i) {
+            const int row = (i * 8 + wave) * 16 + (lane >> 2);
             const int kg = (lane & 3) ^ ((row >> 2) & 3);
             a_k[i] = kg * 8;
-            a_off[i] = row < my_rows ? static_cast<uint32_t>((half0 + row) * static_cast<int>(p.lda) + kg * 8) * 2
-                                     : kOutOfRange;
+            a_off[i] = row < UM && row0 + row < p.M
+                           ? static_cast<uint32_t>(row * static_cast<int>(p.lda) + kg * 8) * 2
+                           : kOutOfRange;
         }
-        // weight copies: wave (mh, nq) copies blocks 2 mh, 2 mh + 1 of pair nq
-        const int pair = min(n_tile * 4 + nq, pairs - 1);
-        const uint16_t* b_src = p.b + static_cast<int64_t>(pair) * (p.Kp / 32) * (kStepBytes / 2) + mh * 1024 + lane * 8;
-        auto issue = [&](auto ac, int kt, int st) {
-            constexpr int AC = decltype(ac)::value;
-            const int k0 = kt * kTileBK;
+        const int bb = wave * BD;                      // first weight block: pair bb / 4, block bb % 4 of its stage
+        const int pair = min(n_tile * WN + bb / 4, pairs - 1);
+        const uint16_t* b_src =
+            p.b + static_cast<int64_t>(pair) * (p.Kp / 32) * (kStepBytes / 2) + (bb & 3) * 512 + lane * 8;
+        auto issue = [&](int kt) {
+            const int st = kt % kTileNB, kc = min(kt, nk - 1), k0 = kc * kTileBK;
 #pragma unroll
             for (int i = 0; i < AC; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     a_rsrc,
                     reinterpret_cast<__attribute__((address_space(3))) void*>(
-                        reinterpret_cast<uintptr_t>(&s_a[st][(mh * 128 + (i * 4 + nq) * 16) * kTileBK])),
+                        reinterpret_cast<uintptr_t>(&s_a[st][(i * 8 + wave) * 16 * kTileBK])),
                     16, static_cast<int>(k0 + a_k[i] < p.K ? a_off[i] + k0 * 2 : kOutOfRange), 0, 0, 0);
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-                dma16(b_src + static_cast<int64_t>(kt) * (kStepBytes / 2) + d * 512, &s_b[st][nq][mh * 2 + d][0]);
+            for (int d = 0; d < BD; ++d)
+                dma16(b_src + static_cast<int64_t>(kc) * (kStepBytes / 2) + d * 512, &s_b[st][bb + d][0]);
         };
-        floatx16 acc[4][2];
+        floatx16 acc[NA][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NA; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-        auto kloop = [&](auto nac) {
-            constexpr int NA = decltype(nac)::value;
-            constexpr int AC = (2 * NA + 3) / 4;       // blocks of this thread that hold the half's row groups
-            constexpr int LOADS = AC + 2;
+        u32x4 fa[2][NA], fb[2][2];
+        auto read_stage = [&](int st) {
 #pragma unroll
-            for (int q = 0; q + 1 < kTileNB; ++q) issue(IntC<AC>{}, min(q, nk - 1), q);
-            u32x4 fa[2][4], fb[2][2];
-            auto read_frags = [&](int buf, int st, int ks) {
+            for (int ks = 0; ks < 2; ++ks) {
                 const int kg = ks * 2 + (lane >> 5);
 #pragma unroll
                 for (int i = 0; i < NA; ++i)
-                    fa[buf][i] = *reinterpret_cast<const u32x4*>(&s_a[st][tile_swz(mh * 128 + i * 32 + (lane & 31), kg)]);
-                fb[buf][0] = *reinterpret_cast<const u32x4*>(&s_b[st][nq][2 * ks][lane * 8]);
-                fb[buf][1] = *reinterpret_cast<const u32x4*>(&s_b[st][nq][2 * ks + 1][lane * 8]);
-            };
-            auto mfmas = [&](int buf) {
+                    fa[ks][i] =
+                        *reinterpret_cast<const u32x4*>(&s_a[st][tile_swz((mh * NA + i) * 32 + (lane & 31), kg)]);
+                fb[ks][0] = *reinterpret_cast<const u32x4*>(&s_b[st][nq * 4 + 2 * ks][lane * 8]);
+                fb[ks][1] = *reinterpret_cast<const u32x4*>(&s_b[st][nq * 4 + 2 * ks + 1][lane * 8]);
+            }
+        };
+        auto multiply = [&]() {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
-                    acc[i][0] = mfma32d(F16, fa[buf][i], fb[buf][0], acc[i][0]);
-                    acc[i][1] = mfma32d(F16, fa[buf][i], fb[buf][1], acc[i][1]);
+                    acc[i][0] = mfma32d(F16, fa[ks][i], fb[ks][0], acc[i][0]);
+                    acc[i][1] = mfma32d(F16, fa[ks][i], fb[ks][1], acc[i][1]);
                 }
-            };
-            // entered with the stage's first fragments in buffer 0
-            auto step = [&](int kt, int st) {
-                if constexpr (NA > 0) {
-                    read_frags(1, st, 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    asm volatile("" ::: "memory");
-                    mfmas(0);
-                }
-                wait_vmcnt<LOADS * (kTileNB - 3)>();   // this wave's copies of the next stage have landed ...
-                __builtin_amdgcn_s_barrier();          // ... and everyone's; nobody reads the stage refilled below
-                issue(IntC<AC>{}, min(kt + kTileNB - 1, nk - 1), (st + kTileNB - 1) % kTileNB);
-                if constexpr (NA > 0) {
-                    read_frags(0, (st + 1) % kTileNB, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    asm volatile("" ::: "memory");
-                    mfmas(1);
-                }
-            };
-            wait_vmcnt<LOADS * (kTileNB - 2)>();
-            __builtin_amdgcn_s_barrier();
-            if constexpr (NA > 0) read_frags(0, 0, 0);
-            int kt0 = 0;
-            for (; kt0 + kTileNB <= nk; kt0 += kTileNB) {
-#pragma unroll
-                for (int q = 0; q < kTileNB; ++q) step(kt0 + q, q);
-            }
-#pragma unroll
-            for (int q = 0; q + 1 < kTileNB; ++q)
-                if (kt0 + q < nk) step(kt0 + q, q);
+            __builtin_amdgcn_s_setprio(0);
         };
-        switch (na) {
-            case 4: kloop(IntC<4>{}); break;
-            case 3: kloop(IntC<3>{}); break;
-            case 2: kloop(IntC<2>{}); break;
-            case 1: kloop(IntC<1>{}); break;
-            default: kloop(IntC<0>{}); break;
+#pragma unroll
+        for (int q = 0; q + 1 < kTileNB; ++q) issue(q);
+        wait_vmcnt<LOADS * (kTileNB - 2)>();
+        phase_end();
+        if (late) phase_end();                         // phase 0 belongs to waves 0-3
+        for (int s0 = 0; s0 < nk; s0 += 2) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int s = s0 + q;
+                // phase 2s (late: 2s + 1): read stage s, refill the buffer of stage s - 1
+                read_stage(s % kTileNB);
+                issue(s + kTileNB - 1);
+                if (late) wait_vmcnt<LOADS * (kTileNB - 2)>();
+                phase_end();
+                // phase 2s + 1 (late: 2s + 2): multiply
+                multiply();
+                if (!late) wait_vmcnt<LOADS * (kTileNB - 2)>();
+                phase_end();
+            }
         }
-        // lane: column lane % 32, rows 8 (v / 4) + 4 (lane / 32) + v % 4 of each 32 x 32 tile
-        const int cc = lane & 31, pc = n_tile * 4 + nq;
+        if (!late) phase_end();                        // the late waves' last multiply
+        // epilogue: a register holds column lane % 32, row 8 (v / 4) + 4 (lane / 32) + v % 4 of a
+        // 32 x 32 tile; 16 rows at a time go through LDS (columns XORed by 32 in every other group
+        // of four rows, against bank conflicts), so that a lane ends up with four columns of a row
+        const int pc = n_tile * WN + nq;
+        const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
+        const int col = pc * (p.gated ? 32 : 64) + lc;
+        floatx4 b0, b1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            const bool on = p.bias != nullptr && col + i < p.N;
+            b0[i] = on ? p.bias[col + i] : 0.0f;
+            b1[i] = on && p.gated ? p.bias[p.N + col + i] : 0.0f;
+        }
+        float (*e)[64] = s_e[wave];
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int r = i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                if (r >= my_rows) continue;
-                const int row = row0 + half0 + r;
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                        e[r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] = acc[i][j][hf * 8 + v];
+                    }
+                const int base = row0 + (mh * NA + i) * 32 + hf * 16;
                 if (p.gated) {
-                    finish(p, row, pc * 32 + cc, acc[i][0][v], acc[i][1][v]);
+#pragma unroll 1
+                    for (int it = 0; it < 2; ++it) {
+                        const int r = it * 8 + (lane >> 3), x = (r & 4) * 8;
+                        finish4(p, base + r, col, *reinterpret_cast<const floatx4*>(&e[r][lc ^ x]),
+                                *reinterpret_cast<const floatx4*>(&e[r][(lc + 32) ^ x]), b0, b1);
+                    }
                 } else {
-                    finish(p, row, pc * 64 + cc, acc[i][0][v], 0.0f);
-                    finish(p, row, pc * 64 + 32 + cc, acc[i][1][v], 0.0f);
+#pragma unroll 1
+                    for (int it = 0; it < 4; ++it) {
+                        const int r = it * 4 + (lane >> 4), x = (r & 4) * 8;
+                        const floatx4 v = *reinterpret_cast<const floatx4*>(&e[r][lc ^ x]);
+                        finish4(p, base + r, col, v, v, b0, b1);
+                    }
                 }
             }
-        __syncthreads();                               // LDS reuse; drains this tile's copies
+        wait_vmcnt<0>();                               // this tile's last copies have landed
+        __syncthreads();
     }
 }
 
@@ -415,6 +500,44 @@ int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     return MOE_OK;
 }
 
+template <bool F16, int MW, int NA>
+int launch_tile(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+    constexpr int WN = 8 / MW, UM = MW * NA * 32;
+    const int ntiles = static_cast<int>((pairs + WN - 1) / WN), mtiles = (p.M + UM - 1) / UM;
+    const int64_t tiles = static_cast<int64_t>(mtiles) * ntiles;
+    const unsigned grid = static_cast<unsigned>(tiles < kCUs ? tiles : kCUs);
+    hipLaunchKernelGGL((dense_tile_kernel<F16, MW, NA>), dim3(grid), dim3(512), 0, st, p, mtiles, ntiles,
+                       static_cast<int>(pairs));
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+// Tile height and width: the least time of the busiest CU, counting a tile's
+// multiplications (rows x columns) and its copies (rows + columns).
+template <bool F16>
+int launch_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+    int best = 0;
+    double least = 0.0;
+    const int rows[6] = {64, 128, 192, 256, 128, 256}, wide[6] = {4, 4, 4, 4, 2, 2};
+    for (int i = 0; i < 6; ++i) {
+        const int64_t tiles = ((p.M + rows[i] - 1) / rows[i]) * ((pairs + wide[i] - 1) / wide[i]);
+        const double mul = rows[i] * wide[i] * 64 / 65536.0, copy = (rows[i] + wide[i] * 64) / 512.0;
+        const double cost = static_cast<double>((tiles + kCUs - 1) / kCUs) * (mul > copy ? mul : copy);
+        if (i == 0 || cost < least) {
+            least = cost;
+            best = i;
+        }
+    }
+    switch (best) {
+        case 0: return launch_tile<F16, 2, 1>(p, pairs, st);
+        case 1: return launch_tile<F16, 2, 2>(p, pairs, st);
+        case 2: return launch_tile<F16, 2, 3>(p, pairs, st);
+        case 3: return launch_tile<F16, 2, 4>(p, pairs, st);
+        case 4: return launch_tile<F16, 4, 1>(p, pairs, st);
+        default: return launch_tile<F16, 4, 2>(p, pairs, st);
+    }
+}
+
 template <bool F16>
 int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     // 16-byte loads need every row to start on 16 bytes, and a k group to end within the row
@@ -431,25 +554,7 @@ int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
         return p.gated ? launch_stream<F16, 1, 2>(p, pairs, st) : launch_stream<F16, 1, 1>(p, pairs, st);
     if (p.M <= 32) return launch_stream<F16, 2, 2>(p, pairs, st);
     if (p.M <= 512) return launch_stream<F16, 4, 2>(p, pairs, st);
-    const int ntiles = static_cast<int>((pairs + 3) / 4);
-    // tile height: the fewest rows through the busiest CU, counting 64 rows' worth of time for a tile's weight copies
-    int um = 256;
-    int64_t best = -1;
-    for (int h = 256; h >= 64; h -= 32) {
-        const int64_t tiles = static_cast<int64_t>((p.M + h - 1) / h) * ntiles;
-        const int64_t cost = (tiles + kCUs - 1) / kCUs * (h + 64);
-        if (best < 0 || cost < best) {
-            best = cost;
-            um = h;
-        }
-    }
-    const int mtiles = (p.M + um - 1) / um;
-    const int64_t tiles = static_cast<int64_t>(mtiles) * ntiles;
-    const unsigned grid = static_cast<unsigned>(tiles < kCUs ? tiles : kCUs);
-    hipLaunchKernelGGL((dense_tile_kernel<F16>), dim3(grid), dim3(512), 0, st, p, um, mtiles, ntiles,
-                       static_cast<int>(pairs));
-    MOE_CHECK_LAUNCH();
-    return MOE_OK;
+    return launch_tiles<F16>(p, pairs, st);
 }
 
 }  // namespace
@@ -492,6 +597,11 @@ int launch_dense_gemm(const moe_dense_shape& s, const uint16_t* a, int a_dtype, 
     p.act = epilogue;
     p.r_dtype = r_dtype;
     p.c_dtype = c_dtype;
+    auto on_four = [](const void* q, int64_t ld, int dtype) {
+        return reinterpret_cast<uintptr_t>(q) % (dtype == MOE_F32 ? 16 : 8) == 0 && ld % 4 == 0;
+    };
+    p.r_vec = on_four(r, ldr, r_dtype);
+    p.c_vec = on_four(c, ldc, c_dtype);
     return a_dtype == MOE_F16 ? launch_dense<true>(p, pairs_of(s), st) : launch_dense<false>(p, pairs_of(s), st);
 }
 
