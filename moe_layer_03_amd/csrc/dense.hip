@@ -292,10 +292,19 @@ __device__ __forceinline__ floatx16 mfma32d(bool f16, const u32x4& a, const u32x
                                                    0, 0, 0);
 }
 
-// End of a phase: nothing moves across it, and this wave's LDS reads are done.
+// One 16-byte-per-lane buffer -> LDS copy: lane l's bytes, at its offset plus the
+// uniform one, land at the wave's base + 16 l.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rsrc, void* lds_wave_base, int lane_offset,
+                                            int offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(lds_wave_base)),
+        16, lane_offset, offset, 0, 0);
+}
+
+// End of a phase: nothing moves across it.
 __device__ __forceinline__ void phase_end() {
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -343,20 +352,28 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         }
         const int bb = wave * BD;                      // first weight block: pair bb / 4, block bb % 4 of its stage
         const int pair = min(n_tile * WN + bb / 4, pairs - 1);
-        const uint16_t* b_src =
-            p.b + static_cast<int64_t>(pair) * (p.Kp / 32) * (kStepBytes / 2) + (bb & 3) * 512 + lane * 8;
+        const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.b) + static_cast<int64_t>(pair) * (p.Kp / 32) * (kStepBytes / 2), 0, kBufferRange,
+            kBufferFlags);
+        const int b_off = (bb & 3) * 1024 + lane * 16;
+        // Copies of k-tile kt (the last one again past the end) into its stage.  The
+        // tile's place along k is the uniform offset of the copy; only a k-tile that
+        // K ends in looks at each lane's k.
         auto issue = [&](int kt) {
             const int st = kt % kTileNB, kc = min(kt, nk - 1), k0 = kc * kTileBK;
+            uint32_t off[AC];
+#pragma unroll
+            for (int i = 0; i < AC; ++i) off[i] = a_off[i];
+            if (k0 + kTileBK > p.K) {                  // uniform
+#pragma unroll
+                for (int i = 0; i < AC; ++i) off[i] = k0 + a_k[i] < p.K ? a_off[i] : kOutOfRange;
+            }
 #pragma unroll
             for (int i = 0; i < AC; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    a_rsrc,
-                    reinterpret_cast<__attribute__((address_space(3))) void*>(
-                        reinterpret_cast<uintptr_t>(&s_a[st][(i * 8 + wave) * 16 * kTileBK])),
-                    16, static_cast<int>(k0 + a_k[i] < p.K ? a_off[i] + k0 * 2 : kOutOfRange), 0, 0, 0);
+                copy_to_lds(a_rsrc, &s_a[st][(i * 8 + wave) * 16 * kTileBK], static_cast<int>(off[i]), k0 * 2);
 #pragma unroll
             for (int d = 0; d < BD; ++d)
-                dma16(b_src + static_cast<int64_t>(kc) * (kStepBytes / 2) + d * 512, &s_b[st][bb + d][0]);
+                copy_to_lds(b_rsrc, &s_b[st][bb + d][0], b_off, kc * kStepBytes + d * 1024);
         };
         floatx16 acc[NA][2];
 #pragma unroll
@@ -403,6 +420,7 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
                 read_stage(s % kTileNB);
                 issue(s + kTileNB - 1);
                 if (late) wait_vmcnt<LOADS * (kTileNB - 2)>();
+                wait_lgkmcnt0();
                 phase_end();
                 // phase 2s + 1 (late: 2s + 2): multiply
                 multiply();
