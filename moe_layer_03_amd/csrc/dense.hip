@@ -257,21 +257,25 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
 }
 
 // ---- many rows: LDS tiles --------------------------------------------------------------
-// A workgroup of 8 waves owns MW * NA * 32 rows x (8 / MW) 64-column pairs; a wave
-// owns NA * 32 rows x one pair, NA x 2 tiles of v_mfma_f32_32x32x16.  Both
-// operands reach LDS by direct copies into a ring of kTileNB stages of 32 k.
+// A workgroup of 8 waves owns MW * NA * 32 rows x NW 64-column pairs.  Its waves
+// are KG groups of MW x NW; a wave owns NA * 32 rows x one pair, NA x 2 tiles of
+// v_mfma_f32_32x32x16, and the groups share out the k of a stage (small tiles:
+// a stage has to be long, since its barriers cost the same whatever it holds).
+// Both operands reach LDS by direct copies into a ring of kTileNB stages of SL
+// slices of 32 k; the ring runs on from a tile into the workgroup's next one.
 //
 // The two waves of a SIMD (w and w + 4) alternate: while one runs a stage's MFMAs
-// from registers, the other reads its next stage's fragments from LDS and issues
-// copies; a barrier ends each phase and the roles swap.  So the matrix unit
-// always has a wave whose operands are ready, and one register set of fragments
-// suffices (128 accumulators + 48 fragment registers at NA = 4).
+// from registers, the other reads its next fragments from LDS and issues copies;
+// a barrier ends each phase and the roles swap.  So the matrix unit always has a
+// wave whose operands are ready, and one register set of fragments suffices (128
+// accumulators + 48 fragment registers at NA = 4).
 //   phase 2s:     waves 0-3 read stage s, waves 4-7 multiply stage s - 1
 //   phase 2s + 1: waves 0-3 multiply stage s, waves 4-7 read stage s
-// Stage s is read in phases 2s and 2s + 1, so from phase 2s + 2 on its buffer may be
-// refilled: a wave reading stage s issues k-tile s + NB - 1 into the buffer of
-// stage s - 1.  At the end of phase 2s + 1 every wave has issued k-tiles up to
-// s + NB - 1 and waits until its copies of k-tile s + 1 have landed.
+// Stage s is read in phases 2s and 2s + 1 (the reads are complete at the phase's
+// end), so from phase 2s + 2 on its buffer may be refilled: a wave reading stage
+// s copies stage s + NB - 1 into the buffer of stage s - 1.  At the end of phase
+// 2s + 1 every wave has issued copies up to stage s + NB - 1 and waits until its
+// copies of stage s + 1 have landed.
 //
 // A's rows go through a buffer resource based at the tile's first row: rows past
 // M and k past K copy zeros.
@@ -310,71 +314,103 @@ __device__ __forceinline__ void phase_end() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool F16, int MW, int NA>
+// The same where LDS written before it is read after it.
+__device__ __forceinline__ void phase_end_lds() {
+    wait_lgkmcnt0();
+    phase_end();
+}
+
+template <bool F16, int MW, int NW, int NA, int SL>
 __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
-    constexpr int WN = 8 / MW;                         // column pairs of the tile
+    constexpr int KG = 8 / (MW * NW);                  // wave groups along k
+    constexpr int WS = SL * 2 / KG;                    // k-steps of 16 of a wave per stage
     constexpr int UM = MW * NA * 32;                   // rows of the tile
-    constexpr int AC = (UM / 16 + 7) / 8;              // 16-row copy blocks per wave and stage
-    constexpr int BD = WN * 4 / 8;                     // 1 KiB weight blocks per wave and stage
+    constexpr int AB = UM / 16;                        // 16-row copy blocks of a slice
+    constexpr int AC = (SL * AB + 7) / 8;              // copy blocks per wave and stage
+    constexpr int BD = SL * NW * 4 / 8;                // 1 KiB weight blocks per wave and stage
     constexpr int LOADS = AC + BD;
-    __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][AC * 128 * kTileBK];
-    __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][WN * 4][512];
+    static_assert(KG * WS == SL * 2 && (SL * NW * 4) % 8 == 0, "a stage splits evenly");
+    static_assert(BD <= 4 && 4 % BD == 0, "a wave's weight blocks lie in one pair and slice");
+    __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][AC * 8 * 16 * kTileBK];   // [slice][row][32]
+    __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][SL * NW * 4][512];        // [slice][pair][4]
     __shared__ __attribute__((aligned(16))) float s_e[8][16][64];   // epilogue: 16 rows of each wave
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool late = wave >= 4;                       // reads in odd phases
-    const int mh = wave / WN, nq = wave % WN;
-    const int nk = p.Kp / kTileBK;                     // even
+    const int kg = wave / (MW * NW), mh = (wave / NW) % MW, nq = wave % NW;
+    // stages, in whole turns of the ring (a stage past K multiplies zeros), so that ring places are constants
+    const int nk32 = p.Kp / kTileBK, nk = (nk32 + SL * kTileNB - 1) / (SL * kTileNB) * kTileNB;
     const int total = mtiles * ntiles;
     const int G = gridDim.x, b = blockIdx.x;
     // one contiguous range of tiles per XCD and round, 8 row tiles x 4 column tiles of it at a time
     const int lid = (G % 8 == 0) ? (b % 8) * (G / 8) + (b / 8) : b;
     constexpr int kGroup = 8;
-
-    for (int tile = lid; tile < total; tile += G) {
+    auto place = [&](int tile, int& m_tile, int& n_tile) {
         const int group = tile / (kGroup * ntiles), in = tile - group * kGroup * ntiles;
         const int gm = min(kGroup, mtiles - group * kGroup);
-        const int n_tile = in / gm, m_tile = group * kGroup + in - n_tile * gm;
+        n_tile = in / gm;
+        m_tile = group * kGroup + in - n_tile * gm;
+    };
+    // what this wave copies of a tile: A blocks i * 8 + wave (slice, then row block; lane: row lane / 4,
+    // granule position lane % 4) and weight blocks wave * BD + d (slice, pair, block)
+    struct Source {
+        __amdgpu_buffer_rsrc_t a, b;
+        uint32_t a_off[AC];
+    };
+    int a_k[AC];
+#pragma unroll
+    for (int i = 0; i < AC; ++i) {
+        const int row = (i * 8 + wave) % AB * 16 + (lane >> 2);
+        a_k[i] = ((lane & 3) ^ ((row >> 2) & 3)) * 8;
+    }
+    const int b_slice = wave * BD / (NW * 4), b_pair = wave * BD / 4 % NW, b_first = wave * BD % 4;
+    auto source = [&](int tile) {
+        Source s;
+        int m_tile, n_tile;
+        place(tile, m_tile, n_tile);
         const int row0 = m_tile * UM;
-
-        const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p.a) + static_cast<int64_t>(row0) * p.lda, 0, kBufferRange, kBufferFlags);
-        uint32_t a_off[AC];                            // block i * 8 + wave: row (lane / 4), granule position lane % 4
-        int a_k[AC];
+        s.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.a) + static_cast<int64_t>(row0) * p.lda, 0,
+                                                kBufferRange, kBufferFlags);
 #pragma unroll
         for (int i = 0; i < AC; ++i) {
-            const int row = (i * 8 + wave) * 16 + (lane >> 2);
-            const int kg = (lane & 3) ^ ((row >> 2) & 3);
-            a_k[i] = kg * 8;
-            a_off[i] = row < UM && row0 + row < p.M
-                           ? static_cast<uint32_t>(row * static_cast<int>(p.lda) + kg * 8) * 2
-                           : kOutOfRange;
+            const int blk = i * 8 + wave, row = blk % AB * 16 + (lane >> 2);
+            s.a_off[i] = blk < SL * AB && row0 + row < p.M
+                             ? static_cast<uint32_t>(row * static_cast<int>(p.lda) + a_k[i]) * 2
+                             : kOutOfRange;
         }
-        const int bb = wave * BD;                      // first weight block: pair bb / 4, block bb % 4 of its stage
-        const int pair = min(n_tile * WN + bb / 4, pairs - 1);
-        const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p.b) + static_cast<int64_t>(pair) * (p.Kp / 32) * (kStepBytes / 2), 0, kBufferRange,
+        const int pair = min(n_tile * NW + b_pair, pairs - 1);
+        s.b = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.b) + static_cast<int64_t>(pair) * nk32 * (kStepBytes / 2), 0, kBufferRange,
             kBufferFlags);
-        const int b_off = (bb & 3) * 1024 + lane * 16;
-        // Copies of k-tile kt (the last one again past the end) into its stage.  The
-        // tile's place along k is the uniform offset of the copy; only a k-tile that
-        // K ends in looks at each lane's k.
-        auto issue = [&](int kt) {
-            const int st = kt % kTileNB, kc = min(kt, nk - 1), k0 = kc * kTileBK;
-            uint32_t off[AC];
+        return s;
+    };
+    // Copies of stage kt of a tile into ring place st.  The place along k is the
+    // uniform offset of a copy; only a slice that K ends in, or past K, looks at
+    // each lane's k.  Weight slices past the packed end read the last one again:
+    // A is zero there.
+    auto issue = [&](const Source& s, int kt, int st) {
 #pragma unroll
-            for (int i = 0; i < AC; ++i) off[i] = a_off[i];
-            if (k0 + kTileBK > p.K) {                  // uniform
+        for (int i = 0; i < AC; ++i) {
+            const int k0 = (kt * SL + (i * 8 + wave) / AB) * kTileBK;
+            uint32_t off = s.a_off[i];
+            if (k0 + kTileBK > p.K) off = k0 + a_k[i] < p.K ? off : kOutOfRange;   // uniform condition
+            copy_to_lds(s.a, &s_a[st][(i * 8 + wave) * 16 * kTileBK], static_cast<int>(off), k0 * 2);
+        }
+        const int kc = min(kt * SL + b_slice, nk32 - 1);
 #pragma unroll
-                for (int i = 0; i < AC; ++i) off[i] = k0 + a_k[i] < p.K ? a_off[i] : kOutOfRange;
-            }
+        for (int d = 0; d < BD; ++d)
+            copy_to_lds(s.b, &s_b[st][wave * BD + d][0], lane * 16, kc * kStepBytes + (b_first + d) * 1024);
+    };
+
+    int tile = lid;                                    // the grid has no more workgroups than tiles
+    Source cur = source(tile);
 #pragma unroll
-            for (int i = 0; i < AC; ++i)
-                copy_to_lds(a_rsrc, &s_a[st][(i * 8 + wave) * 16 * kTileBK], static_cast<int>(off[i]), k0 * 2);
-#pragma unroll
-            for (int d = 0; d < BD; ++d)
-                copy_to_lds(b_rsrc, &s_b[st][bb + d][0], b_off, kc * kStepBytes + d * 1024);
-        };
+    for (int q = 0; q + 1 < kTileNB; ++q) issue(cur, q, q);
+    wait_vmcnt<LOADS * (kTileNB - 2)>();
+    phase_end();
+    for (;;) {
+        const bool more = tile + G < total;            // uniform
+        const Source next = source(more ? tile + G : tile);
         floatx16 acc[NA][2];
 #pragma unroll
         for (int i = 0; i < NA; ++i)
@@ -383,42 +419,41 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-        u32x4 fa[2][NA], fb[2][2];
+        u32x4 fa[WS][NA], fb[WS][2];
         auto read_stage = [&](int st) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const int kg = ks * 2 + (lane >> 5);
+            for (int w = 0; w < WS; ++w) {
+                const int ks = kg * WS + w, slice = ks >> 1, kq = (ks & 1) * 2 + (lane >> 5);
 #pragma unroll
                 for (int i = 0; i < NA; ++i)
-                    fa[ks][i] =
-                        *reinterpret_cast<const u32x4*>(&s_a[st][tile_swz((mh * NA + i) * 32 + (lane & 31), kg)]);
-                fb[ks][0] = *reinterpret_cast<const u32x4*>(&s_b[st][nq * 4 + 2 * ks][lane * 8]);
-                fb[ks][1] = *reinterpret_cast<const u32x4*>(&s_b[st][nq * 4 + 2 * ks + 1][lane * 8]);
+                    fa[w][i] = *reinterpret_cast<const u32x4*>(
+                        &s_a[st][slice * (UM * kTileBK) + tile_swz((mh * NA + i) * 32 + (lane & 31), kq)]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    fb[w][j] =
+                        *reinterpret_cast<const u32x4*>(&s_b[st][(slice * NW + nq) * 4 + 2 * (ks & 1) + j][lane * 8]);
             }
         };
         auto multiply = [&]() {
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
+            for (int w = 0; w < WS; ++w)
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
-                    acc[i][0] = mfma32d(F16, fa[ks][i], fb[ks][0], acc[i][0]);
-                    acc[i][1] = mfma32d(F16, fa[ks][i], fb[ks][1], acc[i][1]);
+                    acc[i][0] = mfma32d(F16, fa[w][i], fb[w][0], acc[i][0]);
+                    acc[i][1] = mfma32d(F16, fa[w][i], fb[w][1], acc[i][1]);
                 }
             __builtin_amdgcn_s_setprio(0);
         };
+        if (late) phase_end();                         // the first phase belongs to waves 0-3
+        for (int s0 = 0; s0 < nk; s0 += kTileNB) {
+            const bool last = s0 + kTileNB == nk;      // uniform
 #pragma unroll
-        for (int q = 0; q + 1 < kTileNB; ++q) issue(q);
-        wait_vmcnt<LOADS * (kTileNB - 2)>();
-        phase_end();
-        if (late) phase_end();                         // phase 0 belongs to waves 0-3
-        for (int s0 = 0; s0 < nk; s0 += 2) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int s = s0 + q;
-                // phase 2s (late: 2s + 1): read stage s, refill the buffer of stage s - 1
-                read_stage(s % kTileNB);
-                issue(s + kTileNB - 1);
+            for (int q = 0; q < kTileNB; ++q) {
+                // phase 2s (late: 2s + 1): read stage s = s0 + q, refill the buffer of stage s - 1
+                read_stage(q);
+                if (q == 0 || !last) issue(cur, s0 + q + kTileNB - 1, (q + kTileNB - 1) % kTileNB);
+                else issue(next, q - 1, q - 1);
                 if (late) wait_vmcnt<LOADS * (kTileNB - 2)>();
                 wait_lgkmcnt0();
                 phase_end();
@@ -429,12 +464,16 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
             }
         }
         if (!late) phase_end();                        // the late waves' last multiply
+
         // epilogue: a register holds column lane % 32, row 8 (v / 4) + 4 (lane / 32) + v % 4 of a
         // 32 x 32 tile; 16 rows at a time go through LDS (columns XORed by 32 in every other group
-        // of four rows, against bank conflicts), so that a lane ends up with four columns of a row
-        const int pc = n_tile * WN + nq;
+        // of four rows, against bank conflicts), so that a lane ends up with four columns of a row;
+        // the k groups' partial sums are added there, in group order
+        int m_tile, n_tile;
+        place(tile, m_tile, n_tile);
         const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
-        const int col = pc * (p.gated ? 32 : 64) + lc;
+        const int lr = p.gated ? lane >> 3 : lane >> 4, dr = p.gated ? 8 : 4;   // rows a wave takes at once
+        const int col = (n_tile * NW + nq) * (p.gated ? 32 : 64) + lc;
         floatx4 b0, b1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -442,7 +481,6 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
             b0[i] = on ? p.bias[col + i] : 0.0f;
             b1[i] = on && p.gated ? p.bias[p.N + col + i] : 0.0f;
         }
-        float (*e)[64] = s_e[wave];
 #pragma unroll
         for (int i = 0; i < NA; ++i)
 #pragma unroll
@@ -452,28 +490,29 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
                         const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                        e[r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] = acc[i][j][hf * 8 + v];
+                        s_e[wave][r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] = acc[i][j][hf * 8 + v];
                     }
-                const int base = row0 + (mh * NA + i) * 32 + hf * 16;
-                if (p.gated) {
+                if constexpr (KG > 1) phase_end_lds();
+                const int base = m_tile * UM + (mh * NA + i) * 32 + hf * 16;
 #pragma unroll 1
-                    for (int it = 0; it < 2; ++it) {
-                        const int r = it * 8 + (lane >> 3), x = (r & 4) * 8;
-                        finish4(p, base + r, col, *reinterpret_cast<const floatx4*>(&e[r][lc ^ x]),
-                                *reinterpret_cast<const floatx4*>(&e[r][(lc + 32) ^ x]), b0, b1);
+                for (int r0 = kg * dr; r0 < 16; r0 += KG * dr) {
+                    const int r = r0 + lr, x = (r & 4) * 8;
+                    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+#pragma unroll
+                    for (int q = 0; q < KG; ++q) {
+                        const float* e = &s_e[q * MW * NW + mh * NW + nq][r][0];
+                        v += *reinterpret_cast<const floatx4*>(e + (lc ^ x));
+                        if (p.gated) u += *reinterpret_cast<const floatx4*>(e + ((lc + 32) ^ x));
                     }
-                } else {
-#pragma unroll 1
-                    for (int it = 0; it < 4; ++it) {
-                        const int r = it * 4 + (lane >> 4), x = (r & 4) * 8;
-                        const floatx4 v = *reinterpret_cast<const floatx4*>(&e[r][lc ^ x]);
-                        finish4(p, base + r, col, v, v, b0, b1);
-                    }
+                    finish4(p, base + r, col, v, u, b0, b1);
                 }
+                if constexpr (KG > 1) phase_end_lds();
             }
-        wait_vmcnt<0>();                               // this tile's last copies have landed
-        __syncthreads();
+        if (!more) break;
+        tile += G;
+        cur = next;
     }
+    wait_vmcnt<0>();                                   // no copy is in flight when the workgroup's LDS is given back
 }
 
 // ---- packing --------------------------------------------------------------------------
@@ -518,41 +557,47 @@ int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     return MOE_OK;
 }
 
-template <bool F16, int MW, int NA>
+template <bool F16, int MW, int NW, int NA, int SL>
 int launch_tile(const DenseArgs& p, int64_t pairs, hipStream_t st) {
-    constexpr int WN = 8 / MW, UM = MW * NA * 32;
-    const int ntiles = static_cast<int>((pairs + WN - 1) / WN), mtiles = (p.M + UM - 1) / UM;
+    constexpr int UM = MW * NA * 32;
+    const int ntiles = static_cast<int>((pairs + NW - 1) / NW), mtiles = (p.M + UM - 1) / UM;
     const int64_t tiles = static_cast<int64_t>(mtiles) * ntiles;
-    const unsigned grid = static_cast<unsigned>(tiles < kCUs ? tiles : kCUs);
-    hipLaunchKernelGGL((dense_tile_kernel<F16, MW, NA>), dim3(grid), dim3(512), 0, st, p, mtiles, ntiles,
+    const unsigned grid = static_cast<unsigned>(tiles < kCUs ? tiles : kCUs);   // persistent, one to a CU
+    hipLaunchKernelGGL((dense_tile_kernel<F16, MW, NW, NA, SL>), dim3(grid), dim3(512), 0, st, p, mtiles, ntiles,
                        static_cast<int>(pairs));
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }
 
-// Tile height and width: the least time of the busiest CU, counting a tile's
-// multiplications (rows x columns) and its copies (rows + columns).
+// Tile shape: the least time of the busiest CU.  A stage takes the longer of its
+// multiplications and its copies, and a fixed part for its two barriers.
+struct TileShape {
+    int rows, pairs, slices;
+};
+constexpr TileShape kTileShapes[] = {{256, 4, 1}, {192, 4, 1}, {128, 4, 1}, {128, 2, 2}, {64, 2, 2}, {64, 1, 4}};
+
 template <bool F16>
 int launch_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     int best = 0;
     double least = 0.0;
-    const int rows[6] = {64, 128, 192, 256, 128, 256}, wide[6] = {4, 4, 4, 4, 2, 2};
     for (int i = 0; i < 6; ++i) {
-        const int64_t tiles = ((p.M + rows[i] - 1) / rows[i]) * ((pairs + wide[i] - 1) / wide[i]);
-        const double mul = rows[i] * wide[i] * 64 / 65536.0, copy = (rows[i] + wide[i] * 64) / 512.0;
-        const double cost = static_cast<double>((tiles + kCUs - 1) / kCUs) * (mul > copy ? mul : copy);
+        const TileShape& t = kTileShapes[i];
+        const int64_t tiles = ((p.M + t.rows - 1) / t.rows) * ((pairs + t.pairs - 1) / t.pairs);
+        const int64_t stages = (p.Kp / kTileBK + t.slices - 1) / t.slices + 8;
+        const double mul = t.rows * t.pairs * t.slices / 1024.0 * 1200, copy = (t.rows + t.pairs * 64) * t.slices / 512.0 * 850;
+        const double cost = static_cast<double>((tiles + kCUs - 1) / kCUs) * stages * ((mul > copy ? mul : copy) + 250);
         if (i == 0 || cost < least) {
             least = cost;
             best = i;
         }
     }
     switch (best) {
-        case 0: return launch_tile<F16, 2, 1>(p, pairs, st);
-        case 1: return launch_tile<F16, 2, 2>(p, pairs, st);
-        case 2: return launch_tile<F16, 2, 3>(p, pairs, st);
-        case 3: return launch_tile<F16, 2, 4>(p, pairs, st);
-        case 4: return launch_tile<F16, 4, 1>(p, pairs, st);
-        default: return launch_tile<F16, 4, 2>(p, pairs, st);
+        case 0: return launch_tile<F16, 2, 4, 4, 1>(p, pairs, st);
+        case 1: return launch_tile<F16, 2, 4, 3, 1>(p, pairs, st);
+        case 2: return launch_tile<F16, 2, 4, 2, 1>(p, pairs, st);
+        case 3: return launch_tile<F16, 2, 2, 2, 2>(p, pairs, st);
+        case 4: return launch_tile<F16, 1, 2, 2, 2>(p, pairs, st);
+        default: return launch_tile<F16, 1, 1, 2, 4>(p, pairs, st);
     }
 }
 
