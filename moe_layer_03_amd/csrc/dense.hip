@@ -182,7 +182,6 @@ struct DenseCursor {
     __amdgpu_buffer_rsrc_t rows;
     uint32_t off[MT];          // byte offset of this lane's k group, or out of range
     int k, K;                  // first k of the lane's group in this step
-    int left;
 
     __device__ __forceinline__ void load(StepRegs<1, false, MT, CT>& s) {
 #pragma unroll
@@ -192,12 +191,10 @@ struct DenseCursor {
         for (int m = 0; m < MT; ++m)
             s.a[m][0][0] = __builtin_bit_cast(
                 u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, k < K ? off[m] : kOutOfRange, 0, 0));
-        const int go = left > 0 ? 1 : 0;               // uniform
-        left -= go;
-        b += go * (kNW * kStepBytes);
-        k += go * (kNW * 32);
+        b += kNW * kStepBytes;
+        k += kNW * 32;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) off[m] += go * (kNW * 64);
+        for (int m = 0; m < MT; ++m) off[m] += kNW * 64;
     }
 };
 
@@ -219,7 +216,6 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     cur.k = wave * 32 + (lane >> 4) * 8;
     cur.K = p.K;
     const int steps = nk > wave ? (nk - wave + kNW - 1) / kNW : 0;
-    cur.left = steps - 1;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int r = m * kRowTile + (lane & 15);
@@ -227,7 +223,9 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     }
     Acc<1, F16, false, MT, CT> acc;
     acc.clear();
-    stream_steps<4>(steps, cur, acc);
+    StepRegs<1, false, MT, CT> ring[4];
+    start_steps(steps, cur, ring);
+    run_steps(steps, cur, ring, acc);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll

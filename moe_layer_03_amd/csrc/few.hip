@@ -33,7 +33,21 @@ namespace moe {
 namespace {
 
 constexpr int kNW = 8;                                 // waves per workgroup of the two products
-constexpr int kRouteNW = 8;
+
+// Steps a gate/up wave has in flight (2 KiB of weights each), as many as the
+// registers of four waves per SIMD hold, four at most: two workgroups on a CU
+// then have 128 KiB in flight.  Rows of many parts (float32 rows with MXFP8
+// weights) keep two steps and half the waves.
+constexpr int gate_up_step_regs(int NP, bool MX, int MT) { return 8 + (MX ? 2 : 0) + MT * NP * (MX ? 8 : 4); }
+constexpr int gate_up_ring(int NP, bool MX, int MT) {
+    const int n = (96 - MT * 8 * (NP == 2 ? 2 : 1)) / gate_up_step_regs(NP, MX, MT);
+    return n > 4 ? 4 : (n < 2 ? 2 : n);
+}
+constexpr int gate_up_waves(int NP, bool MX, int MT) {
+    return 2 * gate_up_step_regs(NP, MX, MT) > 80 ? 2 : 4;
+}
+constexpr int kRouteNW = 16;
+constexpr int kRouteGroups = 2;                        // 32-h groups of a wave in flight together
 constexpr int kMaxSlices = 16;
 
 typedef double doublex4 __attribute__((ext_vector_type(4)));
@@ -54,6 +68,14 @@ struct FewArgs {
     int S, T, H, E, K, I, e_begin, E_loc;
 };
 
+// Barrier for LDS data; loads to registers stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---- route -------------------------------------------------------------------
 
 template <typename XT> __device__ __forceinline__ double widen(XT v);
@@ -61,40 +83,58 @@ template <> __device__ __forceinline__ double widen<uint16_t>(uint16_t v) { retu
 template <> __device__ __forceinline__ double widen<float>(float v) { return v; }
 
 // One workgroup: 16 experts x 16 tokens x one slice of H; its waves take 32-h
-// groups in turn.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and
-// k = l / 16; the four k of a group's step j are h = 8 (l / 16) + j.  The products
-// of bf16 (float32) inputs are exact in double, so only the additions round.
+// groups in turn, at most kRouteGroups each, all loads issued before the first
+// product.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and k = l / 16;
+// the four k of a group's step j are h = 8 (l / 16) + j.  The products of bf16
+// (float32) inputs are exact in double, so only the additions round.
 // NPX > 0: the first expert column also writes the rows' parts for the gate/up product.
 template <typename XT, int NPX, bool F16>
 __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __restrict__ x, const XT* __restrict__ w,
                                                                   int T, int H, int E, double* __restrict__ part,
                                                                   uint16_t* __restrict__ xp, int64_t xp_part) {
     __shared__ double s_red[kRouteNW][4][kWave];
+    constexpr int V = 16 / sizeof(XT);                 // elements of a 16-byte load
+    typedef XT vec __attribute__((ext_vector_type(V)));
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
     const int t = blockIdx.y * kRowTile + r, e = blockIdx.x * kRowTile + r;
     const int groups = H / 32, step = gridDim.z * kRouteNW;
+    const int g0 = blockIdx.z * kRouteNW + wave;
     doublex4 acc = {0.0, 0.0, 0.0, 0.0};
-    for (int g = blockIdx.z * kRouteNW + wave; g < groups; g += step) {
-        const int h0 = g * 32 + kq * 8;
-        XT xv[8], wv[8];
+    for (int gb = g0; gb < groups; gb += kRouteGroups * step) {
+        XT wv[kRouteGroups][8];
+        vec xv[kRouteGroups][8 / V];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            xv[j] = t < T ? x[static_cast<int64_t>(t) * H + h0 + j] : XT(0);
-            wv[j] = e < E ? w[static_cast<int64_t>(h0 + j) * E + e] : XT(0);
+        for (int q = 0; q < kRouteGroups; ++q) {
+            const int g = gb + q * step;
+            const bool in = g < groups;                // uniform
+            const int h0 = (in ? g : g0) * 32 + kq * 8;
+            const XT* wp = w + static_cast<int64_t>(h0) * E + min(e, E - 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wv[q][j] = wp[static_cast<int64_t>(j) * E];
+            const vec* xs = reinterpret_cast<const vec*>(x + static_cast<int64_t>(min(t, T - 1)) * H + h0);
+#pragma unroll
+            for (int j = 0; j < 8 / V; ++j) xv[q][j] = xs[j];
         }
+        // values of rows past T and columns past E are computed and dropped
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(widen<XT>(xv[j]), widen<XT>(wv[j]), acc, 0, 0, 0);
-        if constexpr (NPX > 0) {
-            if (blockIdx.x == 0 && t < T) {
+        for (int q = 0; q < kRouteGroups; ++q) {
+            if (gb + q * step >= groups) break;        // uniform
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint16_t p[NPX];
-                    split_parts<NPX, F16>(static_cast<float>(widen<XT>(xv[j])), p);
+            for (int j = 0; j < 8; ++j)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(widen<XT>(xv[q][j / V][j % V]), widen<XT>(wv[q][j]), acc, 0,
+                                                           0, 0);
+            if constexpr (NPX > 0) {
+                if (blockIdx.x == 0 && t < T) {
+                    const int h0 = (gb + q * step) * 32 + kq * 8;
 #pragma unroll
-                    for (int q = 0; q < NPX; ++q) xp[q * xp_part + static_cast<int64_t>(t) * H + h0 + j] = p[q];
+                    for (int j = 0; j < 8; ++j) {
+                        uint16_t p[NPX];
+                        split_parts<NPX, F16>(static_cast<float>(xv[q][j / V][j % V]), p);
+#pragma unroll
+                        for (int n = 0; n < NPX; ++n) xp[n * xp_part + static_cast<int64_t>(t) * H + h0 + j] = p[n];
+                    }
                 }
             }
         }
@@ -127,26 +167,32 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
                    static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 63))));
 }
 
-// One wave: token t's logits summed over the slices, its K best in order (larger
-// first, equal ones by index) and their weights, to LDS.  A lane holds experts
-// 64 g + lane.  A double is compared by its ordered bits, upper word first; the
+// The logit of (t, e): its slices' sums, then the bias.
+__device__ __forceinline__ double logit_of(const FewArgs& p, int t, int e) {
+    const double* q = p.part + static_cast<int64_t>(t) * p.E + e;
+    const int64_t slice = static_cast<int64_t>(p.T) * p.E;
+    double v = 0.0;
+    for (int s = 0; s < p.S; ++s) v += q[s * slice];
+    if (p.bias != nullptr) v += p.bias[e];
+    return v + 0.0;                                    // -0 and +0 compare equal
+}
+
+// One wave: token t's K best experts in order (larger logit first, equal ones by
+// index) and their weights, to LDS.  logits: the token's, or NULL to sum them
+// here.  A lane holds experts 64 g + lane.  A double is compared by its ordered bits, upper word first; the
 // lower word is looked at only where upper words are equal.
 template <int NE>
-__device__ __forceinline__ void select_token(const FewArgs& p, int t, int* s_idx, float* s_w, double* s_val) {
+__device__ __forceinline__ void select_token(const FewArgs& p, int t, const double* logits, int* s_idx, float* s_w,
+                                             double* s_val) {
     const int lane = threadIdx.x & (kWave - 1);
-    double val[NE];
     uint32_t hi[NE], lo[NE];
     uint32_t dead = 0u;
 #pragma unroll
     for (int g = 0; g < NE; ++g) {
         const int e = g * kWave + lane;
-        val[g] = 0.0;
-        if (e < p.E) {
-            for (int s = 0; s < p.S; ++s) val[g] += p.part[(static_cast<int64_t>(s) * p.T + t) * p.E + e];
-            if (p.bias != nullptr) val[g] += p.bias[e];
-            val[g] += 0.0;                             // -0 and +0 compare equal
-        }
-        uint64_t u = __builtin_bit_cast(uint64_t, val[g]);
+        double v = 0.0;
+        if (e < p.E) v = logits != nullptr ? logits[e] : logit_of(p, t, e);
+        uint64_t u = __builtin_bit_cast(uint64_t, v);
         u ^= (u >> 63) ? ~0ull : (1ull << 63);
         hi[g] = e < p.E ? static_cast<uint32_t>(u >> 32) : 0u;
         lo[g] = static_cast<uint32_t>(u);
@@ -175,7 +221,9 @@ __device__ __forceinline__ void select_token(const FewArgs& p, int t, int* s_idx
 #pragma unroll
         for (int g = 0; g < NE; ++g)
             if (g * kWave + lane == best) {
-                s_val[k] = val[g];
+                uint64_t u = (static_cast<uint64_t>(hi[g]) << 32) | lo[g];
+                u ^= (u >> 63) ? (1ull << 63) : ~0ull;
+                s_val[k] = __builtin_bit_cast(double, u);
                 hi[g] = 0u;
                 dead |= 1u << g;
             }
@@ -280,7 +328,6 @@ struct GateUpCursor {
     __amdgpu_buffer_rsrc_t rows;
     uint32_t off[MT];          // byte offset of this lane's k group in part 0 of its row, or out of range
     uint32_t part_bytes;
-    int left;                  // steps after this one
 
     __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 2>& s) {
         constexpr int half = MX ? 2048 : 1024;         // up columns: the other half of the pair
@@ -298,17 +345,15 @@ struct GateUpCursor {
                 for (int l = 0; l < (MX ? 2 : 1); ++l)
                     s.a[m][q][l] = __builtin_bit_cast(
                         u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off[m] + q * part_bytes + l * 16, 0, 0));
-        const int go = left > 0 ? 1 : 0;               // uniform
-        left -= go;
-        b += go * (kNW * kStepBytes);
-        if constexpr (MX) sc += go * (kNW * 2);
+        b += kNW * kStepBytes;
+        if constexpr (MX) sc += kNW * 2;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) off[m] += go * (kNW * (MX ? 128 : 64));
+        for (int m = 0; m < MT; ++m) off[m] += kNW * (MX ? 128 : 64);
     }
 };
 
 template <int NP, bool F16, bool MX, int MT, int NPH, bool F16H>
-__global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
+__global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_up_kernel(FewArgs p) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][2][4][kWave];
     __shared__ double s_val[kNW][kWave];
@@ -316,10 +361,18 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
+    // the logits of all tokens at once where s_red holds them, so that their loads are in flight together
+    double* logits = reinterpret_cast<double*>(&s_red[0][0][0][0][0]);
+    const bool together = static_cast<size_t>(p.T) * p.E * 8 <= sizeof(s_red);
+    if (together) {
+        for (int i = tid; i < p.T * p.E; i += kNW * 64) logits[i] = logit_of(p, i / p.E, i % p.E);
+        __syncthreads();
+    }
     for (int t = wave; t < p.T; t += kNW) {
-        if (p.E <= 128) select_token<2>(p, t, tb.idx, tb.w, s_val[wave]);
-        else if (p.E <= 256) select_token<4>(p, t, tb.idx, tb.w, s_val[wave]);
-        else select_token<16>(p, t, tb.idx, tb.w, s_val[wave]);
+        const double* mine = together ? logits + t * p.E : nullptr;
+        if (p.E <= 128) select_token<2>(p, t, mine, tb.idx, tb.w, s_val[wave]);
+        else if (p.E <= 256) select_token<4>(p, t, mine, tb.idx, tb.w, s_val[wave]);
+        else select_token<16>(p, t, mine, tb.idx, tb.w, s_val[wave]);
     }
     __syncthreads();
     if (blockIdx.x == 0)
@@ -334,41 +387,56 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
     const int nk = p.H / (MX ? 64 : 32);               // steps of a unit
     const __amdgpu_buffer_rsrc_t rows =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.a), 0, kBufferRange, kBufferFlags);
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    GateUpCursor<NP, MX, MT> cur;
+    cur.rows = rows;
+    cur.part_bytes = static_cast<uint32_t>(p.a_part * 2);
+    cur.sc_up = p.H;                                   // 32 columns further, H / 32 bytes each
+    const int steps = nk > wave ? (nk - wave + kNW - 1) / kNW : 0;
+    auto enter = [&](int unit) {
         const int a = unit / nb, u = unit - a * nb;
         const int e = __builtin_amdgcn_readfirstlane(tb.act[a]);
         const int pair = u >> 1, c0 = (u & 1) * 16;
         const int8_t* slot = tb.slot + a * p.T;
-
-        GateUpCursor<NP, MX, MT> cur;
         const int64_t first = (static_cast<int64_t>(e) * (p.I >> 5) + pair) * nk + wave;
         cur.b = p.gu + first * kStepBytes + step_lane_offset<MX>(0, c0);
         if constexpr (MX) {
             const int64_t col = static_cast<int64_t>(e) * 2 * p.I + pair * 64 + c0 + (lane & 15);
             cur.sc = p.gu_scales + col * (p.H / 32) + wave * 2 + (lane >> 5);
-            cur.sc_up = p.H;                           // 32 columns further, H / 32 bytes each
         }
-        cur.rows = rows;
-        cur.part_bytes = static_cast<uint32_t>(p.a_part * 2);
-        cur.left = (nk - wave + kNW - 1) / kNW - 1;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int t = m * kRowTile + (lane & 15);
             const bool on = t < p.T && slot[t < p.T ? t : 0] >= 0;
             cur.off[m] = on ? static_cast<uint32_t>(t * p.H + (wave * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2 : kOutOfRange;
         }
+    };
+    StepRegs<NP, MX, MT, 2> ring[gate_up_ring(NP, MX, MT)];
+    int unit = blockIdx.x;
+    if (unit < units) {
+        enter(unit);
+        start_steps(steps, cur, ring);
+    }
+    while (unit < units) {                             // uniform over the workgroup
         Acc<NP, F16, MX, MT, 2> acc;
         acc.clear();
-        stream_steps<4>(cur.left + 1, cur, acc);
+        run_steps(steps, cur, ring, acc);
+        // the next unit's first loads are on their way while this one is finished
+        const int done = unit;
+        unit += gridDim.x;
+        if (unit < units) {
+            enter(unit);
+            start_steps(steps, cur, ring);
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) s_red[wave][m][c][v][lane] = acc.value(m, c, v);
-        __syncthreads();
+        lds_barrier();
         // thread -> (row tile, register, lane): row 4 (lane / 16) + register, column lane % 16
         if (tid < MT * 256) {
+            const int a = done / nb, u = done - a * nb;
             const int m = tid >> 8, v = (tid >> 6) & 3;
             const int t = m * kRowTile + (lane >> 4) * 4 + v;
             float g = 0.0f, up = 0.0f;
@@ -377,7 +445,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
                 g += s_red[q][m][0][v][lane];
                 up += s_red[q][m][1][v][lane];
             }
-            const int j = t < p.T ? slot[t] : -1;
+            const int j = t < p.T ? tb.slot[a * p.T + t] : -1;
             if (j >= 0) {
                 const int row = t * p.K + j;
                 const float act = g / (1.0f + expf(-g)) * up * tb.w[row];
@@ -389,7 +457,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_gate_up_kernel(FewArgs p) {
                     p.h[(q * pairs + row) * p.I + u * kRowTile + (lane & 15)] = part[q];
             }
         }
-        __syncthreads();                               // s_red is free
+        lds_barrier();                                 // s_red is free
     }
 }
 
@@ -405,8 +473,8 @@ struct DownCursor {
     int64_t b_expert, sc_expert;   // bytes per expert
     __amdgpu_buffer_rsrc_t rows;
     uint32_t part_bytes;
-    int nk, count;             // steps per expert, chosen experts
-    int a, ks;                 // current step
+    int nk;                    // steps per expert
+    int a, ks;                 // next step
 
     __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 1>& s) {
         const int lane = threadIdx.x & (kWave - 1);
@@ -428,22 +496,18 @@ struct DownCursor {
                     s.a[m][q][l] = __builtin_bit_cast(
                         u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off + q * part_bytes + l * 16, 0, 0));
         }
-        // advance, staying on this wave's last step at the end
-        int na = a, nks = ks + kNW;
-        while (nks >= nk) {
-            nks -= nk;
-            ++na;
-        }
-        if (na < count) {
-            a = na;
-            ks = nks;
+        ks += kNW;
+        while (ks >= nk) {
+            ks -= nk;
+            ++a;
         }
     }
 };
 
 template <int NP, bool F16, bool MX, int MT>
-__global__ __launch_bounds__(kNW * 64, 2) void few_down_kernel(FewArgs p) {
-    constexpr int D = MX ? 2 : 4;                      // an MXFP8 step is 64 k of up to 3 parts
+__global__ __launch_bounds__(kNW * 64, 1) void few_down_kernel(FewArgs p) {
+    // loads in flight: 1 KiB of weights per wave and step, one workgroup to a CU
+    constexpr int D = MX ? (MT == 1 ? 6 : 4) : (MT == 1 ? 8 : 6);
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][4][kWave];
     const Tables tb = carve_tables(smem, p);
@@ -460,8 +524,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_down_kernel(FewArgs p) {
     cur.p = &p;
     cur.tb = &tb;
     cur.nk = p.I / (MX ? 64 : 32);
-    cur.count = __builtin_amdgcn_readfirstlane(*tb.count);
-    const int total = cur.count * cur.nk;
+    const int total = __builtin_amdgcn_readfirstlane(*tb.count) * cur.nk;
     cur.b_expert = static_cast<int64_t>(p.H >> 6) * cur.nk * kStepBytes;
     cur.b = p.dn + static_cast<int64_t>(n64) * cur.nk * kStepBytes + step_lane_offset<MX>(half, c0);
     if constexpr (MX) {
@@ -474,7 +537,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_down_kernel(FewArgs p) {
     cur.ks = wave - cur.a * cur.nk;
     Acc<NP, F16, MX, MT, 1> acc;
     acc.clear();
-    stream_steps<D>(total > wave ? (total - wave + kNW - 1) / kNW : 0, cur, acc);
+    const int steps = total > wave ? (total - wave + kNW - 1) / kNW : 0;
+    StepRegs<NP, MX, MT, 1> ring[D];
+    start_steps(steps, cur, ring);
+    run_steps(steps, cur, ring, acc);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -492,13 +558,15 @@ __global__ __launch_bounds__(kNW * 64, 2) void few_down_kernel(FewArgs p) {
 
 // ---- host -----------------------------------------------------------------------------
 
-// Slices of H in the route step: enough workgroups for the few (16 expert x 16
-// token) tiles, few enough partials for every gate/up workgroup to add.
+// Slices of H in the route step: few enough that a wave has at most
+// kRouteGroups groups in flight at once and that every gate/up workgroup adds
+// them up quickly; one or two tokens take more, as their partials are short.
 int route_slices(int T, int H) {
-    int S = T <= 2 ? kMaxSlices : 32 / T;
-    if (S < 2) S = 2;
-    const int most = (H / 32 + kRouteNW - 1) / kRouteNW;
-    return S < most ? S : most;
+    const int groups = H / 32;
+    const int most = (groups + kRouteNW - 1) / kRouteNW;           // one group a wave
+    const int few = (groups + kRouteNW * kRouteGroups - 1) / (kRouteNW * kRouteGroups);
+    const int S = T <= 8 ? most : few;
+    return S < kMaxSlices ? S : kMaxSlices;
 }
 
 // parts of the gate/up rows that the route step writes (0: the rows are read from x)

@@ -125,18 +125,23 @@ __device__ __forceinline__ int step_lane_offset(int half, int c0) {
     return MX ? half * 2048 + (kq >> 1) * 1024 + slot : (kq >> 1) * 2048 + half * 1024 + slot;
 }
 
-// Adds n steps to acc.  cur.load(regs) issues the loads of the next step (the
-// last step again once there are no more) into a register ring D steps deep;
-// whole turns of the ring have no branch inside, so the wait before a step
-// leaves the younger D - 1 steps' loads in flight.
-template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
-__device__ __forceinline__ void stream_steps(int n, Cursor& cur, Acc<NP, F16, MX, MT, CT>& acc) {
-    if (n <= 0) return;                                // uniform over the wave
-    StepRegs<NP, MX, MT, CT> ring[D];
+// A product of n steps whose first D loads are already on their way: start_steps
+// issues them (cur.load(regs) issues the loads of cur's next step), run_steps adds
+// all n steps, loading D ahead.  Whole turns of the ring have no branch inside, so
+// the wait before a step leaves the younger D - 1 steps' loads in flight; only
+// the last turns test whether a step is there.
+template <int D, int NP, bool MX, int MT, int CT, typename Cursor>
+__device__ __forceinline__ void start_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D]) {
 #pragma unroll
-    for (int j = 0; j < D; ++j) cur.load(ring[j]);
+    for (int j = 0; j < D; ++j)
+        if (j < n) cur.load(ring[j]);                  // uniform
+}
+
+template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
+__device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D],
+                                          Acc<NP, F16, MX, MT, CT>& acc) {
     int i = 0;
-    for (; i + D <= n; i += D) {
+    for (; i + 2 * D <= n; i += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             acc.add(ring[j]);
@@ -144,8 +149,11 @@ __device__ __forceinline__ void stream_steps(int n, Cursor& cur, Acc<NP, F16, MX
         }
     }
 #pragma unroll
-    for (int j = 0; j < D; ++j)
-        if (i + j < n) acc.add(ring[j]);               // uniform
+    for (int j = 0; j < 2 * D - 1; ++j)
+        if (i + j < n) {                               // uniform
+            acc.add(ring[j % D]);
+            if (j < D && i + j + D < n) cur.load(ring[j % D]);
+        }
 }
 
 }  // namespace
