@@ -193,6 +193,8 @@ struct FewWs {
     float* w;
     uint16_t* x;       // parts of float32 rows
     uint16_t* h;       // parts of the weighted SwiGLU rows
+    float* sums;       // partial sums of the down step
+    int* arrived;      // their counters
 };
 // Whether the shape is within the few-token layer's limits.
 bool few_tokens_fits(const moe_shape& s);

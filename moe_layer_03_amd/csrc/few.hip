@@ -49,6 +49,7 @@ constexpr int gate_up_waves(int NP, bool MX, int MT) {
 constexpr int kRouteNW = 16;
 constexpr int kRouteGroups = 2;                        // 32-h groups of a wave in flight together
 constexpr int kMaxSlices = 16;
+constexpr int kMaxParts = 8;
 
 typedef double doublex4 __attribute__((ext_vector_type(4)));
 
@@ -65,6 +66,8 @@ struct FewArgs {
     int32_t* idx;              // [T][K]
     float* w;                  // [T][K]
     float* out;                // [T][H]
+    float* sums;               // [H / 16][parts][T][16] partial sums of the down step
+    int* arrived;              // [H / 16] workgroups that have written theirs; cleared by the route step
     int S, T, H, E, K, I, e_begin, E_loc;
 };
 
@@ -91,7 +94,8 @@ template <> __device__ __forceinline__ double widen<float>(float v) { return v; 
 template <typename XT, int NPX, bool F16>
 __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __restrict__ x, const XT* __restrict__ w,
                                                                   int T, int H, int E, double* __restrict__ part,
-                                                                  uint16_t* __restrict__ xp, int64_t xp_part) {
+                                                                  uint16_t* __restrict__ xp, int64_t xp_part,
+                                                                  int* __restrict__ arrived) {
     __shared__ double s_red[kRouteNW][4][kWave];
     constexpr int V = 16 / sizeof(XT);                 // elements of a 16-byte load
     typedef XT vec __attribute__((ext_vector_type(V)));
@@ -101,6 +105,8 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
     const int t = blockIdx.y * kRowTile + r, e = blockIdx.x * kRowTile + r;
     const int groups = H / 32, step = gridDim.z * kRouteNW;
     const int g0 = blockIdx.z * kRouteNW + wave;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int i = threadIdx.x; i < H / kRowTile; i += kRouteNW * 64) arrived[i] = 0;
     doublex4 acc = {0.0, 0.0, 0.0, 0.0};
     for (int gb = g0; gb < groups; gb += kRouteGroups * step) {
         XT wv[kRouteGroups][8];
@@ -463,96 +469,306 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
 
 // ---- down and combine -----------------------------------------------------------------
 
-// Steps wave, wave + kNW, ... of the reduction over every chosen expert's I.
-template <int NP, bool MX, int MT>
+// The rows a_{t,j} grouped for the down product: pairs (t, j) with a local expert,
+// ordered by expert; a segment is up to RV of one expert's pairs.
+struct Segments {
+    int16_t* order;    // [T K] pairs t K + j
+    int16_t* start;    // [T K] first pair of a segment in order
+    int16_t* expert;   // [T K] its local expert
+    int8_t* rows;      // [T K] its pairs
+    int* first;        // [E_loc] first place of an expert's pairs
+    uint32_t* tokens;  // [E_loc] bit t: token t chose the expert
+    int* count;        // segments
+};
+
+struct SegmentSizes {
+    size_t order, start, expert, first, tokens, count, rows, total;
+};
+
+__host__ __device__ inline SegmentSizes segment_sizes(int T, int K, int E_loc) {
+    const size_t pairs = static_cast<size_t>(T) * K, E = static_cast<size_t>(E_loc);
+    SegmentSizes z;
+    z.first = 0;
+    z.tokens = z.first + 4 * E;
+    z.count = z.tokens + 4 * E;
+    z.order = z.count + 4;
+    z.start = z.order + 2 * pairs;
+    z.expert = z.start + 2 * pairs;
+    z.rows = z.expert + 2 * pairs;
+    z.total = (z.rows + pairs + 15) & ~size_t(15);
+    return z;
+}
+
+__device__ __forceinline__ Segments carve_segments(char* base, const FewArgs& p) {
+    const SegmentSizes z = segment_sizes(p.T, p.K, p.E_loc);
+    Segments s;
+    s.order = reinterpret_cast<int16_t*>(base + z.order);
+    s.start = reinterpret_cast<int16_t*>(base + z.start);
+    s.expert = reinterpret_cast<int16_t*>(base + z.expert);
+    s.rows = reinterpret_cast<int8_t*>(base + z.rows);
+    s.first = reinterpret_cast<int*>(base + z.first);
+    s.tokens = reinterpret_cast<uint32_t*>(base + z.tokens);
+    s.count = reinterpret_cast<int*>(base + z.count);
+    return s;
+}
+
+// Every thread of the workgroup takes part.  An expert's pairs are in order of
+// their tokens (at most 32, a bit each), so every workgroup builds the same list.
+__device__ __forceinline__ void build_segments(const Segments& s, const FewArgs& p, int RV) {
+    const int tid = threadIdx.x, n = blockDim.x, pairs = p.T * p.K;
+    for (int i = tid; i < p.E_loc; i += n) s.tokens[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += n) {
+        const int e = p.idx[i] - p.e_begin;
+        if (e >= 0 && e < p.E_loc) atomicOr(&s.tokens[e], 1u << (i / p.K));
+    }
+    __syncthreads();
+    if (tid < kWave) {
+        int run = 0, segs = 0;                         // pairs and segments of the experts before
+        for (int b = 0; b < p.E_loc; b += kWave) {
+            const int e = b + tid;
+            const int c = e < p.E_loc ? __popc(s.tokens[e]) : 0, g = (c + RV - 1) / RV;
+            int ic = c, ig = g;
+#pragma unroll
+            for (int off = 1; off < kWave; off <<= 1) {
+                const int oc = __shfl_up(ic, off, kWave), og = __shfl_up(ig, off, kWave);
+                if (tid >= off) {
+                    ic += oc;
+                    ig += og;
+                }
+            }
+            const int f = run + ic - c;
+            if (e < p.E_loc) s.first[e] = f;
+            for (int q = 0; q < g; ++q) {
+                const int at = segs + ig - g + q;
+                s.start[at] = static_cast<int16_t>(f + q * RV);
+                s.expert[at] = static_cast<int16_t>(e);
+                s.rows[at] = static_cast<int8_t>(min(RV, c - q * RV));
+            }
+            run += __shfl(ic, kWave - 1, kWave);
+            segs += __shfl(ig, kWave - 1, kWave);
+        }
+        if (tid == 0) *s.count = segs;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += n) {
+        const int e = p.idx[i] - p.e_begin;
+        if (e >= 0 && e < p.E_loc)
+            s.order[s.first[e] + __popc(s.tokens[e] & ((1u << (i / p.K)) - 1u))] = static_cast<int16_t>(i);
+    }
+    __syncthreads();
+}
+
+// How a segment's rows and their parts share the RT * 16 MFMA rows: part and row
+// of MFMA row r of tile m.  Stacking the parts costs one A load per tile where
+// separate products would cost one per part, and loads are what a step is made of.
+template <int NP, int RT> struct RowMap;
+template <> struct RowMap<2, 1> {                      // 8 rows: part 0 in MFMA rows 0-7, part 1 in 8-15
+    static constexpr int RV = 8;
+    __device__ static int part(int, int r) { return r >> 3; }
+    __device__ static int row(int, int r) { return r & 7; }
+};
+template <> struct RowMap<2, 2> {                      // 16 rows, a tile per part
+    static constexpr int RV = 16;
+    __device__ static int part(int m, int) { return m; }
+    __device__ static int row(int, int r) { return r; }
+};
+template <> struct RowMap<3, 1> {                      // 4 rows, parts in groups of four MFMA rows
+    static constexpr int RV = 4;
+    __device__ static int part(int, int r) { return r >> 2; }
+    __device__ static int row(int, int r) { return r & 3; }
+};
+template <> struct RowMap<3, 2> {                      // 8 rows: parts 0 and 1 in tile 0, part 2 in tile 1
+    static constexpr int RV = 8;
+    __device__ static int part(int m, int r) { return m * 2 + (r >> 3); }
+    __device__ static int row(int, int r) { return r & 7; }
+};
+
+// The segment rows' sums from the accumulators: register v of this lane, valid in
+// the lanes of the first RV MFMA rows (row 4 (lane / 16) + v, column lane % 16).
+template <int NP, int RT, typename AccT>
+__device__ __forceinline__ float joined(const AccT& acc, int v) {
+    if constexpr (NP == 2 && RT == 1) {
+        return acc.v[0][0][0][v] + __shfl_xor(acc.v[0][0][0][v], 32, kWave) * (1.0f / kLoScale);
+    } else if constexpr (NP == 2) {
+        return acc.v[0][0][0][v] + acc.v[0][1][0][v] * (1.0f / kLoScale);
+    } else if constexpr (RT == 1) {
+        const float x = acc.v[0][0][0][v];
+        return (x + __shfl(x, (threadIdx.x + 16) & 63, kWave)) + __shfl(x, (threadIdx.x + 32) & 63, kWave);
+    } else {
+        return (acc.v[0][0][0][v] + __shfl_xor(acc.v[0][0][0][v], 32, kWave)) + acc.v[0][1][0][v];
+    }
+}
+
+// The loads of consecutive steps: the I of a segment, then the next segment's.
+template <int NP, bool MX, int RT>
 struct DownCursor {
     const FewArgs* p;
-    const Tables* tb;
-    const uint8_t* b;          // this lane's bytes of expert 0's step 0
-    const uint8_t* sc;         // this lane's scale byte of expert 0's step 0
+    const Segments* sg;
+    bool whole;                // one row per token throughout: every expert's segment has the tokens as its rows
+    const uint8_t* b0;         // this lane's bytes of expert 0's step 0
+    const uint8_t* sc0;        // this lane's scale byte of expert 0's step 0
     int64_t b_expert, sc_expert;   // bytes per expert
     __amdgpu_buffer_rsrc_t rows;
     uint32_t part_bytes;
-    int nk;                    // steps per expert
-    int a, ks;                 // next step
+    int nk, seg, ks;           // steps per segment; the next step
+    const uint8_t* b;
+    const uint8_t* sc;
+    uint32_t off[RT];
 
-    __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 1>& s) {
+    __device__ __forceinline__ void enter() {
+        typedef RowMap<NP, RT> Map;
         const int lane = threadIdx.x & (kWave - 1);
-        const int e = __builtin_amdgcn_readfirstlane(tb->act[a]);
-        s.b[0] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(b + e * b_expert + static_cast<int64_t>(ks) * kStepBytes));
-        if constexpr (MX) s.sc[0] = sc[e * sc_expert + ks * 2];
+        const int e = __builtin_amdgcn_readfirstlane(sg->expert[seg]);
+        const int first = __builtin_amdgcn_readfirstlane(sg->start[seg]);
+        const int n = __builtin_amdgcn_readfirstlane(sg->rows[seg]);
+        b = b0 + e * b_expert + static_cast<int64_t>(ks) * kStepBytes;
+        if constexpr (MX) sc = sc0 + e * sc_expert + ks * 2;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = m * kRowTile + (lane & 15);
-            const int j = t < p->T ? tb->slot[a * p->T + t] : -1;
-            const uint32_t off =
-                j >= 0 ? (static_cast<uint32_t>((t * p->K + j) * p->I) + (ks * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2
-                       : kOutOfRange;
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-#pragma unroll
-                for (int l = 0; l < (MX ? 2 : 1); ++l)
-                    s.a[m][q][l] = __builtin_bit_cast(
-                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off + q * part_bytes + l * 16, 0, 0));
+        for (int m = 0; m < RT; ++m) {
+            const int part = Map::part(m, lane & 15), row = Map::row(m, lane & 15);
+            int pair = -1;
+            if (whole) {
+                for (int i = 0; i < n; ++i) {          // uniform; at most a row per token
+                    const int q = sg->order[first + i];
+                    if (q / p->K == row) pair = q;
+                }
+            } else if (row < n) {
+                pair = sg->order[first + row];
+            }
+            off[m] = pair >= 0 && part < NP ? part * part_bytes + (static_cast<uint32_t>(pair) * p->I +
+                                                                   (ks * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2
+                                            : kOutOfRange;
         }
-        ks += kNW;
-        while (ks >= nk) {
-            ks -= nk;
-            ++a;
+    }
+    __device__ __forceinline__ void load(StepRegs<1, MX, RT, 1>& s) {
+        s.b[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
+        if constexpr (MX) s.sc[0] = sc[0];
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+#pragma unroll
+            for (int l = 0; l < (MX ? 2 : 1); ++l)
+                s.a[m][0][l] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off[m] + l * 16, 0, 0));
+        b += kStepBytes;
+        if constexpr (MX) sc += 2;
+#pragma unroll
+        for (int m = 0; m < RT; ++m) off[m] += MX ? 128 : 64;
+        if (++ks == nk) {                              // uniform
+            ks = 0;
+            if (++seg < *sg->count) enter();
         }
     }
 };
 
-template <int NP, bool F16, bool MX, int MT>
-__global__ __launch_bounds__(kNW * 64, 1) void few_down_kernel(FewArgs p) {
-    // loads in flight: 1 KiB of weights per wave and step, one workgroup to a CU
-    constexpr int D = MX ? (MT == 1 ? 6 : 4) : (MT == 1 ? 8 : 6);
+// A workgroup owns 16 output columns and part blockIdx.y of the steps, each wave a
+// contiguous run of them.  A wave adds its rows' sums to its own [T][16] in LDS
+// where the segment ends (or once at its end, where MFMA rows are tokens all
+// along); the waves' are added in order.  With more than one part, the partial
+// sums go to memory, and the workgroup that finds all others done adds them, in
+// order of the parts, whatever the order of arrival.
+template <int NP, bool F16, bool MX, int RT>
+__global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
+    typedef RowMap<NP, RT> Map;
+    constexpr int D = MX ? (RT == 1 ? 6 : 4) : (RT == 1 ? 8 : 6);   // steps in flight, 1 KiB of weights each
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][4][kWave];
-    const Tables tb = carve_tables(smem, p);
+    float* s_out = reinterpret_cast<float*>(smem);     // [kNW][T][16]
+    const Segments sg = carve_segments(smem + kNW * p.T * 64, p);
+    __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int unit = blockIdx.x, parts = gridDim.y;
 
-    for (int i = tid; i < p.T * p.K; i += kNW * 64) tb.idx[i] = p.idx[i];
-    __syncthreads();
-    build_tables(tb, p);
+    for (int i = tid; i < kNW * p.T * 16; i += kNW * 64) s_out[i] = 0.0f;
+    const bool whole = p.T <= Map::RV;
+    build_segments(sg, p, Map::RV);
 
-    const int unit = blockIdx.x;                       // 16 output columns
     const int n64 = unit >> 2, half = (unit >> 1) & 1, c0 = (unit & 1) * 16;
-    DownCursor<NP, MX, MT> cur;
+    DownCursor<NP, MX, RT> cur;
     cur.p = &p;
-    cur.tb = &tb;
+    cur.sg = &sg;
+    cur.whole = whole;
     cur.nk = p.I / (MX ? 64 : 32);
-    const int total = __builtin_amdgcn_readfirstlane(*tb.count) * cur.nk;
+    const int segs = __builtin_amdgcn_readfirstlane(*sg.count);
     cur.b_expert = static_cast<int64_t>(p.H >> 6) * cur.nk * kStepBytes;
-    cur.b = p.dn + static_cast<int64_t>(n64) * cur.nk * kStepBytes + step_lane_offset<MX>(half, c0);
+    cur.b0 = p.dn + static_cast<int64_t>(n64) * cur.nk * kStepBytes + step_lane_offset<MX>(half, c0);
     if constexpr (MX) {
         cur.sc_expert = static_cast<int64_t>(p.H) * (p.I / 32);
-        cur.sc = p.dn_scales + static_cast<int64_t>(unit * kRowTile + (lane & 15)) * (p.I / 32) + (lane >> 5);
+        cur.sc0 = p.dn_scales + static_cast<int64_t>(unit * kRowTile + (lane & 15)) * (p.I / 32) + (lane >> 5);
     }
     cur.rows = __builtin_amdgcn_make_buffer_rsrc(p.h, 0, kBufferRange, kBufferFlags);
     cur.part_bytes = static_cast<uint32_t>(static_cast<int64_t>(p.T) * p.K * p.I * 2);
-    cur.a = wave / cur.nk;
-    cur.ks = wave - cur.a * cur.nk;
-    Acc<NP, F16, MX, MT, 1> acc;
+    // this wave's steps: an even share of all
+    const int64_t total = static_cast<int64_t>(segs) * cur.nk, shares = static_cast<int64_t>(parts) * kNW;
+    const int64_t share = blockIdx.y * kNW + wave;
+    const int64_t lo = total * share / shares, hi = total * (share + 1) / shares;
+    const int steps = static_cast<int>(hi - lo);
+    cur.seg = static_cast<int>(lo / cur.nk);
+    cur.ks = static_cast<int>(lo - static_cast<int64_t>(cur.seg) * cur.nk);
+    if (steps > 0) cur.enter();
+    int seg = cur.seg, ks = cur.ks;                    // the next step to be added
+
+    Acc<1, F16, MX, RT, 1> acc;
     acc.clear();
-    const int steps = total > wave ? (total - wave + kNW - 1) / kNW : 0;
-    StepRegs<NP, MX, MT, 1> ring[D];
+    float* mine = s_out + wave * p.T * 16;
+    auto flush = [&]() {                               // rows of segment seg
+        const int n = whole ? p.T : __builtin_amdgcn_readfirstlane(sg.rows[seg]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float x = joined<NP, RT>(acc, v);
+            const int r = (lane >> 4) * 4 + v;
+            if (r < n) {
+                const int t = whole ? r : sg.order[sg.start[seg] + r] / p.K;
+                mine[t * 16 + (lane & 15)] += x;
+            }
+        }
+        acc.clear();
+    };
+    StepRegs<1, MX, RT, 1> ring[D];
     start_steps(steps, cur, ring);
-    run_steps(steps, cur, ring, acc);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) s_red[wave][m][v][lane] = acc.value(m, 0, v);
+    run_steps(steps, cur, ring, acc, [&]() {           // after every step
+        if (++ks == cur.nk) {                          // uniform
+            if (!whole) flush();
+            ks = 0;
+            ++seg;
+        }
+    });
+    if (steps > 0 && (whole || ks != 0)) flush();
     __syncthreads();
-    if (tid < MT * 256) {
-        const int m = tid >> 8, v = (tid >> 6) & 3;
-        const int t = m * kRowTile + (lane >> 4) * 4 + v;
+    const int cells = p.T * 16;
+    if (parts == 1) {
+        for (int i = tid; i < cells; i += kNW * 64) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kNW; ++q) s += s_out[q * cells + i];
+            p.out[static_cast<int64_t>(i >> 4) * p.H + unit * kRowTile + (i & 15)] = s;
+        }
+        return;
+    }
+    // Partial sums and the counter move by agent-scope relaxed atomics, which act
+    // where all workgroups see them, past the caches that XCDs do not share.  A
+    // thread's stores are complete once its vector-memory counter is zero, so
+    // with that wait and the barrier before the count, the workgroup that counts
+    // last reads complete sums.  (A release or acquire at agent scope would write
+    // back and invalidate a whole L2 per workgroup: 8 to 12 us here.)
+    for (int i = tid; i < cells; i += kNW * 64) {
         float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kNW; ++q) s += s_red[q][m][v][lane];
-        if (t < p.T) p.out[static_cast<int64_t>(t) * p.H + unit * kRowTile + (lane & 15)] = s;
+        for (int q = 0; q < kNW; ++q) s += s_out[q * cells + i];
+        __hip_atomic_store(&p.sums[(static_cast<int64_t>(unit) * parts + blockIdx.y) * cells + i], s, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+    wait_vmcnt<0>();                                   // this thread's stores are complete
+    __syncthreads();
+    if (tid == 0)
+        s_last = __hip_atomic_fetch_add(&p.arrived[unit], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    __syncthreads();
+    if (!s_last) return;
+    for (int i = tid; i < cells; i += kNW * 64) {
+        float s = 0.0f;
+        for (int q = 0; q < parts; ++q)
+            s += __hip_atomic_load(&p.sums[(static_cast<int64_t>(unit) * parts + q) * cells + i], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        p.out[static_cast<int64_t>(i >> 4) * p.H + unit * kRowTile + (i & 15)] = s;
     }
 }
 
@@ -573,27 +789,51 @@ int route_slices(int T, int H) {
 int x_parts(int x_dtype, bool mx) { return x_dtype == MOE_BF16 ? 0 : (mx ? 3 : 2); }
 int h_parts(bool mx) { return mx ? 3 : 2; }
 
+// Workgroups that share the down step's reduction for 16 columns: up to two
+// workgroups on every CU, as long as a wave keeps kPartSteps steps of what T
+// tokens are expected to choose (a wave has 4 to 8 in flight); below that the
+// handing over of partial sums (about 3 us) costs more than it saves.
+constexpr int kPartSteps = 8;
+int down_parts(const moe_shape& s, bool mx) {
+    const int E_loc = s.e_end - s.e_begin;
+    double none = 1.0;                                 // an expert that no token chooses
+    for (int t = 0; t < s.T; ++t) none *= 1.0 - static_cast<double>(s.K) / s.E;
+    const double steps = E_loc * (1.0 - none) * (s.I / (mx ? 64 : 32)) / kNW;
+    int n = 512 / (s.H / kRowTile);
+    if (n > steps / kPartSteps) n = static_cast<int>(steps / kPartSteps);
+    return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : n);
+}
+
+size_t down_lds(const moe_shape& s) {
+    return static_cast<size_t>(kNW) * s.T * 64 + segment_sizes(s.T, s.K, s.e_end - s.e_begin).total;
+}
+
+template <int NP, bool F16, bool MX>
+int launch_down(const FewArgs& p, int parts, size_t lds, hipStream_t st) {
+    const dim3 g(p.H / kRowTile, parts), block(kNW * 64);
+    // one tile of MFMA rows while the tokens, or the rows an evenly routed expert gets, fit its segments about twice over
+    constexpr int RV = RowMap<NP, 1>::RV;
+    const bool narrow = p.T <= RV || (p.T > RowMap<NP, 2>::RV && p.T * p.K <= p.E * RV / 2);
+    if (narrow) hipLaunchKernelGGL((few_down_kernel<NP, F16, MX, 1>), g, block, lds, st, p);
+    else hipLaunchKernelGGL((few_down_kernel<NP, F16, MX, 2>), g, block, lds, st, p);
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
 template <int MT>
-int launch_products(const FewArgs& p, int x_dtype, bool mx, hipStream_t st) {
+int launch_gate_up(const FewArgs& p, int x_dtype, bool mx, hipStream_t st) {
     const int64_t experts = p.T * p.K < p.E_loc ? p.T * p.K : p.E_loc;
     const int64_t most = experts * (p.I / kRowTile);
-    const dim3 g(static_cast<unsigned>(most < 512 ? most : 512)), block(kNW * 64), d(p.H / kRowTile);
+    const dim3 g(static_cast<unsigned>(most < 512 ? most : 512)), block(kNW * 64);
     const size_t lds = table_sizes(p.T, p.K, p.E_loc).total;
-    if (mx) {
-        if (x_dtype == MOE_BF16)
-            hipLaunchKernelGGL((few_gate_up_kernel<1, false, true, MT, 3, false>), g, block, lds, st, p);
-        else
-            hipLaunchKernelGGL((few_gate_up_kernel<3, false, true, MT, 3, false>), g, block, lds, st, p);
-        MOE_CHECK_LAUNCH();
-        hipLaunchKernelGGL((few_down_kernel<3, false, true, MT>), d, block, lds, st, p);
-    } else {
-        if (x_dtype == MOE_BF16)
-            hipLaunchKernelGGL((few_gate_up_kernel<1, false, false, MT, 2, true>), g, block, lds, st, p);
-        else
-            hipLaunchKernelGGL((few_gate_up_kernel<2, true, false, MT, 2, true>), g, block, lds, st, p);
-        MOE_CHECK_LAUNCH();
-        hipLaunchKernelGGL((few_down_kernel<2, true, false, MT>), d, block, lds, st, p);
-    }
+    if (mx && x_dtype == MOE_BF16)
+        hipLaunchKernelGGL((few_gate_up_kernel<1, false, true, MT, 3, false>), g, block, lds, st, p);
+    else if (mx)
+        hipLaunchKernelGGL((few_gate_up_kernel<3, false, true, MT, 3, false>), g, block, lds, st, p);
+    else if (x_dtype == MOE_BF16)
+        hipLaunchKernelGGL((few_gate_up_kernel<1, false, false, MT, 2, true>), g, block, lds, st, p);
+    else
+        hipLaunchKernelGGL((few_gate_up_kernel<2, true, false, MT, 2, true>), g, block, lds, st, p);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }
@@ -602,10 +842,11 @@ inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
 
+static_assert(MOE_FEW_TOKENS_MAX <= 32, "a bit per token");
+
 bool few_tokens_fits(const moe_shape& s) {
     const int64_t rows = static_cast<int64_t>(s.T) * s.K * s.I * 2 * 3, x = static_cast<int64_t>(s.T) * s.H * 2 * 3;
-    const size_t lds = table_sizes(s.T, s.K, s.e_end - s.e_begin).total;
-    return s.T <= MOE_FEW_TOKENS_MAX && rows <= kBufferRange && x <= kBufferRange && lds <= 64 * 1024;
+    return s.T <= MOE_FEW_TOKENS_MAX && rows <= kBufferRange && x <= kBufferRange;
 }
 
 size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w) {
@@ -623,6 +864,8 @@ size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w) {
     z.w = reinterpret_cast<float*>(take(pairs * 4));
     z.x = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * s.T * s.H * 2));
     z.h = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * pairs * s.I * 2));
+    z.sums = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxParts) * s.T * s.H * 4));
+    z.arrived = reinterpret_cast<int*>(take(static_cast<size_t>(s.H) / kRowTile * 4));
     if (w != nullptr) *w = z;
     return off;
 }
@@ -646,6 +889,8 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     p.idx = idx ? idx : z.idx;
     p.w = tw ? tw : z.w;
     p.out = out;
+    p.sums = z.sums;
+    p.arrived = z.arrived;
     p.a = x_dtype == MOE_BF16 ? static_cast<const uint16_t*>(x) : z.x;
     p.a_part = static_cast<int64_t>(s.T) * s.H;
     const uint8_t* b = static_cast<const uint8_t*>(packed);
@@ -660,15 +905,18 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     const dim3 g((s.E + kRowTile - 1) / kRowTile, (s.T + kRowTile - 1) / kRowTile, p.S), block(kRouteNW * 64);
     if (x_dtype == MOE_BF16)
         hipLaunchKernelGGL((few_route_kernel<uint16_t, 0, false>), g, block, 0, st, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
     else if (mx)
         hipLaunchKernelGGL((few_route_kernel<float, 3, false>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
     else
         hipLaunchKernelGGL((few_route_kernel<float, 2, true>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
     MOE_CHECK_LAUNCH();
-    return s.T <= kRowTile ? launch_products<1>(p, x_dtype, mx, st) : launch_products<2>(p, x_dtype, mx, st);
+    MOE_TRY(s.T <= kRowTile ? launch_gate_up<1>(p, x_dtype, mx, st) : launch_gate_up<2>(p, x_dtype, mx, st));
+    const int parts = down_parts(s, mx);
+    return mx ? launch_down<3, false, true>(p, parts, down_lds(s), st)
+              : launch_down<2, true, false>(p, parts, down_lds(s), st);
 }
 
 }  // namespace moe

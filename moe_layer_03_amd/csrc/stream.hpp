@@ -127,7 +127,7 @@ __device__ __forceinline__ int step_lane_offset(int half, int c0) {
 
 // A product of n steps whose first D loads are already on their way: start_steps
 // issues them (cur.load(regs) issues the loads of cur's next step), run_steps adds
-// all n steps, loading D ahead.  Whole turns of the ring have no branch inside, so
+// all n steps, loading D ahead (after() follows each).  Whole turns of the ring have no branch inside, so
 // the wait before a step leaves the younger D - 1 steps' loads in flight; only
 // the last turns test whether a step is there.
 template <int D, int NP, bool MX, int MT, int CT, typename Cursor>
@@ -137,15 +137,16 @@ __device__ __forceinline__ void start_steps(int n, Cursor& cur, StepRegs<NP, MX,
         if (j < n) cur.load(ring[j]);                  // uniform
 }
 
-template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
+template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor, typename After>
 __device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D],
-                                          Acc<NP, F16, MX, MT, CT>& acc) {
+                                          Acc<NP, F16, MX, MT, CT>& acc, After&& after) {
     int i = 0;
     for (; i + 2 * D <= n; i += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             acc.add(ring[j]);
             cur.load(ring[j]);
+            after();
         }
     }
 #pragma unroll
@@ -153,7 +154,14 @@ __device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, M
         if (i + j < n) {                               // uniform
             acc.add(ring[j % D]);
             if (j < D && i + j + D < n) cur.load(ring[j % D]);
+            after();
         }
+}
+
+template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
+__device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D],
+                                          Acc<NP, F16, MX, MT, CT>& acc) {
+    run_steps(n, cur, ring, acc, [] {});
 }
 
 }  // namespace

@@ -210,3 +210,22 @@ def test_captured_and_replayed():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("dtype,mx", [("bf16", False), ("f32", False), ("bf16", True), ("f32", True)])
+@pytest.mark.parametrize("T", [9, 17, 32])
+def test_crowded_experts(dtype, mx, T):
+    """Experts that more tokens choose than an MFMA tile has rows, beside experts with one token: several row
+    segments of one expert, shared out over workgroups."""
+    s = B.Shape(T, 256, 96, 4, 256, 0, 90)
+    d = make(s, dtype, mx, seed=40 + T)
+    d["bias"] = torch.zeros(96, device="cuda")
+    d["bias"][torch.tensor([3, 64, 91])] = torch.tensor([2.0, 1.2, 1.5], device="cuda")
+    got, idx, w = call(s, d, pack(s, d, dtype, mx), mx)
+    check(s, d, got, idx, w)
+
+
+def test_every_token_every_expert():
+    """32 tokens that all choose the same 8 experts."""
+    run(B.Shape(32, 320, 8, 8, 192, 0, 8), seed=44)
+    run(B.Shape(32, 256, 8, 8, 512, 0, 8), mx=True, seed=45)
