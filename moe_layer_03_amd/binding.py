@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -223,6 +224,22 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream or None
+
+
+def _stream_on(device: torch.device, stream) -> Optional[int]:
+    """The given stream, or the device's current one.  The device has to be the current one, as its kernels are
+    launched there; moving a call to another device is the caller's ``torch.cuda.device``."""
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if stream is not None:
+        return stream.cuda_stream or None
+    return torch._C._cuda_getCurrentRawStream(device.index) or None
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, is on {t.device}")
 
 
 def operand_dtype(x_dtype: torch.dtype) -> torch.dtype:
@@ -555,23 +572,36 @@ def moe_layer_few_tokens_workspace_bytes_mxfp8(s: Shape) -> int:
     return int(load().moe_layer_few_tokens_workspace_bytes_mxfp8(ctypes.byref(s.c())))
 
 
+@functools.lru_cache(maxsize=256)
+def _few_tokens_of(mx: bool, s: Shape):
+    """(C shape, workspace bytes, packed weight bytes) of a shape."""
+    c = s.c()
+    lib = load()
+    if mx:
+        return c, int(lib.moe_layer_few_tokens_workspace_bytes_mxfp8(c)), int(lib.moe_packed_weight_bytes_mxfp8(c))
+    return c, int(lib.moe_layer_few_tokens_workspace_bytes(c)), int(lib.moe_packed_weight_bytes(c))
+
+
 def _layer_few_tokens(mx: bool, s: Shape, x, w_router, packed, bias, out, ws, topk_idx, topk_w, stream):
-    name = "moe_layer_few_tokens_mxfp8" if mx else "moe_layer_few_tokens"
-    need = (moe_layer_few_tokens_workspace_bytes_mxfp8 if mx else moe_layer_few_tokens_workspace_bytes)(s)
-    weights = (moe_packed_weight_bytes_mxfp8 if mx else moe_packed_weight_bytes)(s)
+    c, need, weights = _few_tokens_of(mx, s)
+    dev = x.device
     if packed.numel() < weights:
         raise ValueError(f"packed must hold {weights} bytes, got {packed.numel()}")
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, x.device)
+        out = _empty((s.T, s.H), torch.float32, dev)
     if ws is None:
-        ws = _empty(max(need, 16), torch.uint8, x.device)
-    st = getattr(load(), name)(
-        ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x), _ptr(w_router, None, s.H * s.E, "w_router"),
-        _dt(w_router), _ptr(bias, torch.float32, s.E, "bias"), _ptr(packed, torch.uint8, None, "packed"),
-        _ptr(out, torch.float32, s.T * s.H, "out"), _ptr(topk_idx, torch.int32, s.T * s.K, "topk_idx"),
-        _ptr(topk_w, torch.float32, s.T * s.K, "topk_w"), _ptr(ws, torch.uint8, None, "ws"), ws.numel(),
-        _stream(stream))
-    _check(name, st)
+        ws = _empty(max(need, 16), torch.uint8, dev)
+    pairs = s.T * s.K
+    args = (c, _ptr(x, None, s.T * s.H, "x"), _dt(x), _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
+            _ptr(bias, torch.float32, s.E, "bias"), _ptr(packed, torch.uint8, None, "packed"),
+            _ptr(out, torch.float32, s.T * s.H, "out"), _ptr(topk_idx, torch.int32, pairs, "topk_idx"),
+            _ptr(topk_w, torch.float32, pairs, "topk_w"), _ptr(ws, torch.uint8, None, "ws"), ws.numel())
+    _same_device(dev, w_router=w_router, bias=bias, packed=packed, out=out, topk_idx=topk_idx, topk_w=topk_w, ws=ws)
+    lib = load()
+    if mx:
+        _check("moe_layer_few_tokens_mxfp8", lib.moe_layer_few_tokens_mxfp8(*args, _stream_on(dev, stream)))
+    else:
+        _check("moe_layer_few_tokens", lib.moe_layer_few_tokens(*args, _stream_on(dev, stream)))
     return out
 
 
@@ -593,8 +623,15 @@ def moe_layer_few_tokens_mxfp8(s: Shape, x: torch.Tensor, w_router: torch.Tensor
 # dense products with a fused epilogue
 # ---------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=256)
+def _dense_of(d: DenseShape):
+    """(C shape, packed weight bytes) of a shape."""
+    c = d.c()
+    return c, int(load().moe_packed_dense_bytes(c))
+
+
 def moe_packed_dense_bytes(d: DenseShape) -> int:
-    return int(load().moe_packed_dense_bytes(ctypes.byref(d.c())))
+    return _dense_of(d)[1]
 
 
 def moe_pack_dense(d: DenseShape, w: torch.Tensor, w_up: Optional[torch.Tensor] = None,
@@ -606,8 +643,10 @@ def moe_pack_dense(d: DenseShape, w: torch.Tensor, w_up: Optional[torch.Tensor] 
     if packed.dtype != torch.uint8 or packed.numel() < need:
         raise ValueError(f"packed must be a uint8 buffer of at least {need} bytes")
     n = d.N * d.K
-    st = load().moe_pack_dense(ctypes.byref(d.c()), _ptr(w, None, n, "w"), _ptr(w_up, w.dtype, n, "w_up"), _dt(w),
-                               _ptr(packed, torch.uint8, None, "packed"), _stream(stream))
+    _same_device(w.device, w_up=w_up, packed=packed)
+    args = (ctypes.byref(d.c()), _ptr(w, None, n, "w"), _ptr(w_up, w.dtype, n, "w_up"), _dt(w),
+            _ptr(packed, torch.uint8, None, "packed"))
+    st = load().moe_pack_dense(*args, _stream_on(w.device, stream))
     _check("moe_pack_dense", st)
     return packed
 
@@ -635,17 +674,19 @@ def moe_dense_gemm(d: DenseShape, a: torch.Tensor, packed: torch.Tensor, epilogu
     """act(a @ W + bias) + residual on moe_pack_dense weights (gated: MOE_EPI_SWIGLU, bias [2, N]).
 
     a [M, K], residual and c [M, N] may have any row stride; c may be residual.  c_dtype defaults to a's."""
-    need = moe_packed_dense_bytes(d)
+    shape, need = _dense_of(d)
     if packed.numel() < need:
         raise ValueError(f"packed must hold {need} bytes, got {packed.numel()}")
+    dev = a.device
     if c is None:
-        c = _empty((d.M, d.N), c_dtype or a.dtype, a.device)
+        c = _empty((d.M, d.N), c_dtype or a.dtype, dev)
     pa, lda = _rows(a, d.M, d.K, "a")
     pr, ldr = _rows(residual, d.M, d.N, "residual")
     pc, ldc = _rows(c, d.M, d.N, "c")
-    st = load().moe_dense_gemm(ctypes.byref(d.c()), pa, _dt(a), lda, _ptr(packed, torch.uint8, None, "packed"), epilogue,
-                               _ptr(bias, torch.float32, d.N * (2 if d.gated else 1), "bias"), pr,
-                               _dt(residual) if residual is not None else MOE_F32, ldr, pc, _dt(c), ldc,
-                               _stream(stream))
+    args = (shape, pa, _dt(a), lda, _ptr(packed, torch.uint8, None, "packed"), epilogue,
+            _ptr(bias, torch.float32, d.N * (2 if d.gated else 1), "bias"), pr,
+            _dt(residual) if residual is not None else MOE_F32, ldr, pc, _dt(c), ldc)
+    _same_device(dev, packed=packed, bias=bias, residual=residual, c=c)
+    st = load().moe_dense_gemm(*args, _stream_on(dev, stream))
     _check("moe_dense_gemm", st)
     return c
