@@ -112,56 +112,94 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, fl
     }
 }
 
-// ---- any alignment -----------------------------------------------------------------
+// Rows that may start at any address: 16 bytes at an element's alignment (one
+// load, the hardware takes unaligned addresses).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// The 8 elements k .. k + 7 of a row, zeros from K on.
+__device__ __forceinline__ u32x4 load_tail(const uint16_t* row, int k, int K) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k + j < K ? row[k + j] : 0u;
+    return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+}
+
+// ---- many rows, any alignment --------------------------------------------------------
 // 64 rows x one 64-column pair per workgroup of 4 waves; a wave owns 32 rows x
-// 16 columns of each half.  A goes through LDS element by element, so rows may
-// start at any address.
-constexpr int kAnyLd = 40;                             // LDS row of 32 k, padded against bank conflicts
+// 16 columns of each half.  Direct copies to LDS need aligned rows, so A goes
+// through registers, and a stage is 128 k long to have as few waits as possible:
+// the next stage's rows and weights are on their way while one is multiplied.
+constexpr int kAnyK = 128;
+constexpr int kAnyLd = kAnyK + 8;                      // LDS row, 16 of them in distinct banks
 
 template <bool F16>
 __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
-    __shared__ __attribute__((aligned(16))) uint16_t s_a[64 * kAnyLd];
+    __shared__ __attribute__((aligned(16))) uint16_t s_a[2][64 * kAnyLd];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pair = blockIdx.x, c0 = (wave & 1) * 16, r0 = (wave >> 1) * 32;
     const int row0 = blockIdx.y * 64;
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) + static_cast<int64_t>(pair) * (p.Kp / 32) * kStepBytes;
-    const int o0 = step_lane_offset<false>(0, c0), o1 = step_lane_offset<false>(1, c0);
+    const int nk32 = p.Kp / 32;
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) + static_cast<int64_t>(pair) * nk32 * kStepBytes +
+                       step_lane_offset<false>(0, c0);
     floatx4 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int lr = tid >> 2, lk = (tid & 3) * 8;       // this thread's 8 elements of a step
-    for (int k0 = 0; k0 < p.K; k0 += 32) {
-        uint16_t v[8];
+    const int lr = tid >> 2, lk = (tid & 3) * 32;      // this thread's 32 elements of a stage
+    const uint16_t* row = p.a + static_cast<int64_t>(min(row0 + lr, p.M - 1)) * p.lda;   // rows past M: dropped below
+    u32x4 ra[4], rb[4][2], nb[4][2];
+    auto load_a = [&](int k0) {
+        if (k0 + kAnyK <= p.K) {                       // uniform
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = row0 + lr, k = k0 + lk + j;
-            v[j] = row < p.M && k < p.K ? p.a[row * p.lda + k] : uint16_t(0);
+            for (int j = 0; j < 4; ++j) ra[j] = *reinterpret_cast<const u32x4_any*>(row + k0 + lk + j * 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ra[j] = load_tail(row, k0 + lk + j * 8, p.K);
         }
-        __syncthreads();                               // the last step's reads are done
+    };
+    auto load_b = [&](u32x4 (&r)[4][2], int k0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s_a[lr * kAnyLd + lk + j] = v[j];
-        __syncthreads();
-        const uint8_t* bs = b + static_cast<int64_t>(k0 / 32) * kStepBytes;
-        const u32x4 b0 = *reinterpret_cast<const u32x4*>(bs + o0), b1 = *reinterpret_cast<const u32x4*>(bs + o1);
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const u32x4 a =
-                *reinterpret_cast<const u32x4*>(&s_a[(r0 + m * 16 + (lane & 15)) * kAnyLd + (lane >> 4) * 8]);
-            acc[m][0] = mfma16(F16, a, b0, acc[m][0]);
-            acc[m][1] = mfma16(F16, a, b1, acc[m][1]);
+            for (int h = 0; h < 2; ++h)                // steps past the end: the last one again, A is zero there
+                r[q][h] = *reinterpret_cast<const u32x4*>(
+                    b + static_cast<int64_t>(min(k0 / 32 + q, nk32 - 1)) * kStepBytes + h * 1024);
+    };
+    load_a(0);
+    load_b(rb, 0);
+    int buf = 0;
+    for (int k0 = 0; k0 < p.K; k0 += kAnyK, buf ^= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4*>(&s_a[buf][lr * kAnyLd + lk + j * 8]) = ra[j];
+        lds_barrier();                                 // the other buffer is no longer read either
+        if (k0 + kAnyK < p.K) {
+            load_a(k0 + kAnyK);
+            load_b(nb, k0 + kAnyK);
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const u32x4 a = *reinterpret_cast<const u32x4*>(
+                    &s_a[buf][(r0 + m * 16 + (lane & 15)) * kAnyLd + q * 32 + (lane >> 4) * 8]);
+                acc[m][0] = mfma16(F16, a, rb[q][0], acc[m][0]);
+                acc[m][1] = mfma16(F16, a, rb[q][1], acc[m][1]);
+            }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) rb[q][h] = nb[q][h];
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = row0 + r0 + m * 16 + (lane >> 4) * 4 + i, cc = c0 + (lane & 15);
+            const int r = row0 + r0 + m * 16 + (lane >> 4) * 4 + i, cc = c0 + (lane & 15);
             if (p.gated) {
-                finish(p, row, pair * 32 + cc, acc[m][0][i], acc[m][1][i]);
+                finish(p, r, pair * 32 + cc, acc[m][0][i], acc[m][1][i]);
             } else {
-                finish(p, row, pair * 64 + cc, acc[m][0][i], 0.0f);
-                finish(p, row, pair * 64 + 32 + cc, acc[m][1][i], 0.0f);
+                finish(p, r, pair * 64 + cc, acc[m][0][i], 0.0f);
+                finish(p, r, pair * 64 + 32 + cc, acc[m][1][i], 0.0f);
             }
         }
 }
@@ -170,27 +208,36 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
 // A workgroup owns MT * 16 rows x 16 columns of CT column halves (gated: gate
 // and up, CT = 2) and its kNW waves take every kNW-th step of the reduction, so
 // the weights go straight from memory to registers, each element once per
-// MT * 16 rows.  The partial tiles are added through LDS in wave order.  Rows
-// past M and k past K (a multiple of 8) load zeros through an out-of-range
-// buffer offset.
+// MT * 16 rows.  The partial tiles are added through LDS in wave order.
 constexpr int kNW = 8;
 
-template <int MT, int CT>
+// ROWS16: rows on 16 bytes and K a multiple of 8; rows past M and k past K then
+// load zeros through an out-of-range buffer offset.  Otherwise rows past M load
+// the last row (their results are dropped), and the step that K ends in is done
+// apart, element by element.
+template <bool ROWS16, int MT, int CT>
 struct DenseCursor {
     const uint8_t* b;          // this lane's bytes of the step, first column half of the tile
-    int half;                  // bytes to the second
     __amdgpu_buffer_rsrc_t rows;
-    uint32_t off[MT];          // byte offset of this lane's k group, or out of range
+    const uint8_t* base;       // the tile's first row
+    uint32_t off[MT];          // byte offset of this lane's k group in its row, or out of range
     int k, K;                  // first k of the lane's group in this step
 
-    __device__ __forceinline__ void load(StepRegs<1, false, MT, CT>& s) {
+    __device__ __forceinline__ void load_b(StepRegs<1, false, MT, CT>& s) {
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-            s.b[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + c * half));
+            s.b[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + c * 1024));
+    }
+    __device__ __forceinline__ void load(StepRegs<1, false, MT, CT>& s) {
+        load_b(s);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            s.a[m][0][0] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, k < K ? off[m] : kOutOfRange, 0, 0));
+        for (int m = 0; m < MT; ++m) {
+            if constexpr (ROWS16)
+                s.a[m][0][0] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, k < K ? off[m] : kOutOfRange, 0, 0));
+            else
+                s.a[m][0][0] = *reinterpret_cast<const u32x4_any*>(base + off[m]);
+        }
         b += kNW * kStepBytes;
         k += kNW * 32;
 #pragma unroll
@@ -198,7 +245,7 @@ struct DenseCursor {
     }
 };
 
-template <bool F16, int MT, int CT>
+template <bool F16, bool ROWS16, int MT, int CT>
 __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel(DenseArgs p) {
     __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][CT][4][kWave];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -206,26 +253,39 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     const int unit = blockIdx.x, row0 = blockIdx.y * MT * kRowTile;
     // CT = 2: both halves of a pair; CT = 1: one half
     const int pair = CT == 2 ? unit >> 1 : unit >> 2, half = CT == 2 ? 0 : (unit >> 1) & 1, c0 = (unit & 1) * 16;
-    const int nk = (p.K + 31) / 32;
-    DenseCursor<MT, CT> cur;
+    const int nk = ROWS16 ? (p.K + 31) / 32 : p.K / 32;
+    DenseCursor<ROWS16, MT, CT> cur;
     cur.b = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<int64_t>(pair) * (p.Kp / 32) + wave) * kStepBytes +
             step_lane_offset<false>(half, c0);
-    cur.half = 1024;
-    cur.rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.a) + row0 * p.lda, 0, kBufferRange,
-                                                 kBufferFlags);
+    const uint16_t* first = p.a + row0 * p.lda;
+    cur.base = reinterpret_cast<const uint8_t*>(first);
+    cur.rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(first), 0, kBufferRange, kBufferFlags);
     cur.k = wave * 32 + (lane >> 4) * 8;
     cur.K = p.K;
     const int steps = nk > wave ? (nk - wave + kNW - 1) / kNW : 0;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int r = m * kRowTile + (lane & 15);
-        cur.off[m] = row0 + r < p.M ? static_cast<uint32_t>(r * static_cast<int>(p.lda) + cur.k) * 2 : kOutOfRange;
+        const int row = ROWS16 ? r : min(r, p.M - 1 - row0);
+        cur.off[m] = ROWS16 && row0 + r >= p.M
+                         ? kOutOfRange
+                         : static_cast<uint32_t>(row * static_cast<int>(p.lda) + cur.k) * 2;
     }
     Acc<1, F16, false, MT, CT> acc;
     acc.clear();
     StepRegs<1, false, MT, CT> ring[4];
     start_steps(steps, cur, ring);
     run_steps(steps, cur, ring, acc);
+    if (!ROWS16 && p.K % 32 != 0 && wave == nk % kNW) {   // the cursor stands at the last, short step
+        StepRegs<1, false, MT, CT> last;
+        cur.load_b(last);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = min(m * kRowTile + (lane & 15), p.M - 1 - row0);
+            last.a[m][0][0] = load_tail(first + static_cast<int64_t>(row) * p.lda, cur.k, p.K);
+        }
+        acc.add(last);
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -546,13 +606,23 @@ inline int64_t pairs_of(const moe_dense_shape& s) {
 }
 
 constexpr int kCUs = 256;
+constexpr int kStreamRows = 128;                       // most rows of the weight-streaming kernel
 
-template <bool F16, int MT, int CT>
-int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+template <bool F16, bool ROWS16, int MT, int CT>
+int launch_stream_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     const dim3 g(static_cast<unsigned>(pairs * (4 / CT)), (p.M + MT * kRowTile - 1) / (MT * kRowTile));
-    hipLaunchKernelGGL((dense_stream_kernel<F16, MT, CT>), g, dim3(kNW * 64), 0, st, p);
+    hipLaunchKernelGGL((dense_stream_kernel<F16, ROWS16, MT, CT>), g, dim3(kNW * 64), 0, st, p);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
+}
+
+template <bool F16, bool ROWS16>
+int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+    if (p.M <= 16)
+        return p.gated ? launch_stream_tiles<F16, ROWS16, 1, 2>(p, pairs, st)
+                       : launch_stream_tiles<F16, ROWS16, 1, 1>(p, pairs, st);
+    if (p.M <= 32) return launch_stream_tiles<F16, ROWS16, 2, 2>(p, pairs, st);
+    return launch_stream_tiles<F16, ROWS16, 4, 2>(p, pairs, st);
 }
 
 template <bool F16, int MW, int NW, int NA, int SL>
@@ -601,20 +671,19 @@ int launch_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
 
 template <bool F16>
 int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
-    // 16-byte loads need every row to start on 16 bytes, and a k group to end within the row
+    // direct copies to LDS and 16-byte buffer loads need every row to start on 16
+    // bytes, and a k group to end within the row
     const bool rows16 = reinterpret_cast<uintptr_t>(p.a) % 16 == 0 && p.lda % 8 == 0 && p.K % 8 == 0;
     // byte offsets within a tile of rows stay below the buffer range
     const bool near = p.lda * 2 * 256 <= kBufferRange;
+    if (near && p.M <= (rows16 ? kStreamRows : 64))
+        return rows16 ? launch_stream<F16, true>(p, pairs, st) : launch_stream<F16, false>(p, pairs, st);
     if (!rows16 || !near) {
         const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
         hipLaunchKernelGGL((dense_any_kernel<F16>), g, dim3(256), 0, st, p);
         MOE_CHECK_LAUNCH();
         return MOE_OK;
     }
-    if (p.M <= 16)
-        return p.gated ? launch_stream<F16, 1, 2>(p, pairs, st) : launch_stream<F16, 1, 1>(p, pairs, st);
-    if (p.M <= 32) return launch_stream<F16, 2, 2>(p, pairs, st);
-    if (p.M <= 512) return launch_stream<F16, 4, 2>(p, pairs, st);
     return launch_tiles<F16>(p, pairs, st);
 }
 

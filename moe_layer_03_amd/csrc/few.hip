@@ -71,14 +71,6 @@ struct FewArgs {
     int S, T, H, E, K, I, e_begin, E_loc;
 };
 
-// Barrier for LDS data; loads to registers stay in flight across it.
-__device__ __forceinline__ void lds_barrier() {
-    wait_lgkmcnt0();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // ---- route -------------------------------------------------------------------
 
 template <typename XT> __device__ __forceinline__ double widen(XT v);
@@ -161,18 +153,6 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
 
 // ---- selection ------------------------------------------------------------------
 
-// Maximum over the wave (DPP row shifts, then the four rows' results).
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x111, 0xf, 0xf, false)));
-    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x112, 0xf, 0xf, false)));
-    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x114, 0xf, 0xf, false)));
-    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x118, 0xf, 0xf, false)));
-    return max(max(static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 15)),
-                   static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 31))),
-               max(static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 47)),
-                   static_cast<uint32_t>(__builtin_amdgcn_readlane(v, 63))));
-}
-
 // The logit of (t, e): its slices' sums, then the bias.
 __device__ __forceinline__ double logit_of(const FewArgs& p, int t, int e) {
     const double* q = p.part + static_cast<int64_t>(t) * p.E + e;
@@ -183,65 +163,89 @@ __device__ __forceinline__ double logit_of(const FewArgs& p, int t, int e) {
     return v + 0.0;                                    // -0 and +0 compare equal
 }
 
-// One wave: token t's K best experts in order (larger logit first, equal ones by
-// index) and their weights, to LDS.  logits: the token's, or NULL to sum them
-// here.  A lane holds experts 64 g + lane.  A double is compared by its ordered bits, upper word first; the
-// lower word is looked at only where upper words are equal.
-template <int NE>
-__device__ __forceinline__ void select_token(const FewArgs& p, int t, const double* logits, int* s_idx, float* s_w,
-                                             double* s_val) {
-    const int lane = threadIdx.x & (kWave - 1);
-    uint32_t hi[NE], lo[NE];
-    uint32_t dead = 0u;
-#pragma unroll
-    for (int g = 0; g < NE; ++g) {
-        const int e = g * kWave + lane;
-        double v = 0.0;
-        if (e < p.E) v = logits != nullptr ? logits[e] : logit_of(p, t, e);
-        uint64_t u = __builtin_bit_cast(uint64_t, v);
-        u ^= (u >> 63) ? ~0ull : (1ull << 63);
-        hi[g] = e < p.E ? static_cast<uint32_t>(u >> 32) : 0u;
-        lo[g] = static_cast<uint32_t>(u);
-        dead |= e < p.E ? 0u : (1u << g);
-    }
-    for (int k = 0; k < p.K; ++k) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int g = 0; g < NE; ++g) m = max(m, hi[g]);
-        m = wave_max(m);
-        int many = 0;
-#pragma unroll
-        for (int g = 0; g < NE; ++g) many += __popcll(__ballot(hi[g] == m && !((dead >> g) & 1u)));
-        uint32_t m2 = 0u;
-        if (many > 1) {                                // uniform
-#pragma unroll
-            for (int g = 0; g < NE; ++g) m2 = max(m2, hi[g] == m && !((dead >> g) & 1u) ? lo[g] : 0u);
-            m2 = wave_max(m2);
+// A double's bits in the order of the numbers, and back.
+__device__ __forceinline__ uint64_t ordered(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return u ^ ((u >> 63) ? ~0ull : (1ull << 63));
+}
+__device__ __forceinline__ double unordered(uint64_t u) {
+    return __builtin_bit_cast(double, u ^ ((u >> 63) ? (1ull << 63) : ~0ull));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
+}
+
+// The better of this lane's (key, index) and the one N lanes on in its row of 16.
+template <int CTRL>
+__device__ __forceinline__ void row_best(uint64_t& key, int& index) {
+    const uint64_t k = (static_cast<uint64_t>(row_rotate<CTRL>(static_cast<uint32_t>(key >> 32))) << 32) |
+                       row_rotate<CTRL>(static_cast<uint32_t>(key));
+    const int i = static_cast<int>(row_rotate<CTRL>(static_cast<uint32_t>(index)));
+    const bool take = k > key || (k == key && i < index);
+    key = take ? k : key;
+    index = take ? i : index;
+}
+
+// Every token's K best experts in order (larger logit first, equal ones by index)
+// and their weights, to LDS (idx, w: [T K]).  Tokens are taken as many at a time
+// as `keys` (`room` of them) holds the ordered logits of, one to a row of 16
+// lanes, whose K rounds run side by side: a round scans the row's keys, finds the
+// best over the row by rotations and strikes it out.  The loops are left rolled:
+// a launch starts with a cold instruction cache, and straight code runs at the
+// rate it is fetched (unrolled rounds took 9 us for 24 tokens, these take 3).
+__device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys, int room, int* idx, float* w) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), c = lane & 15;
+    constexpr int kRows = kNW * 4;
+    const int batch = min(kRows, room / p.E);
+    for (int t0 = 0; t0 < p.T; t0 += batch) {
+        const int n = min(batch, p.T - t0);
+        for (int i = tid; i < n * p.E; i += kNW * kWave) {
+            const int t = i / p.E;
+            keys[i] = ordered(logit_of(p, t0 + t, i - t * p.E));
         }
-        int best = -1;
-#pragma unroll
-        for (int g = 0; g < NE; ++g) {
-            const uint64_t b = __ballot(hi[g] == m && !((dead >> g) & 1u) && (many == 1 || lo[g] == m2));
-            if (best < 0 && b != 0ull) best = g * kWave + __builtin_ctzll(b);
-        }
-#pragma unroll
-        for (int g = 0; g < NE; ++g)
-            if (g * kWave + lane == best) {
-                uint64_t u = (static_cast<uint64_t>(hi[g]) << 32) | lo[g];
-                u ^= (u >> 63) ? (1ull << 63) : ~0ull;
-                s_val[k] = __builtin_bit_cast(double, u);
-                hi[g] = 0u;
-                dead |= 1u << g;
+        __syncthreads();
+        const int row = tid >> 4;
+        const bool on = row < n;
+        uint64_t* mine = keys + (on ? row : 0) * p.E;
+        const int at = (t0 + row) * p.K;               // used where on
+        double top = 0.0;
+#pragma unroll 1
+        for (int k = 0; k < p.K; ++k) {
+            uint64_t key = 0;
+            int index = 0x7FFFFFFF;
+#pragma unroll 2
+            for (int e = c; e < p.E; e += 16) {
+                const uint64_t v = mine[e];
+                if (v > key || index == 0x7FFFFFFF) {
+                    key = v;
+                    index = e;
+                }
             }
-        if (lane == 0) s_idx[t * p.K + k] = best;
+            row_best<0x128>(key, index);               // row_ror:8, :4, :2, :1
+            row_best<0x124>(key, index);
+            row_best<0x122>(key, index);
+            row_best<0x121>(key, index);
+            if (on && c == 0) {
+                mine[index] = 0;
+                const double v = unordered(key);
+                if (k == 0) top = v;
+                idx[at + k] = index;
+                w[at + k] = static_cast<float>(v - top);
+            }
+            asm volatile("" ::: "memory");             // a wave's LDS operations run in order
+        }
+        if (on) {
+            for (int k = c; k < p.K; k += 16) w[at + k] = expf(w[at + k]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            float sum = 0.0f;
+            for (int k = 0; k < p.K; ++k) sum += w[at + k];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            for (int k = c; k < p.K; k += 16) w[at + k] = w[at + k] / sum;
+        }
+        __syncthreads();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const float ex = lane < p.K ? expf(static_cast<float>(s_val[lane] - s_val[0])) : 0.0f;
-    float sum = 0.0f;
-    for (int k = 0; k < p.K; ++k)
-        sum += __uint_as_float(__builtin_amdgcn_readlane(__builtin_bit_cast(int, ex), k));
-    if (lane < p.K) s_w[t * p.K + lane] = ex / sum;
 }
 
 // LDS tables of the routing, sized by the call (T K pairs, at most `amax` chosen
@@ -358,29 +362,17 @@ struct GateUpCursor {
     }
 };
 
+static_assert(kNW * 2 * 4 * kWave * 4 / 8 >= 1024, "one token's keys fit the reduction buffer");
+
 template <int NP, bool F16, bool MX, int MT, int NPH, bool F16H>
 __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_up_kernel(FewArgs p) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ __attribute__((aligned(16))) float s_red[kNW][MT][2][4][kWave];
-    __shared__ double s_val[kNW][kWave];
     const Tables tb = carve_tables(smem, p);
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // the logits of all tokens at once where s_red holds them, so that their loads are in flight together
-    double* logits = reinterpret_cast<double*>(&s_red[0][0][0][0][0]);
-    const bool together = static_cast<size_t>(p.T) * p.E * 8 <= sizeof(s_red);
-    if (together) {
-        for (int i = tid; i < p.T * p.E; i += kNW * 64) logits[i] = logit_of(p, i / p.E, i % p.E);
-        __syncthreads();
-    }
-    for (int t = wave; t < p.T; t += kNW) {
-        const double* mine = together ? logits + t * p.E : nullptr;
-        if (p.E <= 128) select_token<2>(p, t, mine, tb.idx, tb.w, s_val[wave]);
-        else if (p.E <= 256) select_token<4>(p, t, mine, tb.idx, tb.w, s_val[wave]);
-        else select_token<16>(p, t, mine, tb.idx, tb.w, s_val[wave]);
-    }
-    __syncthreads();
+    select_experts(p, reinterpret_cast<uint64_t*>(&s_red[0][0][0][0][0]), sizeof(s_red) / 8, tb.idx, tb.w);
     if (blockIdx.x == 0)
         for (int i = tid; i < p.T * p.K; i += kNW * 64) {
             p.idx[i] = tb.idx[i];

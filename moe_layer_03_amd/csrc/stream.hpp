@@ -32,6 +32,14 @@ constexpr float kLoScale = 2048.0f;                    // 2^11, the second fp16 
 constexpr int kStepBytes = 4096;                       // packed weights of a 64-column pair per step
 constexpr int kRowTile = 16;                           // rows (and columns) of an MFMA tile
 
+// Barrier for LDS data; loads to registers stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ floatx4 mfma16(bool f16, const u32x4& a, const u32x4& b, floatx4 c) {
     if (f16)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8_t, a),
