@@ -140,8 +140,9 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
     const int pair = blockIdx.x, c0 = (wave & 1) * 16, r0 = (wave >> 1) * 32;
     const int row0 = blockIdx.y * 64;
     const int nk32 = p.Kp / 32;
+    // k group lane / 16 of 8 in a 32-k step: block lane / 32, half (lane / 16) % 2
     const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) + static_cast<int64_t>(pair) * nk32 * kStepBytes +
-                       step_lane_offset<false>(0, c0);
+                       (lane >> 5) * 2048 + (((lane >> 4) & 1) * 32 + c0 + (lane & 15)) * 16;
     floatx4 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -225,23 +226,25 @@ struct DenseCursor {
 
     __device__ __forceinline__ void load_b(StepRegs<1, false, MT, CT>& s) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-            s.b[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + c * 1024));
+        for (int c = 0; c < CT; ++c) load_weights<false>(b + c * 1024, s.b[c]);
     }
     __device__ __forceinline__ void load(StepRegs<1, false, MT, CT>& s) {
         load_b(s);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if constexpr (ROWS16)
-                s.a[m][0][0] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, k < K ? off[m] : kOutOfRange, 0, 0));
-            else
-                s.a[m][0][0] = *reinterpret_cast<const u32x4_any*>(base + off[m]);
-        }
-        b += kNW * kStepBytes;
-        k += kNW * 32;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) off[m] += kNW * 64;
+            for (int l = 0; l < 2; ++l) {
+                if constexpr (ROWS16)
+                    s.a[m][0][l] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                   rows, k + l * 8 < K ? off[m] + l * 16 : kOutOfRange, 0, 0));
+                else
+                    s.a[m][0][l] = *reinterpret_cast<const u32x4_any*>(base + off[m] + l * 16);
+            }
+        b += kNW * step_bytes<false>();
+        k += kNW * 64;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) off[m] += kNW * 128;
     }
 };
 
@@ -253,14 +256,14 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     const int unit = blockIdx.x, row0 = blockIdx.y * MT * kRowTile;
     // CT = 2: both halves of a pair; CT = 1: one half
     const int pair = CT == 2 ? unit >> 1 : unit >> 2, half = CT == 2 ? 0 : (unit >> 1) & 1, c0 = (unit & 1) * 16;
-    const int nk = ROWS16 ? (p.K + 31) / 32 : p.K / 32;
+    const int nk = ROWS16 ? (p.K + 63) / 64 : p.K / 64;
     DenseCursor<ROWS16, MT, CT> cur;
-    cur.b = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<int64_t>(pair) * (p.Kp / 32) + wave) * kStepBytes +
-            step_lane_offset<false>(half, c0);
+    cur.b = reinterpret_cast<const uint8_t*>(p.b) +
+            (static_cast<int64_t>(pair) * (p.Kp / 64) + wave) * step_bytes<false>() + step_lane_offset<false>(half, c0);
     const uint16_t* first = p.a + row0 * p.lda;
     cur.base = reinterpret_cast<const uint8_t*>(first);
     cur.rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(first), 0, kBufferRange, kBufferFlags);
-    cur.k = wave * 32 + (lane >> 4) * 8;
+    cur.k = wave * 64 + (lane >> 4) * 16;
     cur.K = p.K;
     const int steps = nk > wave ? (nk - wave + kNW - 1) / kNW : 0;
 #pragma unroll
@@ -273,16 +276,18 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     }
     Acc<1, F16, false, MT, CT> acc;
     acc.clear();
-    StepRegs<1, false, MT, CT> ring[4];
+    StepRegs<1, false, MT, CT> ring[MT == 1 ? 4 : 2];
     start_steps(steps, cur, ring);
     run_steps(steps, cur, ring, acc);
-    if (!ROWS16 && p.K % 32 != 0 && wave == nk % kNW) {   // the cursor stands at the last, short step
+    if (!ROWS16 && p.K % 64 != 0 && wave == nk % kNW) {   // the cursor stands at the last, short step
         StepRegs<1, false, MT, CT> last;
         cur.load_b(last);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int row = min(m * kRowTile + (lane & 15), p.M - 1 - row0);
-            last.a[m][0][0] = load_tail(first + static_cast<int64_t>(row) * p.lda, cur.k, p.K);
+#pragma unroll
+            for (int l = 0; l < 2; ++l)
+                last.a[m][0][l] = load_tail(first + static_cast<int64_t>(row) * p.lda, cur.k + l * 8, p.K);
         }
         acc.add(last);
     }

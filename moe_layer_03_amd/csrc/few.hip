@@ -34,11 +34,11 @@ namespace {
 
 constexpr int kNW = 8;                                 // waves per workgroup of the two products
 
-// Steps a gate/up wave has in flight (2 KiB of weights each), as many as the
-// registers of four waves per SIMD hold, four at most: two workgroups on a CU
-// then have 128 KiB in flight.  Rows of many parts (float32 rows with MXFP8
-// weights) keep two steps and half the waves.
-constexpr int gate_up_step_regs(int NP, bool MX, int MT) { return 8 + (MX ? 2 : 0) + MT * NP * (MX ? 8 : 4); }
+// Steps a gate/up wave has in flight (2 KiB of weights each in MXFP8, 4 else), as
+// many as the registers of four waves per SIMD hold, four at most: two workgroups
+// on a CU then have 128 KiB or more in flight.  Rows of many parts (float32 rows
+// with MXFP8 weights) keep two steps and half the waves.
+constexpr int gate_up_step_regs(int NP, bool MX, int MT) { return (MX ? 10 : 16) + MT * NP * 8; }
 constexpr int gate_up_ring(int NP, bool MX, int MT) {
     const int n = (96 - MT * 8 * (NP == 2 ? 2 : 1)) / gate_up_step_regs(NP, MX, MT);
     return n > 4 ? 4 : (n < 2 ? 2 : n);
@@ -340,9 +340,8 @@ struct GateUpCursor {
     uint32_t part_bytes;
 
     __device__ __forceinline__ void load(StepRegs<NP, MX, MT, 2>& s) {
-        constexpr int half = MX ? 2048 : 1024;         // up columns: the other half of the pair
-        s.b[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
-        s.b[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + half));
+        load_weights<MX>(b, s.b[0]);
+        load_weights<MX>(b + (MX ? 2048 : 1024), s.b[1]);   // up columns: the other half of the pair
         if constexpr (MX) {
             s.sc[0] = sc[0];
             s.sc[1] = sc[sc_up];
@@ -350,15 +349,11 @@ struct GateUpCursor {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int q = 0; q < NP; ++q)
-#pragma unroll
-                for (int l = 0; l < (MX ? 2 : 1); ++l)
-                    s.a[m][q][l] = __builtin_bit_cast(
-                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off[m] + q * part_bytes + l * 16, 0, 0));
-        b += kNW * kStepBytes;
+            for (int q = 0; q < NP; ++q) load_row(rows, off[m] + q * part_bytes, s.a[m][q]);
+        b += kNW * step_bytes<MX>();
         if constexpr (MX) sc += kNW * 2;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) off[m] += kNW * (MX ? 128 : 64);
+        for (int m = 0; m < MT; ++m) off[m] += kNW * 128;
     }
 };
 
@@ -382,7 +377,7 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
 
     const int nb = p.I / kRowTile;                     // units per expert
     const int units = *tb.count * nb;
-    const int nk = p.H / (MX ? 64 : 32);               // steps of a unit
+    const int nk = p.H / 64;                           // steps of a unit
     const __amdgpu_buffer_rsrc_t rows =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.a), 0, kBufferRange, kBufferFlags);
     GateUpCursor<NP, MX, MT> cur;
@@ -396,7 +391,7 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
         const int pair = u >> 1, c0 = (u & 1) * 16;
         const int8_t* slot = tb.slot + a * p.T;
         const int64_t first = (static_cast<int64_t>(e) * (p.I >> 5) + pair) * nk + wave;
-        cur.b = p.gu + first * kStepBytes + step_lane_offset<MX>(0, c0);
+        cur.b = p.gu + first * step_bytes<MX>() + step_lane_offset<MX>(0, c0);
         if constexpr (MX) {
             const int64_t col = static_cast<int64_t>(e) * 2 * p.I + pair * 64 + c0 + (lane & 15);
             cur.sc = p.gu_scales + col * (p.H / 32) + wave * 2 + (lane >> 5);
@@ -405,7 +400,7 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
         for (int m = 0; m < MT; ++m) {
             const int t = m * kRowTile + (lane & 15);
             const bool on = t < p.T && slot[t < p.T ? t : 0] >= 0;
-            cur.off[m] = on ? static_cast<uint32_t>(t * p.H + (wave * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2 : kOutOfRange;
+            cur.off[m] = on ? static_cast<uint32_t>(t * p.H + (wave * 4 + (lane >> 4)) * 16) * 2 : kOutOfRange;
         }
     };
     StepRegs<NP, MX, MT, 2> ring[gate_up_ring(NP, MX, MT)];
@@ -614,7 +609,7 @@ struct DownCursor {
         const int e = __builtin_amdgcn_readfirstlane(sg->expert[seg]);
         const int first = __builtin_amdgcn_readfirstlane(sg->start[seg]);
         const int n = __builtin_amdgcn_readfirstlane(sg->rows[seg]);
-        b = b0 + e * b_expert + static_cast<int64_t>(ks) * kStepBytes;
+        b = b0 + e * b_expert + static_cast<int64_t>(ks) * step_bytes<MX>();
         if constexpr (MX) sc = sc0 + e * sc_expert + ks * 2;
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
@@ -629,22 +624,19 @@ struct DownCursor {
                 pair = sg->order[first + row];
             }
             off[m] = pair >= 0 && part < NP ? part * part_bytes + (static_cast<uint32_t>(pair) * p->I +
-                                                                   (ks * 4 + (lane >> 4)) * (MX ? 16 : 8)) * 2
+                                                                   (ks * 4 + (lane >> 4)) * 16) * 2
                                             : kOutOfRange;
         }
     }
     __device__ __forceinline__ void load(StepRegs<1, MX, RT, 1>& s) {
-        s.b[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
+        load_weights<MX>(b, s.b[0]);
         if constexpr (MX) s.sc[0] = sc[0];
 #pragma unroll
-        for (int m = 0; m < RT; ++m)
-#pragma unroll
-            for (int l = 0; l < (MX ? 2 : 1); ++l)
-                s.a[m][0][l] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off[m] + l * 16, 0, 0));
-        b += kStepBytes;
+        for (int m = 0; m < RT; ++m) load_row(rows, off[m], s.a[m][0]);
+        b += step_bytes<MX>();
         if constexpr (MX) sc += 2;
 #pragma unroll
-        for (int m = 0; m < RT; ++m) off[m] += MX ? 128 : 64;
+        for (int m = 0; m < RT; ++m) off[m] += 128;
         if (++ks == nk) {                              // uniform
             ks = 0;
             if (++seg < *sg->count) enter();
@@ -661,7 +653,7 @@ struct DownCursor {
 template <int NP, bool F16, bool MX, int RT>
 __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
     typedef RowMap<NP, RT> Map;
-    constexpr int D = MX ? (RT == 1 ? 6 : 4) : (RT == 1 ? 8 : 6);   // steps in flight, 1 KiB of weights each
+    constexpr int D = MX ? (RT == 1 ? 6 : 4) : (RT == 1 ? 4 : 3);   // steps in flight, 1 KiB (MXFP8) or 2 of weights each
     extern __shared__ __attribute__((aligned(16))) char smem[];
     float* s_out = reinterpret_cast<float*>(smem);     // [kNW][T][16]
     const Segments sg = carve_segments(smem + kNW * p.T * 64, p);
@@ -679,10 +671,10 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
     cur.p = &p;
     cur.sg = &sg;
     cur.whole = whole;
-    cur.nk = p.I / (MX ? 64 : 32);
+    cur.nk = p.I / 64;
     const int segs = __builtin_amdgcn_readfirstlane(*sg.count);
-    cur.b_expert = static_cast<int64_t>(p.H >> 6) * cur.nk * kStepBytes;
-    cur.b0 = p.dn + static_cast<int64_t>(n64) * cur.nk * kStepBytes + step_lane_offset<MX>(half, c0);
+    cur.b_expert = static_cast<int64_t>(p.H >> 6) * cur.nk * step_bytes<MX>();
+    cur.b0 = p.dn + static_cast<int64_t>(n64) * cur.nk * step_bytes<MX>() + step_lane_offset<MX>(half, c0);
     if constexpr (MX) {
         cur.sc_expert = static_cast<int64_t>(p.H) * (p.I / 32);
         cur.sc0 = p.dn_scales + static_cast<int64_t>(unit * kRowTile + (lane & 15)) * (p.I / 32) + (lane >> 5);
@@ -782,17 +774,17 @@ int x_parts(int x_dtype, bool mx) { return x_dtype == MOE_BF16 ? 0 : (mx ? 3 : 2
 int h_parts(bool mx) { return mx ? 3 : 2; }
 
 // Workgroups that share the down step's reduction for 16 columns: up to two
-// workgroups on every CU, as long as a wave keeps kPartSteps steps of what T
-// tokens are expected to choose (a wave has 4 to 8 in flight); below that the
+// workgroups on every CU, as long as a wave keeps 8 KiB of weights of what T
+// tokens are expected to choose (it has that much in flight); below that the
 // handing over of partial sums (about 3 us) costs more than it saves.
-constexpr int kPartSteps = 8;
 int down_parts(const moe_shape& s, bool mx) {
     const int E_loc = s.e_end - s.e_begin;
     double none = 1.0;                                 // an expert that no token chooses
     for (int t = 0; t < s.T; ++t) none *= 1.0 - static_cast<double>(s.K) / s.E;
-    const double steps = E_loc * (1.0 - none) * (s.I / (mx ? 64 : 32)) / kNW;
+    const double steps = E_loc * (1.0 - none) * (s.I / 64) / kNW;
     int n = 512 / (s.H / kRowTile);
-    if (n > steps / kPartSteps) n = static_cast<int>(steps / kPartSteps);
+    const int least = mx ? 8 : 4;
+    if (n > steps / least) n = static_cast<int>(steps / least);
     return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : n);
 }
 
