@@ -191,13 +191,16 @@ __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
 // Every token's K best experts in order (larger logit first, equal ones by index)
 // and their weights, to LDS (idx, w: [T K]).  Tokens are taken as many at a time
 // as `keys` (`room` of them) holds the ordered logits of, one to a row of 16
-// lanes, whose K rounds run side by side: a round scans the row's keys, finds the
-// best over the row by rotations and strikes it out.  The loops are left rolled:
-// a launch starts with a cold instruction cache, and straight code runs at the
-// rate it is fetched (unrolled rounds took 9 us for 24 tokens, these take 3).
+// lanes, whose K rounds run side by side.  A lane owns every 16th expert; a round
+// takes the best of its keys, then the best of the row.  Up to 128 experts the
+// keys stay in registers and the row compares their upper words by DPP maxima,
+// the rest only where two lanes' agree; beyond that a round scans the LDS keys.
+// The rounds' loop is left rolled: a launch starts with a cold instruction
+// cache, and straight code runs at the rate it is fetched (unrolled rounds of one
+// token after the other took 9 us for 24 tokens, these take under 3).
 __device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys, int room, int* idx, float* w) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), c = lane & 15;
-    constexpr int kRows = kNW * 4;
+    constexpr int kRows = kNW * 4, kHeld = 8;
     const int batch = min(kRows, room / p.E);
     for (int t0 = 0; t0 < p.T; t0 += batch) {
         const int n = min(batch, p.T - t0);
@@ -210,38 +213,84 @@ __device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys,
         const bool on = row < n;
         uint64_t* mine = keys + (on ? row : 0) * p.E;
         const int at = (t0 + row) * p.K;               // used where on
-        double top = 0.0;
+        if (p.E <= 16 * kHeld) {                       // uniform
+            uint64_t held[kHeld];
+#pragma unroll
+            for (int q = 0; q < kHeld; ++q) held[q] = q * 16 + c < p.E ? mine[q * 16 + c] : 0;
 #pragma unroll 1
-        for (int k = 0; k < p.K; ++k) {
-            uint64_t key = 0;
-            int index = 0x7FFFFFFF;
-#pragma unroll 2
-            for (int e = c; e < p.E; e += 16) {
-                const uint64_t v = mine[e];
-                if (v > key || index == 0x7FFFFFFF) {
-                    key = v;
-                    index = e;
+            for (int k = 0; k < p.K; ++k) {
+                uint64_t key = held[0];
+                int index = c;
+#pragma unroll
+                for (int q = 1; q < kHeld; ++q) {
+                    const bool take = held[q] > key;   // the lower index stays
+                    key = take ? held[q] : key;
+                    index = take ? q * 16 + c : index;
+                }
+                uint32_t m = static_cast<uint32_t>(key >> 32);
+                const uint32_t own = m;
+                m = max(m, row_rotate<0x128>(m));      // row_ror:8, :4, :2, :1
+                m = max(m, row_rotate<0x124>(m));
+                m = max(m, row_rotate<0x122>(m));
+                m = max(m, row_rotate<0x121>(m));
+                const uint32_t best = static_cast<uint32_t>(__ballot(own == m) >> (lane & 48)) & 0xFFFFu;
+                bool win = own == m;
+                if (__ballot((best & (best - 1u)) != 0u) != 0ull) {   // some row's upper words agree
+                    uint64_t top = key;
+                    int where = index;
+                    row_best<0x128>(top, where);
+                    row_best<0x124>(top, where);
+                    row_best<0x122>(top, where);
+                    row_best<0x121>(top, where);
+                    win = where == index;
+                }
+                if (win) {
+                    if (on) {
+                        idx[at + k] = index;
+                        mine[k] = key;                 // in LDS the row's keys are no longer needed
+                    }
+#pragma unroll
+                    for (int q = 0; q < kHeld; ++q)
+                        if (index == q * 16 + c) held[q] = 0;
                 }
             }
-            row_best<0x128>(key, index);               // row_ror:8, :4, :2, :1
-            row_best<0x124>(key, index);
-            row_best<0x122>(key, index);
-            row_best<0x121>(key, index);
-            if (on && c == 0) {
-                mine[index] = 0;
-                const double v = unordered(key);
-                if (k == 0) top = v;
-                idx[at + k] = index;
-                w[at + k] = static_cast<float>(v - top);
+        } else {
+            double top = 0.0;
+#pragma unroll 1
+            for (int k = 0; k < p.K; ++k) {
+                uint64_t key = 0;
+                int index = 0x7FFFFFFF;
+#pragma unroll 2
+                for (int e = c; e < p.E; e += 16) {
+                    const uint64_t v = mine[e];
+                    if (v > key || index == 0x7FFFFFFF) {
+                        key = v;
+                        index = e;
+                    }
+                }
+                row_best<0x128>(key, index);
+                row_best<0x124>(key, index);
+                row_best<0x122>(key, index);
+                row_best<0x121>(key, index);
+                if (on && c == 0) {
+                    mine[index] = 0;
+                    const double v = unordered(key);
+                    if (k == 0) top = v;
+                    idx[at + k] = index;
+                    w[at + k] = static_cast<float>(v - top);
+                }
+                asm volatile("" ::: "memory");         // a wave's LDS operations run in order
             }
-            asm volatile("" ::: "memory");             // a wave's LDS operations run in order
         }
         if (on) {
+            if (p.E <= 16 * kHeld)
+                for (int k = c; k < p.K; k += 16) w[at + k] = static_cast<float>(unordered(mine[k]) - unordered(mine[0]));
+            asm volatile("" ::: "memory");
             for (int k = c; k < p.K; k += 16) w[at + k] = expf(w[at + k]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            asm volatile("" ::: "memory");
             float sum = 0.0f;
             for (int k = 0; k < p.K; ++k) sum += w[at + k];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            asm volatile("" ::: "memory");
             for (int k = c; k < p.K; k += 16) w[at + k] = w[at + k] / sum;
         }
         __syncthreads();
