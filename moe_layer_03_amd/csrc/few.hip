@@ -188,11 +188,58 @@ __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
     index = take ? i : index;
 }
 
+// K rounds of a row whose keys its lanes hold, HELD each: winner k's index to
+// idx[k], its key to mine[k] (in LDS the row's keys are no longer needed).
+template <int HELD>
+__device__ __forceinline__ void held_rounds(int E, int K, bool on, uint64_t* mine, int* idx) {
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15;
+    uint64_t held[HELD];
+#pragma unroll
+    for (int q = 0; q < HELD; ++q) held[q] = q * 16 + c < E ? mine[q * 16 + c] : 0;
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        uint64_t key = held[0];
+        int index = c;
+#pragma unroll
+        for (int q = 1; q < HELD; ++q) {
+            const bool take = held[q] > key;   // the lower index stays
+            key = take ? held[q] : key;
+            index = take ? q * 16 + c : index;
+        }
+        uint32_t m = static_cast<uint32_t>(key >> 32);
+        const uint32_t own = m;
+        m = max(m, row_rotate<0x128>(m));      // row_ror:8, :4, :2, :1
+        m = max(m, row_rotate<0x124>(m));
+        m = max(m, row_rotate<0x122>(m));
+        m = max(m, row_rotate<0x121>(m));
+        const uint32_t best = static_cast<uint32_t>(__ballot(own == m) >> (lane & 48)) & 0xFFFFu;
+        bool win = own == m;
+        if (__ballot((best & (best - 1u)) != 0u) != 0ull) {   // some row's upper words agree
+            uint64_t top = key;
+            int where = index;
+            row_best<0x128>(top, where);
+            row_best<0x124>(top, where);
+            row_best<0x122>(top, where);
+            row_best<0x121>(top, where);
+            win = where == index;
+        }
+        if (win) {
+            if (on) {
+                idx[k] = index;
+                mine[k] = key;
+            }
+#pragma unroll
+            for (int q = 0; q < HELD; ++q)
+                if (index == q * 16 + c) held[q] = 0;
+        }
+    }
+}
+
 // Every token's K best experts in order (larger logit first, equal ones by index)
 // and their weights, to LDS (idx, w: [T K]).  Tokens are taken as many at a time
 // as `keys` (`room` of them) holds the ordered logits of, one to a row of 16
 // lanes, whose K rounds run side by side.  A lane owns every 16th expert; a round
-// takes the best of its keys, then the best of the row.  Up to 128 experts the
+// takes the best of its keys, then the best of the row.  Up to 256 experts the
 // keys stay in registers and the row compares their upper words by DPP maxima,
 // the rest only where two lanes' agree; beyond that a round scans the LDS keys.
 // The rounds' loop is left rolled: a launch starts with a cold instruction
@@ -200,7 +247,7 @@ __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
 // token after the other took 9 us for 24 tokens, these take under 3).
 __device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys, int room, int* idx, float* w) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), c = lane & 15;
-    constexpr int kRows = kNW * 4, kHeld = 8;
+    constexpr int kRows = kNW * 4;
     const int batch = min(kRows, room / p.E);
     for (int t0 = 0; t0 < p.T; t0 += batch) {
         const int n = min(batch, p.T - t0);
@@ -213,48 +260,9 @@ __device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys,
         const bool on = row < n;
         uint64_t* mine = keys + (on ? row : 0) * p.E;
         const int at = (t0 + row) * p.K;               // used where on
-        if (p.E <= 16 * kHeld) {                       // uniform
-            uint64_t held[kHeld];
-#pragma unroll
-            for (int q = 0; q < kHeld; ++q) held[q] = q * 16 + c < p.E ? mine[q * 16 + c] : 0;
-#pragma unroll 1
-            for (int k = 0; k < p.K; ++k) {
-                uint64_t key = held[0];
-                int index = c;
-#pragma unroll
-                for (int q = 1; q < kHeld; ++q) {
-                    const bool take = held[q] > key;   // the lower index stays
-                    key = take ? held[q] : key;
-                    index = take ? q * 16 + c : index;
-                }
-                uint32_t m = static_cast<uint32_t>(key >> 32);
-                const uint32_t own = m;
-                m = max(m, row_rotate<0x128>(m));      // row_ror:8, :4, :2, :1
-                m = max(m, row_rotate<0x124>(m));
-                m = max(m, row_rotate<0x122>(m));
-                m = max(m, row_rotate<0x121>(m));
-                const uint32_t best = static_cast<uint32_t>(__ballot(own == m) >> (lane & 48)) & 0xFFFFu;
-                bool win = own == m;
-                if (__ballot((best & (best - 1u)) != 0u) != 0ull) {   // some row's upper words agree
-                    uint64_t top = key;
-                    int where = index;
-                    row_best<0x128>(top, where);
-                    row_best<0x124>(top, where);
-                    row_best<0x122>(top, where);
-                    row_best<0x121>(top, where);
-                    win = where == index;
-                }
-                if (win) {
-                    if (on) {
-                        idx[at + k] = index;
-                        mine[k] = key;                 // in LDS the row's keys are no longer needed
-                    }
-#pragma unroll
-                    for (int q = 0; q < kHeld; ++q)
-                        if (index == q * 16 + c) held[q] = 0;
-                }
-            }
-        } else {
+        if (p.E <= 128) held_rounds<8>(p.E, p.K, on, mine, idx + at);       // uniform
+        else if (p.E <= 256) held_rounds<16>(p.E, p.K, on, mine, idx + at);
+        else {
             double top = 0.0;
 #pragma unroll 1
             for (int k = 0; k < p.K; ++k) {
@@ -283,7 +291,7 @@ __device__ __forceinline__ void select_experts(const FewArgs& p, uint64_t* keys,
             }
         }
         if (on) {
-            if (p.E <= 16 * kHeld)
+            if (p.E <= 256)
                 for (int k = c; k < p.K; k += 16) w[at + k] = static_cast<float>(unordered(mine[k]) - unordered(mine[0]));
             asm volatile("" ::: "memory");
             for (int k = c; k < p.K; k += 16) w[at + k] = expf(w[at + k]);
