@@ -25,13 +25,21 @@ struct DenseArgs {
 
 // ---- epilogue ------------------------------------------------------------------
 
+// v / (1 + exp(-c v')): the hardware's exp2 and reciprocal, an ulp each, and the
+// rounding of the exponent, (|v'| + 3) 2^-24 of the result in all.  (With expf and
+// a division, 6000 x 4096 x 4096 with bias and SiLU took 206 us; so 196.)  The
+// reciprocal underflows below v' = -87, where the result is under 1e-36: zero.
+__device__ __forceinline__ float over_one_plus_exp(float v, float minus_x_log2e) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(minus_x_log2e));
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {                                     // uniform
-        case MOE_EPI_SILU: return v / (1.0f + expf(-v));
+        case MOE_EPI_SILU: return over_one_plus_exp(v, v * -1.4426950408889634f);
         case MOE_EPI_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
         // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)): no cancellation for negative z
         case MOE_EPI_GELU_TANH:
-            return v / (1.0f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+            return over_one_plus_exp(v, -2.3022081981443250f * (v + 0.044715f * v * v * v));
         case MOE_EPI_RELU: return fmaxf(v, 0.0f);
         default: return v;
     }
@@ -55,7 +63,7 @@ __device__ __forceinline__ void finish(const DenseArgs& p, int row, int col, flo
     if (p.bias != nullptr) v += p.bias[col];
     if (p.gated) {
         if (p.bias != nullptr) u += p.bias[p.N + col];
-        v = v / (1.0f + expf(-v)) * u;
+        v = activate(v, MOE_EPI_SILU) * u;
     } else {
         v = activate(v, p.act);
     }
@@ -71,7 +79,7 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, fl
     v += b0;
     if (p.gated) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * (u[i] + b1[i]);
+        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], MOE_EPI_SILU) * (u[i] + b1[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = activate(v[i], p.act);
