@@ -170,9 +170,11 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)                // steps past the end: the last one again, A is zero there
-                r[q][h] = *reinterpret_cast<const u32x4*>(
-                    b + static_cast<int64_t>(min(k0 / 32 + q, nk32 - 1)) * kStepBytes + h * 1024);
+            for (int h = 0; h < 2; ++h)                // zeros past the end, as A's (an infinity times A's would be NaN)
+                r[q][h] = k0 / 32 + q < nk32           // uniform
+                              ? *reinterpret_cast<const u32x4*>(
+                                    b + static_cast<int64_t>(k0 / 32 + q) * kStepBytes + h * 1024)
+                              : u32x4{0u, 0u, 0u, 0u};
     };
     load_a(0);
     load_b(rb, 0);
@@ -457,8 +459,8 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     };
     // Copies of stage kt of a tile into ring place st.  The place along k is the
     // uniform offset of a copy; only a slice that K ends in, or past K, looks at
-    // each lane's k.  Weight slices past the packed end read the last one again:
-    // A is zero there.
+    // each lane's k.  Past the packed end both sides are zero: a weight read again
+    // there would turn an infinity of the last slice into NaN.
     auto issue = [&](const Source& s, int kt, int st) {
 #pragma unroll
         for (int i = 0; i < AC; ++i) {
@@ -467,10 +469,11 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
             if (k0 + kTileBK > p.K) off = k0 + a_k[i] < p.K ? off : kOutOfRange;   // uniform condition
             copy_to_lds(s.a, &s_a[st][(i * 8 + wave) * 16 * kTileBK], static_cast<int>(off), k0 * 2);
         }
-        const int kc = min(kt * SL + b_slice, nk32 - 1);
+        const int ks = kt * SL + b_slice, kc = min(ks, nk32 - 1);
+        const int off_b = ks < nk32 ? lane * 16 : static_cast<int>(kOutOfRange);
 #pragma unroll
         for (int d = 0; d < BD; ++d)
-            copy_to_lds(s.b, &s_b[st][wave * BD + d][0], lane * 16, kc * kStepBytes + (b_first + d) * 1024);
+            copy_to_lds(s.b, &s_b[st][wave * BD + d][0], off_b, kc * kStepBytes + (b_first + d) * 1024);
     };
 
     int tile = lid;                                    // the grid has no more workgroups than tiles

@@ -193,6 +193,25 @@ def test_offsets_past_32_bits():
     assert ((got.double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(1, 64, 40, 0), (5, 64, 72, 1), (100, 64, 104, 0), (70, 100, 33, 1),
+                                       (130, 192, 40, 0), (300, 320, 104, 0), (1100, 512, 296, 0), (300, 100, 161, 3)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_infinite_weights(M, N, K, pad, value):
+    """An infinity in the last row of the weights reaches its own column only, as an infinity: what a kernel multiplies
+    beyond K is zero on both sides."""
+    g = torch.Generator().manual_seed(9)
+    w = (torch.randn((K, N), generator=g) * 0.05).bfloat16()
+    w[K - 1, 3::5] = value
+    buf = torch.full((M, K + pad), math.nan, dtype=torch.bfloat16, device="cuda")
+    a = buf[:, :K]
+    a.copy_(torch.rand((M, K), generator=g) + 0.5)
+    s = B.DenseShape(M, N, K)
+    c = torch.empty((M, N), dtype=torch.float32, device="cuda")
+    B.moe_dense_gemm(s, a, B.moe_pack_dense(s, w.cuda()), c=c)
+    assert torch.isfinite(c[:, [j for j in range(N) if j % 5 != 3]]).all()
+    assert (c[:, 3::5] == value).all()
+
+
 def test_no_rows():
     s = B.DenseShape(0, 40, 64)
     packed = B.moe_pack_dense(s, torch.zeros((64, 40), dtype=torch.bfloat16, device="cuda"))
