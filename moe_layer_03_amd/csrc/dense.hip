@@ -40,7 +40,7 @@ __device__ __forceinline__ float activate(float v, int act) {
         // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)): no cancellation for negative z
         case MOE_EPI_GELU_TANH:
             return over_one_plus_exp(v, -2.3022081981443250f * (v + 0.044715f * v * v * v));
-        case MOE_EPI_RELU: return fmaxf(v, 0.0f);
+        case MOE_EPI_RELU: return v < 0.0f ? 0.0f : v;       // NaN stays
         default: return v;
     }
 }
@@ -53,7 +53,7 @@ __device__ __forceinline__ float load_as(const void* p, int64_t i, int dtype) {
 
 __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v) {
     if (dtype == MOE_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = dtype == MOE_BF16 ? f32_to_bf16(v) : f32_to_f16_sat(v);
+    else static_cast<uint16_t*>(p)[i] = dtype == MOE_BF16 ? f32_to_bf16(v) : f32_to_f16_or_nan(v);
 }
 
 // The element (row, col): v is its sum (gated: the gate's, u the up's).  The
@@ -112,7 +112,8 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, fl
                 make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         else
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
-                make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+                make_uint2(f32_to_f16_or_nan(v[0]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[1])) << 16,
+                           f32_to_f16_or_nan(v[2]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[3])) << 16);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -607,7 +608,7 @@ __global__ __launch_bounds__(256) void pack_dense_kernel(const ST* __restrict__ 
         if (col < N && k < K) {
             const ST x = src[static_cast<int64_t>(k) * N + col];
             if constexpr (sizeof(ST) == 2) v[j] = x;
-            else v[j] = f32_to_f16_sat(x);
+            else v[j] = f32_to_f16_or_nan(x);
         }
     }
     uint16_t* d = dst + ((static_cast<int64_t>(pc >> 6) * (Kp >> 4) + (k8 >> 1)) * 2 + ((pc >> 5) & 1)) * 512 +

@@ -12,8 +12,8 @@
 // takes column l % 16 of 16 and k group l / 16, 16 consecutive k of the step, as
 // two MFMA operands of 8 (the MFMA's own order of k does not matter as long as
 // both operands share it).  So a row's four lanes read 128 consecutive bytes, a
-// whole cache line, in two loads (32 rows of
-// 4096 x 4096: 15.8 us, against 18.0 us with 64 bytes of a line at a time).
+// whole cache line, in two loads (32 rows of 4096 x 4096: 15.8 us, against 18.0 us
+// with 64 bytes of a line at a time).
 //
 // Rows are held as NP 16-bit parts whose sum is the row's value:
 //   1 part: the value itself;
@@ -62,11 +62,14 @@ __device__ __forceinline__ u32x4 mx_to_bf16(uint32_t w0, uint32_t w1, uint32_t s
     return r;
 }
 
-// Parts of v (see above); fp16 saturates at 65504.
+// fp16, saturating at 65504; NaN stays NaN.
+__device__ __forceinline__ uint16_t f32_to_f16_or_nan(float v) { return v == v ? f32_to_f16_sat(v) : uint16_t{0x7E00}; }
+
+// Parts of v (see above); fp16 saturates at 65504, NaN stays in the first part.
 template <int NP, bool F16>
 __device__ __forceinline__ void split_parts(float v, uint16_t (&p)[NP]) {
     if constexpr (F16) {
-        p[0] = f32_to_f16_sat(v);
+        p[0] = f32_to_f16_or_nan(v);
         if constexpr (NP == 2) {
             const float c = fminf(fmaxf(v, -65504.0f), 65504.0f);
             p[1] = f32_to_f16_sat((c - f16_to_f32(p[0])) * kLoScale);

@@ -212,6 +212,20 @@ def test_infinite_weights(M, N, K, pad, value):
     assert (c[:, 3::5] == value).all()
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(3, 70, 72, 0), (20, 64, 33, 1), (100, 128, 64, 0), (130, 100, 65, 0),
+                                       (300, 256, 96, 0)])
+@pytest.mark.parametrize("c", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", list(EPI))
+def test_nan_stays_in_its_row(M, N, K, pad, c, act):
+    """A NaN reaches its own row's outputs, whatever the activation and type, and no other row."""
+    d = inputs(M, N, K, act, "f16", pad=pad, seed=8)
+    d["a"][M // 2, K - 1] = math.nan
+    s = B.DenseShape(M, N, K, gated=act == "swiglu")
+    got = B.moe_dense_gemm(s, d["a"], B.moe_pack_dense(s, *d["w"]), EPI[act], c_dtype=TYPES[c])
+    assert torch.isnan(got[M // 2]).all()
+    assert torch.isfinite(got[: M // 2]).all() and torch.isfinite(got[M // 2 + 1:]).all()
+
+
 def test_no_rows():
     s = B.DenseShape(0, 40, 64)
     packed = B.moe_pack_dense(s, torch.zeros((64, 40), dtype=torch.bfloat16, device="cuda"))

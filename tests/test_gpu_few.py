@@ -163,6 +163,19 @@ def test_shards_add_up():
     assert ((total - ref).abs() <= bound + 4 * 2.0 ** -24 * ref.abs()).all()
 
 
+@pytest.mark.parametrize("T", [1, 4, 6, 13, 27])
+@pytest.mark.parametrize("mx,dtype", [(False, "bf16"), (False, "f32"), (True, "bf16"), (True, "f32")])
+def test_nan_stays_in_its_token(T, mx, dtype):
+    s = B.Shape(T, 256, 24, 4, 256, 0, 24)
+    d = make(s, dtype, mx, seed=31)
+    d["x"][T // 2, 5] = float("nan")
+    got, idx, w = call(s, d, pack(s, d, dtype, mx), mx)
+    assert ((idx >= 0) & (idx < s.E)).all() and all(len(set(r)) == s.K for r in idx.tolist())
+    rest = [t for t in range(T) if t != T // 2]
+    assert torch.isnan(got[T // 2]).all() and torch.isnan(w[T // 2]).all()
+    assert torch.isfinite(got[rest]).all() and torch.isfinite(w[rest]).all()
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_repeats_bit_for_bit(mx):
     s = B.Shape(20, 512, 128, 8, 256, 0, 128)
