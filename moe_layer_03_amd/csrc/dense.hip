@@ -416,6 +416,9 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     const int nk32 = p.Kp / kTileBK, nk = (nk32 + SL * kTileNB - 1) / (SL * kTileNB) * kTileNB;
     const int total = mtiles * ntiles;
     const int G = gridDim.x, b = blockIdx.x;
+    // A workgroup's only tile may leave the zero stages out.  The longest stages do (1000 x 1024 x 1096: 13.4 -> 12.5
+    // us); with shorter ones the test costs more than the at most three stages (1024 x 4096 x 4096: 49 -> 51 us).
+    const int run = SL > 2 && total <= G ? (nk32 + SL - 1) / SL : nk;
     // one contiguous range of tiles per XCD and round, 8 row tiles x 4 column tiles of it at a time
     const int lid = (G % 8 == 0) ? (b % 8) * (G / 8) + (b / 8) : b;
     constexpr int kGroup = 8;
@@ -525,6 +528,8 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
             const bool last = s0 + kTileNB == nk;      // uniform
 #pragma unroll
             for (int q = 0; q < kTileNB; ++q) {
+                if constexpr (SL > 2)
+                    if (s0 + q >= run) break;          // uniform
                 // phase 2s (late: 2s + 1): read stage s = s0 + q, refill the buffer of stage s - 1
                 read_stage(q);
                 if (q == 0 || !last) issue(cur, s0 + q + kTileNB - 1, (q + kTileNB - 1) % kTileNB);
