@@ -6,6 +6,8 @@
 // padded to a multiple of 64 and the columns to whole 64-column pairs (gated:
 // 32 gate columns and the same 32 up columns to a pair, so a lane holds g and u
 // of one output element); the padding is zero, so only A's reads need masks.
+#include <algorithm>
+
 #include "stream.hpp"
 
 namespace moe {
@@ -654,13 +656,29 @@ int launch_stream_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
 
 template <bool F16, bool ROWS16>
 int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
-    // wide units where they give every CU a workgroup, half ones else (1 row of 4096, gated: N 1536 6.98 us against 8.70
-    // with wide units, N 12288 35.9 against 31.4)
-    if (p.M <= 16)
-        return pairs * 2 < kCUs ? launch_stream_tiles<F16, ROWS16, 1, 1>(p, pairs, st)
-                                : launch_stream_tiles<F16, ROWS16, 1, 2>(p, pairs, st);
-    if (p.M <= 32) return launch_stream_tiles<F16, ROWS16, 2, 2>(p, pairs, st);
-    return launch_stream_tiles<F16, ROWS16, 4, 2>(p, pairs, st);
+    // Unit shape: what the busiest CU reads (rows and columns of its units; a CU's share of the caches bounds few units,
+    // not memory).  64 x 1024 x 4096: 16 x 16 8.1 us, 64 x 16 19.7; 64 x 4096 x 4096: 32 x 32 16.1 us, 64 x 16 20.8;
+    // 16 x 8192 x 4096: 16 x 32 12.8 us, 16 x 16 16.0.
+    int best = 0;
+    int64_t least = 0;
+    for (int i = 0; i < 6; ++i) {
+        const int mt = 4 >> (i >> 1), ct = 2 - (i & 1), rows = mt * kRowTile;
+        if (i < 4 && p.M <= rows / 2) continue;        // half of its rows would be past M
+        const int64_t groups = pairs * (4 / ct) * ((p.M + rows - 1) / rows);
+        const int64_t cost = (groups + kCUs - 1) / kCUs * (std::min(rows, p.M) + ct * kRowTile);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = i;
+        }
+    }
+    switch (best) {
+        case 0: return launch_stream_tiles<F16, ROWS16, 4, 2>(p, pairs, st);
+        case 1: return launch_stream_tiles<F16, ROWS16, 4, 1>(p, pairs, st);
+        case 2: return launch_stream_tiles<F16, ROWS16, 2, 2>(p, pairs, st);
+        case 3: return launch_stream_tiles<F16, ROWS16, 2, 1>(p, pairs, st);
+        case 4: return launch_stream_tiles<F16, ROWS16, 1, 2>(p, pairs, st);
+        default: return launch_stream_tiles<F16, ROWS16, 1, 1>(p, pairs, st);
+    }
 }
 
 template <bool F16, int MW, int NW, int NA, int SL>
