@@ -644,7 +644,13 @@ inline int64_t pairs_of(const moe_dense_shape& s) {
 }
 
 constexpr int kCUs = 256;
-constexpr int kStreamRows = 128;                       // most rows of the weight-streaming kernel
+constexpr int kStreamRows = 512;                       // most rows the weight-streaming kernel is considered for
+
+// A kernel's shape and the time expected of it, in ns.
+struct Choice {
+    int shape;
+    double ns;
+};
 
 template <bool F16, bool ROWS16, int MT, int CT>
 int launch_stream_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
@@ -654,29 +660,36 @@ int launch_stream_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     return MOE_OK;
 }
 
-template <bool F16, bool ROWS16>
-int launch_stream(const DenseArgs& p, int64_t pairs, hipStream_t st) {
-    // Unit shape: what the busiest CU reads (rows and columns of its units; a CU's share of the caches bounds few units,
-    // not memory).  64 x 1024 x 4096: 16 x 16 8.1 us, 64 x 16 19.7; 64 x 4096 x 4096: 32 x 32 16.1 us, 64 x 16 20.8;
-    // 16 x 8192 x 4096: 16 x 32 12.8 us, 16 x 16 16.0.
-    int best = 0;
-    int64_t least = 0;
-    for (int i = 0; i < 6; ++i) {
-        const int mt = 4 >> (i >> 1), ct = 2 - (i & 1), rows = mt * kRowTile;
-        if (i < 4 && p.M <= rows / 2) continue;        // half of its rows would be past M
+// Unit shape: what the busiest CU reads, at the 37 bytes/ns it gets from the
+// caches (half that with unaligned rows), decides; few rows are bound there and
+// not by memory.  64 x 1024 x 4096: 16 x 16 8.1 us, 64 x 16 19.7; 64 x 4096 x
+// 4096: 32 x 32 16.1 us, 64 x 16 20.8; 16 x 8192 x 4096: 16 x 32 12.8 us, 16 x 16
+// 16.0.  Expected times were within 20 % of measured ones from 4 to 65 us.
+struct UnitShape {
+    int mt, ct;
+};
+constexpr UnitShape kUnitShapes[] = {{4, 2}, {2, 2}, {2, 1}, {1, 2}, {1, 1}};   // 4, 1 reads more than 2, 2 always
+
+Choice stream_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
+    Choice best{0, 0.0};
+    for (int i = 0; i < 5; ++i) {
+        const int ct = kUnitShapes[i].ct, rows = kUnitShapes[i].mt * kRowTile;
+        if (rows > kRowTile && p.M <= rows / 2) continue;   // half of its rows would be past M
         const int64_t groups = pairs * (4 / ct) * ((p.M + rows - 1) / rows);
-        const int64_t cost = (groups + kCUs - 1) / kCUs * (std::min(rows, p.M) + ct * kRowTile);
-        if (least == 0 || cost < least) {
-            least = cost;
-            best = i;
-        }
+        const int64_t read = (groups + kCUs - 1) / kCUs * (std::min(rows, p.M) + ct * kRowTile) * p.Kp * 2;
+        const double ns = read / (rows16 ? 37.0 : 18.5) + 2000.0;
+        if (best.ns == 0.0 || ns < best.ns) best = Choice{i, ns};
     }
-    switch (best) {
+    return best;
+}
+
+template <bool F16, bool ROWS16>
+int launch_stream(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
+    switch (shape) {
         case 0: return launch_stream_tiles<F16, ROWS16, 4, 2>(p, pairs, st);
-        case 1: return launch_stream_tiles<F16, ROWS16, 4, 1>(p, pairs, st);
-        case 2: return launch_stream_tiles<F16, ROWS16, 2, 2>(p, pairs, st);
-        case 3: return launch_stream_tiles<F16, ROWS16, 2, 1>(p, pairs, st);
-        case 4: return launch_stream_tiles<F16, ROWS16, 1, 2>(p, pairs, st);
+        case 1: return launch_stream_tiles<F16, ROWS16, 2, 2>(p, pairs, st);
+        case 2: return launch_stream_tiles<F16, ROWS16, 2, 1>(p, pairs, st);
+        case 3: return launch_stream_tiles<F16, ROWS16, 1, 2>(p, pairs, st);
         default: return launch_stream_tiles<F16, ROWS16, 1, 1>(p, pairs, st);
     }
 }
@@ -700,22 +713,23 @@ struct TileShape {
 };
 constexpr TileShape kTileShapes[] = {{256, 4, 1}, {192, 4, 1}, {128, 4, 1}, {128, 2, 2}, {64, 2, 2}, {64, 1, 4}};
 
-template <bool F16>
-int launch_tiles(const DenseArgs& p, int64_t pairs, hipStream_t st) {
-    int best = 0;
-    double least = 0.0;
+Choice tile_choice(const DenseArgs& p, int64_t pairs) {
+    Choice best{0, 0.0};
     for (int i = 0; i < 6; ++i) {
         const TileShape& t = kTileShapes[i];
         const int64_t tiles = ((p.M + t.rows - 1) / t.rows) * ((pairs + t.pairs - 1) / t.pairs);
         const int64_t stages = (p.Kp / kTileBK + t.slices - 1) / t.slices + 8;
         const double mul = t.rows * t.pairs * t.slices / 1024.0 * 1200, copy = (t.rows + t.pairs * 64) * t.slices / 512.0 * 850;
-        const double cost = static_cast<double>((tiles + kCUs - 1) / kCUs) * stages * ((mul > copy ? mul : copy) + 250);
-        if (i == 0 || cost < least) {
-            least = cost;
-            best = i;
-        }
+        const double cycles = static_cast<double>((tiles + kCUs - 1) / kCUs) * stages * ((mul > copy ? mul : copy) + 250);
+        const double ns = cycles * 0.52 + 2000.0;      // about 1.9 GHz, and what a launch takes
+        if (best.ns == 0.0 || ns < best.ns) best = Choice{i, ns};
     }
-    switch (best) {
+    return best;
+}
+
+template <bool F16>
+int launch_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
+    switch (shape) {
         case 0: return launch_tile<F16, 2, 4, 4, 1>(p, pairs, st);
         case 1: return launch_tile<F16, 2, 4, 3, 1>(p, pairs, st);
         case 2: return launch_tile<F16, 2, 4, 2, 1>(p, pairs, st);
@@ -732,15 +746,23 @@ int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     const bool rows16 = reinterpret_cast<uintptr_t>(p.a) % 16 == 0 && p.lda % 8 == 0 && p.K % 8 == 0;
     // byte offsets within a tile of rows stay below the buffer range
     const bool near = p.lda * 2 * 256 <= kBufferRange;
-    if (near && p.M <= (rows16 ? kStreamRows : 64))
-        return rows16 ? launch_stream<F16, true>(p, pairs, st) : launch_stream<F16, false>(p, pairs, st);
-    if (!rows16 || !near) {
-        const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
-        hipLaunchKernelGGL((dense_any_kernel<F16>), g, dim3(256), 0, st, p);
-        MOE_CHECK_LAUNCH();
-        return MOE_OK;
+    const Choice stream = stream_choice(p, pairs, rows16);
+    const bool few = near && p.M <= kStreamRows;
+    if (rows16 && near) {
+        // 96 x 12288 x 4096: tiles 38.5 us, streaming 64.8; 256 x 1024 x 4096: 19.6 and 13.6
+        const Choice tile = tile_choice(p, pairs);
+        return few && stream.ns <= tile.ns ? launch_stream<F16, true>(p, pairs, stream.shape, st)
+                                           : launch_tiles<F16>(p, pairs, tile.shape, st);
     }
-    return launch_tiles<F16>(p, pairs, st);
+    const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
+    // a stage of the any-alignment kernel takes about 1.65 us while its workgroups fit the chip twice over.
+    // 128 x 1003 x 1091: streaming 8.2 us, 16.2 there; 128 x 4099 x 1091: 26.3 and 16.4
+    const double rounds = std::max(1.0, static_cast<double>(g.x) * g.y / (2 * kCUs));
+    if (few && stream.ns <= (p.Kp + kAnyK - 1) / kAnyK * 1650.0 * rounds)
+        return launch_stream<F16, false>(p, pairs, stream.shape, st);
+    hipLaunchKernelGGL((dense_any_kernel<F16>), g, dim3(256), 0, st, p);
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
 }
 
 }  // namespace

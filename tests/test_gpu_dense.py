@@ -105,6 +105,21 @@ def test_sizes(size, gated):
     run(*size, act="swiglu" if gated else "none", c="bf16", bias=True, residual="bf16", seed=1 + sum(size), pad=8)
 
 
+# one size for each unit and tile shape, ungated and gated
+SHAPES = [(5, 4100, 40), (17, 2050, 40), (17, 4100, 40), (48, 4100, 40), (200, 200, 40), (65, 16400, 264), (2050, 1000, 40),
+          (2050, 4100, 40), (600, 16400, 40), (513, 70, 520), (513, 70, 40), (5, 4100, 131), (17, 2050, 131),
+          (17, 4100, 131), (48, 4100, 1031), (128, 4100, 131)]
+SHAPES_GATED = [(5, 2050, 40), (48, 2050, 40), (65, 8200, 264), (1030, 1000, 40), (300, 12300, 72), (200, 16400, 72),
+                (200, 200, 40), (513, 70, 520), (513, 70, 40), (5, 2050, 131), (17, 2050, 131), (200, 200, 131),
+                (48, 2050, 1031), (128, 2050, 131)]
+
+
+@pytest.mark.parametrize("size,act", [(s, "relu") for s in SHAPES] + [(s, "swiglu") for s in SHAPES_GATED])
+@pytest.mark.parametrize("a", ["bf16", "f16"])
+def test_unit_and_tile_shapes(size, act, a):
+    run(*size, act, a=a, c="f32", bias=True, residual="bf16", pad=8, seed=sum(size))
+
+
 @pytest.mark.parametrize("act", list(EPI))
 @pytest.mark.parametrize("a", ["bf16", "f16"])
 @pytest.mark.parametrize("M", [5, 70, 300])
