@@ -6,7 +6,7 @@
 #include <cstddef>
 #include <mutex>
 
-#include "common.hpp"
+#include "block.hpp"
 #include "route_prefetch.hpp"
 
 // Workspace of moe_layer_noalloc: one copy per GPU, held by that GPU from the

@@ -8,6 +8,7 @@
 // of one output element); the padding is zero, so only A's reads need masks.
 #include <algorithm>
 
+#include "block.hpp"
 #include "stream.hpp"
 
 namespace moe {

@@ -27,6 +27,7 @@
 // Precision: the rows a are kept to 22 bits (two fp16 parts) or 24 (three bf16
 // parts, MXFP8), and nothing else is rounded below float32, so the float32
 // output is a float32 result, not an fp16 one (stream.hpp).
+#include "block.hpp"
 #include "stream.hpp"
 
 namespace moe {
