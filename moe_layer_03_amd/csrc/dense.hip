@@ -141,6 +141,8 @@ __device__ __forceinline__ u32x4 load_tail(const uint16_t* row, int k, int K) {
 // 16 columns of each half.  Direct copies to LDS need aligned rows, so A goes
 // through registers, and a stage is 128 k long to have as few waits as possible:
 // the next stage's rows and weights are on their way while one is multiplied.
+// Bound by the latency of a stage, 1.65 us: 283 x 1516 x 1396 16.5 us (a library
+// product of the same sizes 14.7).
 constexpr int kAnyK = 128;
 constexpr int kAnyLd = kAnyK + 8;                      // LDS row, 16 of them in distinct banks
 
@@ -220,6 +222,12 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
 }
 
 // ---- few rows: weight streaming ------------------------------------------------------
+// Bound by what a CU reads (its unit's rows and columns), 37 bytes/ns from the
+// caches: 128 rows of 4096 x 4096 take 23.3 us, 786 KB on each CU, against 5.6 us
+// for one pass over memory; a unit that reads less needs the reduction split over
+// workgroups, and partial sums in memory.  One row is bound by the launch and
+// one round of latency: 1536 columns, gated, 25 MB in 7.0 us (3.6 TB/s); 12288
+// columns, gated, 201 MB in 31.2 us (6.45 TB/s).
 // A workgroup owns MT * 16 rows x 16 columns of CT column halves (CT = 1, gated:
 // 8 gate and 8 up columns) and its kNW waves take every kNW-th step of the
 // reduction, so the weights go straight from memory to registers, each element
@@ -370,6 +378,15 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
 //
 // A's rows go through a buffer resource based at the tile's first row: rows past
 // M and k past K copy zeros.
+//
+// Bound by the matrix unit at the clock the power limit leaves it (random inputs
+// hold 1.7 GHz; zeros run a fifth faster): 8192^3 851 us, 1292 TFLOP/s (a library product 775 to
+// 812); 6000 x 4096 x 4096 195 us, 1035 TFLOP/s (167), 192 x 256 tiles, of which
+// 512 fill the chip exactly twice.  Besides the clock LDS bounds it: a stage of
+// the 256 x 256 tile reads 96 KB and copies 32 KB while the MFMAs take 1024
+// cycles (without the MFMAs 685 us, without the copies 775, then 899 in all).
+// Tried at 8192^3: 4 waves of 128 x 128 each 897 us, weights straight to registers
+// 893, copies issued in the multiplying phase 929.
 constexpr int kTileNB = 4;
 constexpr int kTileBK = 32;
 

@@ -8,7 +8,9 @@
 // With so few rows the layer is bound by reading the chosen experts' weights
 // once: 6 H I bytes per expert (16-bit) against 6 H I operations per row.
 //
-// Three steps:
+// Three launches (hidden 4096, expert 1536, top 8 of 128, one token: 5.0, 40.2
+// and 20.4 us with 16-bit weights, 4.6, 26.7 and 16.5 us with MXFP8; 62 and 47 us
+// in all, where the weights alone take 46 and 24 at 6.6 TB/s):
 //   route    partial logits over slices of H, double-precision MFMA;
 //   gate/up  every workgroup sums the partials and selects the experts itself
 //            (T rows of E values, cheaper than another launch), then takes
@@ -18,11 +20,17 @@
 //            long reduction: out[T, n] = [rows of every chosen expert] x
 //            [their down weights stacked], where row t of an expert's slice is
 //            zero if token t did not choose it.  A workgroup owns 16 output
-//            columns and the whole reduction: no scatter, no atomics, and the
-//            summation order does not depend on timing.
-// An MFMA row is a token in both products (no packing): rows of tokens that
-// did not choose the expert load zeros through an out-of-range buffer offset,
-// without memory traffic.
+//            columns and a part of the reduction, so nothing is scattered, and
+//            the parts are added in their order, whatever the timing.
+// In gate/up an MFMA row is a token: rows of tokens that did not choose the
+// expert load zeros through an out-of-range buffer offset, without memory
+// traffic.  In down, an expert's rows are compacted, their parts stacked into
+// one tile (RowMap).
+//
+// One kernel for gate/up and down, handing over by counters in memory, was
+// right and slower wherever the grid fills the chip (one token, MXFP8: 72 us
+// against 49.5): the workgroups' atomics and looks at shared counters cost about
+// 25 us.  Kernel boundaries cost 1.6 us each.
 //
 // Precision: the rows a are kept to 22 bits (two fp16 parts) or 24 (three bf16
 // parts, MXFP8), and nothing else is rounded below float32, so the float32
@@ -78,6 +86,9 @@ template <typename XT> __device__ __forceinline__ double widen(XT v);
 template <> __device__ __forceinline__ double widen<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
 template <> __device__ __forceinline__ double widen<float>(float v) { return v; }
 
+// Bound by latency: one round of loads, at most 16 double-precision MFMAs per wave
+// and a reduction through LDS, 3.4 us (tiny) to 6.2 (32 tokens of 4096 to 128
+// experts, 1 MB of router weights) of which an empty launch takes 1.6.
 // One workgroup: 16 experts x 16 tokens x one slice of H; its waves take 32-h
 // groups in turn, at most kRouteGroups each, all loads issued before the first
 // product.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and k = l / 16;
@@ -386,6 +397,12 @@ __device__ __forceinline__ void build_tables(const Tables& s, const FewArgs& p) 
 }
 
 // ---- gate and up ------------------------------------------------------------------
+// Bound by the weights' arrival once the launch has started and selected (about
+// 5 us): 32 tokens, who choose 111 of 128 experts, read 2.8 GB in 444 us (6.3
+// TB/s); one token 201 MB in 40.2 us (5.0), with MXFP8 104 MB in 26.7 (3.9).
+// An even number of units for every workgroup (384 of them, two each, for 768
+// units) was slower than 512 workgroups of which half take two: 53 us against 47
+// for the MXFP8 layer.
 
 // Steps wave, wave + kNW, ... of a gate/up unit.
 template <int NP, bool MX, int MT>
@@ -702,6 +719,9 @@ struct DownCursor {
     }
 };
 
+// Bound as gate/up is, behind the segments' tables (about 3 us) and the handing
+// over of partial sums (3 us): 32 tokens 1.4 GB in 222 us (6.4 TB/s), one token
+// 101 MB in 20.4 us (4.9), with MXFP8 52 MB in 16.5 (3.1).
 // A workgroup owns 16 output columns and part blockIdx.y of the steps, each wave a
 // contiguous run of them.  A wave adds its rows' sums to its own [T][16] in LDS
 // where the segment ends (or once at its end, where MFMA rows are tokens all
