@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the layer runs in the library's HIP
 kernels.  Functions carry the C names; each takes a ``Shape`` and torch
 tensors on the GPU, passes their data pointers and the current HIP stream,
-and raises ``MoeError`` on a non-zero status.  Output tensors the caller
-does not pass are allocated with torch (device memory only).
+and raises ``MoeError`` on a non-zero status.  Output tensors and workspaces
+the caller does not pass are allocated with torch (device memory only), as
+under ``torch.cuda.stream(stream)`` where a stream is given.
 
 The library must be built (``moe_layer_03_amd.build``); loading fails loudly
 otherwise -- there is no fallback path.
@@ -247,8 +248,21 @@ def operand_dtype(x_dtype: torch.dtype) -> torch.dtype:
     return torch.bfloat16 if x_dtype == torch.bfloat16 else torch.float16
 
 
-def _empty(n, dtype, device):
-    return torch.empty(n, dtype=dtype, device=device)
+def _scratch(n, dtype, device, stream=None):
+    """Memory that the caller never sees, from the pool of the stream that the call runs on (None: the current one):
+    the allocator hands it on only behind that stream's work, so it may be dropped once the call is enqueued."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
+def _empty(n, dtype, device, stream=None):
+    """A result, allocated as scratch is; the caller's stream reads it, so it is not handed on before that has."""
+    t = _scratch(n, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 # ---------------------------------------------------------------------------
@@ -287,7 +301,7 @@ def moe_pack_weights(s: Shape, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     dt = w_gate.dtype
     need = moe_packed_weight_bytes(s)
     if packed is None:
-        packed = _empty(need, torch.uint8, w_gate.device)
+        packed = _empty(need, torch.uint8, w_gate.device, stream)
     if packed.dtype != torch.uint8 or packed.numel() < need:
         raise ValueError(f"packed must be a uint8 buffer of at least {need} bytes")
     st = load().moe_pack_weights(ctypes.byref(s.c()), _ptr(w_gate, dt, n, "w_gate"), _ptr(w_up, dt, n, "w_up"),
@@ -307,16 +321,16 @@ def moe_route(s: Shape, x: torch.Tensor, w_router: torch.Tensor, bias: Optional[
     tiles small ones when the shape allows it (the outputs are the same)."""
     dev = x.device
     if topk_idx is None:
-        topk_idx = _empty((s.T, s.K), torch.int32, dev)
+        topk_idx = _empty((s.T, s.K), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = _empty((s.T, s.K), torch.float32, dev)
+        topk_w = _empty((s.T, s.K), torch.float32, dev, stream)
     if logits is None and want_logits:
-        logits = _empty((s.T, s.E), torch.float32, dev)
+        logits = _empty((s.T, s.E), torch.float32, dev, stream)
     if not screened:
         ws = None
     elif ws is None:
         need = moe_route_workspace_bytes(s)
-        ws = _empty(need, torch.uint8, dev) if need > 0 else None
+        ws = _scratch(need, torch.uint8, dev, stream) if need > 0 else None
     st = load().moe_route(ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x),
                           _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
                           _ptr(bias, torch.float32, s.E, "bias"), _ptr(topk_idx, torch.int32, s.T * s.K, "topk_idx"),
@@ -330,9 +344,9 @@ def moe_route(s: Shape, x: torch.Tensor, w_router: torch.Tensor, bias: Optional[
 def moe_route_from_logits(s: Shape, logits: torch.Tensor, topk_idx=None, topk_w=None, stream=None):
     dev = logits.device
     if topk_idx is None:
-        topk_idx = _empty((s.T, s.K), torch.int32, dev)
+        topk_idx = _empty((s.T, s.K), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = _empty((s.T, s.K), torch.float32, dev)
+        topk_w = _empty((s.T, s.K), torch.float32, dev, stream)
     st = load().moe_route_from_logits(ctypes.byref(s.c()), _ptr(logits, torch.float32, s.T * s.E, "logits"),
                                       _ptr(topk_idx, torch.int32, s.T * s.K, "topk_idx"),
                                       _ptr(topk_w, torch.float32, s.T * s.K, "topk_w"), _stream(stream))
@@ -345,16 +359,16 @@ def moe_dispatch(s: Shape, topk_idx: torch.Tensor, x: Optional[torch.Tensor] = N
     """Returns dict(counts, offsets, row_token, row_slot, slot_row, x_packed)."""
     dev = topk_idx.device
     cap = s.cap
-    counts = _empty(s.E_loc, torch.int32, dev) if counts is None else counts
-    offsets = _empty(s.E_loc + 1, torch.int32, dev) if offsets is None else offsets
-    row_token = _empty(cap, torch.int32, dev) if row_token is None else row_token
-    row_slot = _empty(cap, torch.int32, dev) if row_slot is None else row_slot
-    slot_row = _empty((s.T, s.K), torch.int32, dev) if slot_row is None else slot_row
+    counts = _empty(s.E_loc, torch.int32, dev, stream) if counts is None else counts
+    offsets = _empty(s.E_loc + 1, torch.int32, dev, stream) if offsets is None else offsets
+    row_token = _empty(cap, torch.int32, dev, stream) if row_token is None else row_token
+    row_slot = _empty(cap, torch.int32, dev, stream) if row_slot is None else row_slot
+    slot_row = _empty((s.T, s.K), torch.int32, dev, stream) if slot_row is None else slot_row
     if x is not None and x_packed is None:
-        x_packed = _empty((cap, s.H), operand_dtype(x.dtype), dev)
+        x_packed = _empty((cap, s.H), operand_dtype(x.dtype), dev, stream)
     need = moe_dispatch_workspace_bytes(s)
     if ws is None:
-        ws = _empty(max(need, 16), torch.uint8, dev)
+        ws = _scratch(max(need, 16), torch.uint8, dev, stream)
     st = load().moe_dispatch(ctypes.byref(s.c()), _ptr(topk_idx, torch.int32, s.T * s.K, "topk_idx"),
                              _ptr(x, None, s.T * s.H, "x"), _dt(x) if x is not None else MOE_BF16,
                              _ptr(counts, torch.int32, s.E_loc, "counts"),
@@ -381,7 +395,7 @@ def moe_grouped_gemm(s: Shape, a: torch.Tensor, offsets: torch.Tensor, packed: t
     else:
         nc = s.H
     if c is None:
-        c = _empty((cap, nc), c_dtype, a.device)
+        c = _empty((cap, nc), c_dtype, a.device, stream)
     if a_rows is None and a.numel() != cap * kd:
         raise ValueError(f"a must have {cap * kd} elements without a_rows")
     if a.numel() % kd:
@@ -398,7 +412,7 @@ def moe_grouped_gemm(s: Shape, a: torch.Tensor, offsets: torch.Tensor, packed: t
 def moe_combine(s: Shape, y_packed: torch.Tensor, slot_row: torch.Tensor, topk_w: torch.Tensor, out=None,
                 stream=None) -> torch.Tensor:
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, y_packed.device)
+        out = _empty((s.T, s.H), torch.float32, y_packed.device, stream)
     st = load().moe_combine(ctypes.byref(s.c()), _ptr(y_packed, None, s.cap * s.H, "y_packed"), _dt(y_packed),
                             _ptr(slot_row, torch.int32, s.T * s.K, "slot_row"),
                             _ptr(topk_w, torch.float32, s.T * s.K, "topk_w"),
@@ -412,9 +426,9 @@ def moe_layer(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed: torch.T
               offsets=None, row_token=None, row_slot=None, slot_row=None, stream=None) -> torch.Tensor:
     """The fused layer share; optional routing/dispatch outputs are written when given."""
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, x.device)
+        out = _empty((s.T, s.H), torch.float32, x.device, stream)
     if ws is None:
-        ws = _empty(max(moe_layer_workspace_bytes(s), 16), torch.uint8, x.device)
+        ws = _scratch(max(moe_layer_workspace_bytes(s), 16), torch.uint8, x.device, stream)
     cap = s.cap
     st = load().moe_layer(ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x),
                           _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
@@ -436,7 +450,7 @@ def moe_layer_noalloc(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed:
                       offsets=None, row_token=None, row_slot=None, slot_row=None, stream=None) -> torch.Tensor:
     """moe_layer with the library's static per-GPU workspace (the C call allocates nothing)."""
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, x.device)
+        out = _empty((s.T, s.H), torch.float32, x.device, stream)
     cap = s.cap
     st = load().moe_layer_noalloc(ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x),
                                   _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
@@ -478,7 +492,7 @@ def moe_pack_weights_mxfp8(s: Shape, w_gate: torch.Tensor, w_up: torch.Tensor, w
     if need == 0:
         raise MoeError("moe_packed_weight_bytes_mxfp8", MOE_ERR_UNSUPPORTED, 0, "shape not supported for MXFP8")
     if packed is None:
-        packed = _empty(need, torch.uint8, w_gate.device)
+        packed = _empty(need, torch.uint8, w_gate.device, stream)
     st = load().moe_pack_weights_mxfp8(ctypes.byref(s.c()), _ptr(w_gate, dt, n, "w_gate"), _ptr(w_up, dt, n, "w_up"),
                                        _ptr(w_down, dt, n, "w_down"), _dt(w_gate),
                                        _ptr(packed, torch.uint8, None, "packed"), _stream(stream))
@@ -490,9 +504,9 @@ def moe_quantize_mxfp8(x: torch.Tensor, codes=None, scales=None, stream=None):
     """x [rows, K] bf16/fp32 -> (codes uint8 [rows, K], scales uint8 [rows, K/32])."""
     rows, K = x.shape
     if codes is None:
-        codes = _empty((rows, K), torch.uint8, x.device)
+        codes = _empty((rows, K), torch.uint8, x.device, stream)
     if scales is None:
-        scales = _empty((rows, K // 32), torch.uint8, x.device)
+        scales = _empty((rows, K // 32), torch.uint8, x.device, stream)
     st = load().moe_quantize_mxfp8(rows, K, _ptr(x, None, rows * K, "x"), _dt(x),
                                    _ptr(codes, torch.uint8, rows * K, "codes"),
                                    _ptr(scales, torch.uint8, rows * (K // 32), "scales"), _stream(stream))
@@ -513,9 +527,9 @@ def moe_grouped_gemm_mxfp8(s: Shape, a: torch.Tensor, a_scales: torch.Tensor, of
         nc = s.H
     mx_out = c_dtype == torch.uint8
     if c is None:
-        c = _empty((cap, nc), c_dtype, a.device)
+        c = _empty((cap, nc), c_dtype, a.device, stream)
     if mx_out and c_scales is None:
-        c_scales = _empty((cap, nc // 32), torch.uint8, a.device)
+        c_scales = _empty((cap, nc // 32), torch.uint8, a.device, stream)
     if a.numel() % kd or a_scales.numel() * 32 != a.numel():
         raise ValueError("a [rows, K] codes with a_scales [rows, K/32]")
     st = load().moe_grouped_gemm_mxfp8(ctypes.byref(s.c()), _ptr(a, torch.uint8, None, "a"),
@@ -540,9 +554,9 @@ def moe_layer_mxfp8(s: Shape, x: torch.Tensor, w_router: torch.Tensor, packed: t
                     stream=None) -> torch.Tensor:
     """The layer share with MXFP8 expert GEMMs (packed from moe_pack_weights_mxfp8)."""
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, x.device)
+        out = _empty((s.T, s.H), torch.float32, x.device, stream)
     if ws is None:
-        ws = _empty(max(moe_layer_workspace_bytes_mxfp8(s), 16), torch.uint8, x.device)
+        ws = _scratch(max(moe_layer_workspace_bytes_mxfp8(s), 16), torch.uint8, x.device, stream)
     cap = s.cap
     st = load().moe_layer_mxfp8(ctypes.byref(s.c()), _ptr(x, None, s.T * s.H, "x"), _dt(x),
                                 _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
@@ -588,9 +602,9 @@ def _layer_few_tokens(mx: bool, s: Shape, x, w_router, packed, bias, out, ws, to
     if packed.numel() < weights:
         raise ValueError(f"packed must hold {weights} bytes, got {packed.numel()}")
     if out is None:
-        out = _empty((s.T, s.H), torch.float32, dev)
+        out = _empty((s.T, s.H), torch.float32, dev, stream)
     if ws is None:
-        ws = _empty(max(need, 16), torch.uint8, dev)
+        ws = _scratch(max(need, 16), torch.uint8, dev, stream)
     pairs = s.T * s.K
     args = (c, _ptr(x, None, s.T * s.H, "x"), _dt(x), _ptr(w_router, None, s.H * s.E, "w_router"), _dt(w_router),
             _ptr(bias, torch.float32, s.E, "bias"), _ptr(packed, torch.uint8, None, "packed"),
@@ -639,7 +653,7 @@ def moe_pack_dense(d: DenseShape, w: torch.Tensor, w_up: Optional[torch.Tensor] 
     """Pack w [K, N] (gated: the gate weight, with w_up [K, N]), bf16, fp16 or fp32; M does not matter."""
     need = moe_packed_dense_bytes(d)
     if packed is None:
-        packed = _empty(max(need, 16), torch.uint8, w.device)
+        packed = _empty(max(need, 16), torch.uint8, w.device, stream)
     if packed.dtype != torch.uint8 or packed.numel() < need:
         raise ValueError(f"packed must be a uint8 buffer of at least {need} bytes")
     n = d.N * d.K
@@ -679,7 +693,7 @@ def moe_dense_gemm(d: DenseShape, a: torch.Tensor, packed: torch.Tensor, epilogu
         raise ValueError(f"packed must hold {need} bytes, got {packed.numel()}")
     dev = a.device
     if c is None:
-        c = _empty((d.M, d.N), c_dtype or a.dtype, dev)
+        c = _empty((d.M, d.N), c_dtype or a.dtype, dev, stream)
     pa, lda = _rows(a, d.M, d.K, "a")
     pr, ldr = _rows(residual, d.M, d.N, "residual")
     pc, ldc = _rows(c, d.M, d.N, "c")
