@@ -56,7 +56,7 @@ __device__ __forceinline__ float load_as(const void* p, int64_t i, int dtype) {
 
 __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v) {
     if (dtype == MOE_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = dtype == MOE_BF16 ? f32_to_bf16(v) : f32_to_f16_or_nan(v);
+    else static_cast<uint16_t*>(p)[i] = dtype == MOE_BF16 ? f32_to_bf16_or_nan(v) : f32_to_f16_or_nan(v);
 }
 
 // The element (row, col): v is its sum (gated: the gate's, u the up's).  The
@@ -112,7 +112,7 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, fl
             *reinterpret_cast<floatx4*>(static_cast<float*>(p.c) + at) = v;
         else if (p.c_dtype == MOE_BF16)
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                make_uint2(pack_bf16x2_or_nan(v[0], v[1]), pack_bf16x2_or_nan(v[2], v[3]));
         else
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
                 make_uint2(f32_to_f16_or_nan(v[0]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[1])) << 16,

@@ -65,6 +65,17 @@ __device__ __forceinline__ u32x4 mx_to_bf16(uint32_t w0, uint32_t w1, uint32_t s
 // fp16, saturating at 65504; NaN stays NaN.
 __device__ __forceinline__ uint16_t f32_to_f16_or_nan(float v) { return v == v ? f32_to_f16_sat(v) : uint16_t{0x7E00}; }
 
+// bf16, to nearest even; NaN of any payload stays NaN (f32_to_bf16 takes finite
+// values only: it carries a full payload into the sign).  One instruction.
+__device__ __forceinline__ uint16_t f32_to_bf16_or_nan(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16x2_or_nan(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{lo, hi}), bf16x2_t));
+}
+
 // Parts of v (see above); fp16 saturates at 65504, NaN stays in the first part.
 template <int NP, bool F16>
 __device__ __forceinline__ void split_parts(float v, uint16_t (&p)[NP]) {
