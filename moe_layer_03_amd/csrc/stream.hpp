@@ -20,7 +20,7 @@
 //   2 parts (fp16): v = p0 + 2^-11 p1, |error| <= 2^-22 |v| for 2^-14 <= |v| <=
 //     65504 (p1 is scaled up so that it stays a normal fp16 number); the parts
 //     have their own accumulators, joined at the end;
-//   3 parts (bf16): v = p0 + p1 + p2, exact to 2^-24 |v|; one accumulator.
+//   3 parts (bf16): v = p0 + p1 + p2, exact for |v| >= 2^-102; one accumulator.
 // The MFMAs of the extra parts are free here: the weights' arrival bounds the
 // product, and a row held to 22 bits or more keeps the float32 output's digits.
 #pragma once
@@ -77,6 +77,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2_or_nan(float lo, float hi) {
 }
 
 // Parts of v (see above); fp16 saturates at 65504, NaN stays in the first part.
+// bf16 parts are cut off, not rounded: three times the top 8 of the 24 bits left,
+// exact, and the first part of no number becomes infinite.  A NaN whose payload
+// is cut off leaves an infinity in the first part and NaN in the second.
 template <int NP, bool F16>
 __device__ __forceinline__ void split_parts(float v, uint16_t (&p)[NP]) {
     if constexpr (F16) {
@@ -89,7 +92,7 @@ __device__ __forceinline__ void split_parts(float v, uint16_t (&p)[NP]) {
         float rest = v;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            p[i] = f32_to_bf16(rest);
+            p[i] = static_cast<uint16_t>(__float_as_uint(rest) >> 16);
             rest -= bf16_to_f32(p[i]);                 // exact
         }
     }

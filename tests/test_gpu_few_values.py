@@ -1,0 +1,118 @@
+"""The few-token layer's digits: rows far below and above one, NaN of every payload."""
+import math
+
+import pytest
+import torch
+
+from few_reference import make, pack
+from moe_layer_03_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def reference(s, d, parts):
+    """(out, bound, spread) in 64 bits; bound is the largest error that float32 accumulation and the rows' parts can
+    leave, spread a token's largest difference of logits between its first and a local expert.
+
+    A float32 sum of n products in any order is off by at most n u sum|products|.  silu has slope at most 1.1; expf
+    (2 u), its sum, the division and three products leave 8 u of a row's value; the weight of a logit d below the first
+    (d + K + 6) u: d rounded to float32, expf, a sum of K (whose own d exp(-d) is at most 0.37 each) and a division.
+    Two fp16 parts of a row scaled to a largest value in [2^14, 2^15) (x) or [2^-9, 2^15) (the down step's input) hold
+    each value to 2^-22 of it plus 2^-36, that is 2^-50 or 2^-27 of the token's largest; three bf16 parts to 2^-24."""
+    x = d["x"].double()
+    f32 = d["x"].dtype == torch.float32
+    logits = x @ d["w_router"].double()
+    if d["bias"] is not None:
+        logits = logits + d["bias"].double()
+    xa = x.abs()
+    dx = torch.zeros_like(x)
+    if f32:
+        dx = 2.0 ** -24 * xa if parts == 3 else 2.0 ** -22 * xa + 2.0 ** -50 * xa.amax(1, keepdim=True)
+    out = torch.zeros((s.T, s.H), dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(out)
+    spread = torch.zeros(s.T, dtype=torch.float64, device=x.device)
+    for t, row in enumerate(logits.tolist()):
+        pick = sorted(range(s.E), key=lambda e: (-row[e], e))[: s.K]
+        ex = [math.exp(row[e] - row[pick[0]]) for e in pick]
+        rows = []
+        for j, e in enumerate(pick):
+            if not s.e_begin <= e < s.e_end:
+                continue
+            wg, wu, wd = (d[k][e - s.e_begin].double() for k in ("gate", "up", "down"))
+            a, b = x[t] @ wg, x[t] @ wu
+            sg, w = a * torch.sigmoid(a), ex[j] / math.fsum(ex)
+            da = s.H * U * (xa[t] @ wg.abs()) + dx[t] @ wg.abs()
+            db = s.H * U * (xa[t] @ wu.abs()) + dx[t] @ wu.abs()
+            h = w * sg * b
+            dh = w * (1.1 * da * b.abs() + sg.abs() * db + 1.1 * da * db) + (
+                (14 + s.K + row[pick[0]] - row[e]) * U + 2.0 ** -22) * h.abs()
+            rows.append((h, dh, wd))
+            spread[t] = max(spread[t].item(), row[pick[0]] - row[e])
+        top = max((h.abs().max().item() for h, _, _ in rows), default=0.0)
+        for h, dh, wd in rows:
+            dh = dh + (2.0 ** -27 * top if parts == 2 else 0)
+            out[t] += h @ wd
+            bound[t] += dh @ wd.abs() + s.I * s.K * U * (h.abs() @ wd.abs())
+    return out, bound, spread
+
+
+def call(s, d, packed, mx=False, **kw):
+    ws = torch.full((B.moe_layer_few_tokens_workspace_bytes(s),), 0xFF, dtype=torch.uint8, device="cuda")
+    f = B.moe_layer_few_tokens_mxfp8 if mx else B.moe_layer_few_tokens
+    got = f(s, d["x"], d["w_router"], packed, d["bias"], ws=ws, **kw)
+    torch.cuda.synchronize()
+    return got
+
+
+def check(s, d, got, parts, rms=3e-6):
+    """Within the bound everywhere, and every token within rms of its own RMS (and its weights' error), however small
+    that is: random rounding of the longest float32 chain (512 additions) leaves 8e-7 in each of three products."""
+    ref, bound, spread = reference(s, d, parts)
+    err = (got.double() - ref).abs()
+    assert torch.isfinite(got).all()
+    assert (err <= bound + 2.0 ** -148).all(), f"{(err / bound.clamp(min=1e-300)).max().item():.3g} of the bound"
+    size = ref.pow(2).mean(1).sqrt()
+    assert (err.pow(2).mean(1).sqrt() <= (rms + spread * U) * size + 2.0 ** -148).all()
+
+
+@pytest.mark.parametrize("std", [1e-3, 1e-7, 30.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_mxfp8_rows_of_any_size(std, dtype):
+    s = B.Shape(9, 512, 24, 4, 256, 0, 20)
+    d = make(s, dtype, mx=True, seed=95)
+    d["x"] = (d["x"].float() * std).to(d["x"].dtype)
+    check(s, d, call(s, d, pack(s, d, dtype, True), True), 3)
+
+
+def test_mxfp8_largest_float32_row():
+    """x at float32's largest number, beside weights that bring it back."""
+    s = B.Shape(2, 256, 4, 1, 256, 0, 4)
+    d = make(s, "f32", mx=True, seed=96)
+    d["x"].zero_()
+    d["x"][:, 7] = torch.tensor([3.4028234663852886e38, -3.4e38])
+    d["w_router"].zero_()
+    for k, e in (("gate", -110), ("up", -110), ("down", -8)):
+        d[k].fill_(2.0 ** e)
+    got = call(s, d, pack(s, d, "f32", True), True)
+    check(s, d, got, 3)
+
+
+@pytest.mark.parametrize("nan", [0x7FC00000, 0x7FFFFFFF, 0x7F800001, 0xFFFFFFFF, 0xFF800001])
+@pytest.mark.parametrize("mx", [False, True])
+def test_every_nan_stays_in_its_token(nan, mx):
+    s = B.Shape(5, 256, 24, 4, 256, 0, 24)
+    d = make(s, "f32", mx, seed=97)
+    x = d["x"].cpu()
+    x.view(torch.int32)[2, 5] = nan - (1 << 32) if nan >> 31 else nan
+    d["x"] = x.cuda()
+    got = call(s, d, pack(s, d, "f32", mx), mx)
+    assert torch.isnan(got[2]).all()
+    assert torch.isfinite(got[[0, 1, 3, 4]]).all()
