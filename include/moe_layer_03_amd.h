@@ -375,8 +375,11 @@ int moe_layer_noalloc(const moe_shape* s, const void* x, int x_dtype, const void
  *   - logits are summed in double precision (moe_route: a float32 fma chain).
  *     Where two experts' logits are closer than the chain's rounding, the two
  *     may choose differently; exactly equal double sums go to the lower index.
- *   - nothing between x and out is rounded below 22 bits: SwiGLU activations
- *     and expert outputs are not rounded to fp16, so out is a float32 result.
+ *   - nothing between x and out is rounded to fp16: the weighted SwiGLU
+ *     activations keep 22 bits of each value or, where that is more, 2^-27 of
+ *     the token's largest, expert outputs are not rounded, and out is a float32
+ *     result however small the activations are.  (Past T * K * I = 2^31 / 24
+ *     not every scale fits, and values may be held to 2^-36 only.)
  *   Arguments as in moe_layer(); topk_idx [T, K] int32 and topk_w [T, K]
  *   float32 are optional outputs.  Rows of tokens with no local expert are
  *   written as zeros.  float32 x saturates at 65504 (fp16 parts), as in

@@ -20,9 +20,10 @@ struct FewWs {
     int32_t* idx;
     float* w;
     uint16_t* x;       // parts of float32 rows
-    uint16_t* h;       // parts of the weighted SwiGLU rows
+    uint16_t* h;       // parts of the weighted SwiGLU rows, at each level
     float* sums;       // partial sums of the down step
     int* arrived;      // their counters
+    uint32_t* levels;  // levels of those rows' units, four to a word, and a word for all
 };
 // Whether the shape is within the few-token layer's limits.
 bool few_tokens_fits(const moe_shape& s);

@@ -32,9 +32,12 @@
 // against 49.5): the workgroups' atomics and looks at shared counters cost about
 // 25 us.  Kernel boundaries cost 1.6 us each.
 //
-// Precision: the rows a are kept to 22 bits (two fp16 parts) or 24 (three bf16
-// parts, MXFP8), and nothing else is rounded below float32, so the float32
-// output is a float32 result, not an fp16 one (stream.hpp).
+// Precision: the rows a are kept to 22 bits (two fp16 parts; of small values to
+// 2^-27 of the token's largest, see kLevels) or 24 (three bf16 parts, MXFP8), and
+// nothing else is rounded below float32, so the float32 output is a float32
+// result, not an fp16 one (stream.hpp).
+#include <algorithm>
+
 #include "block.hpp"
 #include "stream.hpp"
 
@@ -60,6 +63,18 @@ constexpr int kRouteGroups = 2;                        // 32-h groups of a wave 
 constexpr int kMaxSlices = 16;
 constexpr int kMaxParts = 8;
 
+// Levels of the rows a where they have two fp16 parts: those hold 22 bits of values
+// from 2^-14 on but 2^-36 below, so a token whose rows are small needs them scaled
+// up.  By how much is known only once all its rows are, and one sum adds up a
+// token's rows across experts, so the scale is the token's: level l multiplies by
+// 2^(24 l).  Gate/up writes a unit's 16 columns of a row at every level at which
+// they stay below 2^15: level 0 always, and no other where one is 2^-9 or more, as
+// rows commonly have.  The down step takes the highest level that all units of the
+// token have.  Its largest value there is 2^-9 or more, and 2^-36 at most 2^-27 of
+// it, for any largest value that float32 holds.
+constexpr int kLevelBits = 24;
+constexpr int kLevels = 6;
+
 typedef double doublex4 __attribute__((ext_vector_type(4)));
 
 struct FewArgs {
@@ -77,6 +92,9 @@ struct FewArgs {
     float* out;                // [T][H]
     float* sums;               // [H / 16][parts][T][16] partial sums of the down step
     int* arrived;              // [H / 16] workgroups that have written theirs; cleared by the route step
+    uint8_t* levels;           // [T * K][I / 16] highest level written of a row's unit; cleared by the route step
+    int* above;                // whether one is above 0; cleared by the route step
+    int top;                   // highest level there is memory for
     int S, T, H, E, K, I, e_begin, E_loc;
 };
 
@@ -99,7 +117,8 @@ template <typename XT, int NPX, bool F16>
 __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __restrict__ x, const XT* __restrict__ w,
                                                                   int T, int H, int E, double* __restrict__ part,
                                                                   uint16_t* __restrict__ xp, int64_t xp_part,
-                                                                  int* __restrict__ arrived) {
+                                                                  int* __restrict__ arrived,
+                                                                  uint32_t* __restrict__ levels, int level_words) {
     __shared__ double s_red[kRouteNW][4][kWave];
     constexpr int V = 16 / sizeof(XT);                 // elements of a 16-byte load
     typedef XT vec __attribute__((ext_vector_type(V)));
@@ -111,6 +130,9 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
     const int g0 = blockIdx.z * kRouteNW + wave;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         for (int i = threadIdx.x; i < H / kRowTile; i += kRouteNW * 64) arrived[i] = 0;
+    const int block = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    const int threads = gridDim.x * gridDim.y * gridDim.z * (kRouteNW * 64);
+    for (int i = block * (kRouteNW * 64) + threadIdx.x; i < level_words; i += threads) levels[i] = 0u;
     doublex4 acc = {0.0, 0.0, 0.0, 0.0};
     for (int gb = g0; gb < groups; gb += kRouteGroups * step) {
         XT wv[kRouteGroups][8];
@@ -198,6 +220,17 @@ __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
     const bool take = k > key || (k == key && i < index);
     key = take ? k : key;
     index = take ? i : index;
+}
+
+// The highest level at which a row's 16 columns, one to each of 16 lanes, stay below 2^15.
+__device__ __forceinline__ int level_of(float v, int top) {
+    uint32_t m = __float_as_uint(fabsf(v));            // ordered as the numbers, NaN above them
+    m = max(m, row_rotate<0x128>(m));
+    m = max(m, row_rotate<0x124>(m));
+    m = max(m, row_rotate<0x122>(m));
+    m = max(m, row_rotate<0x121>(m));
+    const int room = 127 + 14 - static_cast<int>(m >> 23);
+    return room < kLevelBits ? 0 : min(room / kLevelBits, top);
 }
 
 // K rounds of a row whose keys its lanes hold, HELD each: winner k's index to
@@ -517,12 +550,27 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
             if (j >= 0) {
                 const int row = t * p.K + j;
                 const float act = g / (1.0f + expf(-g)) * up * tb.w[row];
-                uint16_t part[NPH];
-                split_parts<NPH, F16H>(act, part);
                 const int64_t pairs = static_cast<int64_t>(p.T) * p.K;
+                auto write = [&](int level, float v) {
+                    uint16_t part[NPH];
+                    split_parts<NPH, F16H>(v, part);
 #pragma unroll
-                for (int q = 0; q < NPH; ++q)
-                    p.h[(q * pairs + row) * p.I + u * kRowTile + (lane & 15)] = part[q];
+                    for (int q = 0; q < NPH; ++q)
+                        p.h[((level * NPH + q) * pairs + row) * p.I + u * kRowTile + (lane & 15)] = part[q];
+                };
+                write(0, act);
+                if constexpr (F16H) {
+                    const int level = level_of(act, p.top);
+                    if (level > 0) {
+                        float v = act;
+#pragma unroll 1
+                        for (int l = 1; l <= level; ++l) write(l, v *= 1 << kLevelBits);
+                        if ((lane & 15) == 0) {
+                            p.levels[row * nb + u] = static_cast<uint8_t>(level);
+                            *p.above = 1;
+                        }
+                    }
+                }
             }
         }
         lds_barrier();                                 // s_red is free
@@ -621,6 +669,26 @@ __device__ __forceinline__ void build_segments(const Segments& s, const FewArgs&
     __syncthreads();
 }
 
+// The level of every token's rows: the least of its units'.  Every thread of the
+// workgroup takes part; a wave takes every kNW-th pair, a lane four units at once.
+__device__ __forceinline__ void token_levels(const Segments& s, const FewArgs& p, int* level) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int words = p.I / 64, segs = *s.count, pairs = segs > 0 ? s.start[segs - 1] + s.rows[segs - 1] : 0;
+    const uint32_t* units = reinterpret_cast<const uint32_t*>(p.levels);
+    if (tid < p.T) level[tid] = kLevels - 1;
+    __syncthreads();
+#pragma unroll 4
+    for (int q = wave; q < pairs; q += kNW) {
+        const int pair = s.order[q];
+        for (int i = lane; i < words; i += kWave) {
+            const uint32_t v = units[pair * words + i];
+            const uint32_t least = min(min(v & 255u, v >> 8 & 255u), min(v >> 16 & 255u, v >> 24));
+            atomicMin(&level[pair / p.K], static_cast<int>(least));
+        }
+    }
+    __syncthreads();
+}
+
 // How a segment's rows and their parts share the RT * 16 MFMA rows: part and row
 // of MFMA row r of tile m.  Stacking the parts costs one A load per tile where
 // separate products would cost one per part, and loads are what a step is made of.
@@ -667,6 +735,7 @@ template <int NP, bool MX, int RT>
 struct DownCursor {
     const FewArgs* p;
     const Segments* sg;
+    const int* level;          // [T] of the tokens' rows, or NULL: 0
     bool whole;                // one row per token throughout: every expert's segment has the tokens as its rows
     const uint8_t* b0;         // this lane's bytes of expert 0's step 0
     const uint8_t* sc0;        // this lane's scale byte of expert 0's step 0
@@ -701,6 +770,7 @@ struct DownCursor {
             off[m] = pair >= 0 && part < NP ? part * part_bytes + (static_cast<uint32_t>(pair) * p->I +
                                                                    (ks * 4 + (lane >> 4)) * 16) * 2
                                             : kOutOfRange;
+            if (NP == 2 && level != nullptr && off[m] != kOutOfRange) off[m] += level[pair / p->K] * NP * part_bytes;
         }
     }
     __device__ __forceinline__ void load(StepRegs<1, MX, RT, 1>& s) {
@@ -735,19 +805,22 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     float* s_out = reinterpret_cast<float*>(smem);     // [kNW][T][16]
     const Segments sg = carve_segments(smem + kNW * p.T * 64, p);
-    __shared__ int s_last;
+    __shared__ int s_last, s_level[MOE_FEW_TOKENS_MAX];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit = blockIdx.x, parts = gridDim.y;
 
+    const bool leveled = NP == 2 && *p.above != 0;     // uniform
     for (int i = tid; i < kNW * p.T * 16; i += kNW * 64) s_out[i] = 0.0f;
     const bool whole = p.T <= Map::RV;
     build_segments(sg, p, Map::RV);
+    if (leveled) token_levels(sg, p, s_level);
 
     const int n64 = unit >> 2, half = (unit >> 1) & 1, c0 = (unit & 1) * 16;
     DownCursor<NP, MX, RT> cur;
     cur.p = &p;
     cur.sg = &sg;
+    cur.level = leveled ? s_level : nullptr;
     cur.whole = whole;
     cur.nk = p.I / 64;
     const int segs = __builtin_amdgcn_readfirstlane(*sg.count);
@@ -797,12 +870,16 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
     if (steps > 0 && (whole || ks != 0)) flush();
     __syncthreads();
     const int cells = p.T * 16;
+    auto write = [&](int i, float s) {                 // element i of [T][16]
+        if (leveled) s = ldexpf(s, -kLevelBits * s_level[i >> 4]);
+        p.out[static_cast<int64_t>(i >> 4) * p.H + unit * kRowTile + (i & 15)] = s;
+    };
     if (parts == 1) {
         for (int i = tid; i < cells; i += kNW * 64) {
             float s = 0.0f;
 #pragma unroll
             for (int q = 0; q < kNW; ++q) s += s_out[q * cells + i];
-            p.out[static_cast<int64_t>(i >> 4) * p.H + unit * kRowTile + (i & 15)] = s;
+            write(i, s);
         }
         return;
     }
@@ -830,7 +907,7 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
         for (int q = 0; q < parts; ++q)
             s += __hip_atomic_load(&p.sums[(static_cast<int64_t>(unit) * parts + q) * cells + i], __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
-        p.out[static_cast<int64_t>(i >> 4) * p.H + unit * kRowTile + (i & 15)] = s;
+        write(i, s);
     }
 }
 
@@ -847,9 +924,11 @@ int route_slices(int T, int H) {
     return S < kMaxSlices ? S : kMaxSlices;
 }
 
-// parts of the gate/up rows that the route step writes (0: the rows are read from x)
-int x_parts(int x_dtype, bool mx) { return x_dtype == MOE_BF16 ? 0 : (mx ? 3 : 2); }
-int h_parts(bool mx) { return mx ? 3 : 2; }
+// Highest level of the rows a (two parts each): the last, or as many as offsets below the buffer range allow.
+int top_level(const moe_shape& s) {
+    const int64_t level = static_cast<int64_t>(s.T) * s.K * s.I * 2 * 2;
+    return static_cast<int>(std::min<int64_t>(kLevels, kBufferRange / std::max<int64_t>(level, 1))) - 1;
+}
 
 // Workgroups that share the down step's reduction for 16 columns: up to two
 // workgroups on every CU, as long as a wave keeps 8 KiB of weights of what T
@@ -925,9 +1004,11 @@ size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w) {
     z.idx = reinterpret_cast<int32_t*>(take(pairs * 4));
     z.w = reinterpret_cast<float*>(take(pairs * 4));
     z.x = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * s.T * s.H * 2));
-    z.h = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * pairs * s.I * 2));
+    const size_t h_parts = std::max(3, 2 * (top_level(s) + 1));    // three (MXFP8), or two at each level
+    z.h = reinterpret_cast<uint16_t*>(take(h_parts * pairs * s.I * 2));
     z.sums = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxParts) * s.T * s.H * 4));
     z.arrived = reinterpret_cast<int*>(take(static_cast<size_t>(s.H) / kRowTile * 4));
+    z.levels = reinterpret_cast<uint32_t*>(take(pairs * (s.I / kRowTile) + 4));
     if (w != nullptr) *w = z;
     return off;
 }
@@ -953,6 +1034,10 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     p.out = out;
     p.sums = z.sums;
     p.arrived = z.arrived;
+    const int level_words = s.T * s.K * (s.I / 64);
+    p.levels = reinterpret_cast<uint8_t*>(z.levels);
+    p.above = reinterpret_cast<int*>(z.levels + level_words);
+    p.top = top_level(s);
     p.a = x_dtype == MOE_BF16 ? static_cast<const uint16_t*>(x) : z.x;
     p.a_part = static_cast<int64_t>(s.T) * s.H;
     const uint8_t* b = static_cast<const uint8_t*>(packed);
@@ -967,13 +1052,16 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     const dim3 g((s.E + kRowTile - 1) / kRowTile, (s.T + kRowTile - 1) / kRowTile, p.S), block(kRouteNW * 64);
     if (x_dtype == MOE_BF16)
         hipLaunchKernelGGL((few_route_kernel<uint16_t, 0, false>), g, block, 0, st, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
+                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
+                           z.levels, mx ? 0 : level_words + 1);
     else if (mx)
         hipLaunchKernelGGL((few_route_kernel<float, 3, false>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
+                           z.levels, mx ? 0 : level_words + 1);
     else
         hipLaunchKernelGGL((few_route_kernel<float, 2, true>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
+                           z.levels, mx ? 0 : level_words + 1);
     MOE_CHECK_LAUNCH();
     MOE_TRY(s.T <= kRowTile ? launch_gate_up<1>(p, x_dtype, mx, st) : launch_gate_up<2>(p, x_dtype, mx, st));
     const int parts = down_parts(s, mx);

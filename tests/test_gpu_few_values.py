@@ -83,6 +83,56 @@ def check(s, d, got, parts, rms=3e-6):
     assert (err.pow(2).mean(1).sqrt() <= (rms + spread * U) * size + 2.0 ** -148).all()
 
 
+SHAPES = [(1, 64, 4, 1, 64, 0, 4), (3, 256, 16, 4, 256, 2, 14), (8, 512, 64, 8, 256, 0, 64),
+          (13, 256, 32, 4, 512, 0, 32), (20, 256, 8, 4, 256, 0, 8), (32, 512, 128, 8, 256, 16, 100)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("std", [1e-2, 1e-3, 1e-4, 1e-7, 1e-12, 30.0])
+def test_rows_of_any_size(shape, dtype, std):
+    """x of std 1e-12 makes rows of 1e-25 and smaller."""
+    s = B.Shape(*shape)
+    d = make(s, dtype, seed=70 + s.T)
+    d["x"] = (d["x"].float() * std).to(d["x"].dtype)
+    check(s, d, call(s, d, pack(s, d, dtype)), 2)
+
+
+@pytest.mark.parametrize("T", [1, 7, 12, 32])
+@pytest.mark.parametrize("dtype", ["bf16"])
+def test_rows_of_every_size_together(T, dtype):
+    """A call whose tokens lie 2^46 apart, a zero row among them, and experts whose weights shrink their rows."""
+    s = B.Shape(T, 256, 24, 4, 256, 1, 23)
+    d = make(s, dtype, seed=80 + T, bias=True)
+    scale = torch.tensor([2.0 ** -(7 * t % 47) for t in range(T)], device="cuda")[:, None]
+    if T > 3:
+        scale[3] = 0.0
+    d["x"] = (d["x"].float() * scale).to(d["x"].dtype)
+    d["up"][5:9] = (d["up"][5:9] * 2.0 ** -6).to(torch.float16 if dtype == "f32" else torch.bfloat16).float()
+    check(s, d, call(s, d, pack(s, d, dtype)), 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16"])
+def test_one_large_value_in_a_small_row(dtype):
+    """One large x in a row of small ones, and one expert's row far above the others of its token."""
+    s = B.Shape(6, 512, 16, 4, 256, 0, 16)
+    d = make(s, dtype, seed=90)
+    x = d["x"].float() * 1e-5
+    x[:, 17] = 100.0
+    d["x"] = x.to(d["x"].dtype)
+    check(s, d, call(s, d, pack(s, d, dtype)), 2)
+    d = make(s, dtype, seed=91)
+    d["bias"] = torch.linspace(0, 8, 16, device="cuda")      # routing weights from 1 to e^-8
+    check(s, d, call(s, d, pack(s, d, dtype)), 2)
+
+
+def test_fewest_levels():
+    """So many rows that only the unscaled ones fit below 2 GiB."""
+    s = B.Shape(32, 64, 64, 64, 134400, 0, 2)
+    d = make(s, seed=92)
+    check(s, d, call(s, d, pack(s, d)), 2)
+
+
 @pytest.mark.parametrize("std", [1e-3, 1e-7, 30.0])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_mxfp8_rows_of_any_size(std, dtype):
