@@ -379,7 +379,9 @@ int moe_layer_noalloc(const moe_shape* s, const void* x, int x_dtype, const void
  *     activations keep 22 bits of each value or, where that is more, 2^-27 of
  *     the token's largest, expert outputs are not rounded, and out is a float32
  *     result however small the activations are.  (Past T * K * I = 2^31 / 24
- *     not every scale fits, and values may be held to 2^-36 only.)
+ *     not every scale fits, and values may be held to 2^-36 only.)  float32
+ *     rows of x keep 22 bits or 2^-50 of the row's largest value (MXFP8: 24
+ *     bits).
  *   Arguments as in moe_layer(); topk_idx [T, K] int32 and topk_w [T, K]
  *   float32 are optional outputs.  Rows of tokens with no local expert are
  *   written as zeros.  float32 x saturates at 65504 (fp16 parts), as in

@@ -20,6 +20,7 @@ struct FewWs {
     int32_t* idx;
     float* w;
     uint16_t* x;       // parts of float32 rows
+    int* x_exp;        // exponents of those rows' scales
     uint16_t* h;       // parts of the weighted SwiGLU rows, at each level
     float* sums;       // partial sums of the down step
     int* arrived;      // their counters

@@ -80,6 +80,7 @@ typedef double doublex4 __attribute__((ext_vector_type(4)));
 struct FewArgs {
     const uint16_t* a;         // gate/up rows: parts [NP][T][H]
     int64_t a_part;            // elements per part
+    const int* a_exp;          // [T] the parts are of the row times 2^this (two parts)
     const uint8_t* gu;         // packed gate/up weights (16-bit or MXFP8 codes)
     const uint8_t* gu_scales;
     const uint8_t* dn;
@@ -98,6 +99,19 @@ struct FewArgs {
     int S, T, H, E, K, I, e_begin, E_loc;
 };
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
+}
+
+// The largest of a row of 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+    m = max(m, row_rotate<0x128>(m));                  // row_ror:8, :4, :2, :1
+    m = max(m, row_rotate<0x124>(m));
+    m = max(m, row_rotate<0x122>(m));
+    return max(m, row_rotate<0x121>(m));
+}
+
 // ---- route -------------------------------------------------------------------
 
 template <typename XT> __device__ __forceinline__ double widen(XT v);
@@ -112,12 +126,15 @@ template <> __device__ __forceinline__ double widen<float>(float v) { return v; 
 // product.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and k = l / 16;
 // the four k of a group's step j are h = 8 (l / 16) + j.  The products of bf16
 // (float32) inputs are exact in double, so only the additions round.
-// NPX > 0: the first expert column also writes the rows' parts for the gate/up product.
+// NPX > 0: the first expert column also writes the rows' parts for the gate/up
+// product.  Two fp16 parts hold 22 bits of values from 2^-14 on and 2^-36 below, so
+// a row is scaled by a power of two until its largest value lies in [2^14, 2^15):
+// 2^-36 is then 2^-50 of that.  The scale's exponent goes to xe.
 template <typename XT, int NPX, bool F16>
 __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __restrict__ x, const XT* __restrict__ w,
                                                                   int T, int H, int E, double* __restrict__ part,
                                                                   uint16_t* __restrict__ xp, int64_t xp_part,
-                                                                  int* __restrict__ arrived,
+                                                                  int* __restrict__ xe, int* __restrict__ arrived,
                                                                   uint32_t* __restrict__ levels, int level_words) {
     __shared__ double s_red[kRouteNW][4][kWave];
     constexpr int V = 16 / sizeof(XT);                 // elements of a 16-byte load
@@ -133,10 +150,22 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
     const int block = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
     const int threads = gridDim.x * gridDim.y * gridDim.z * (kRouteNW * 64);
     for (int i = block * (kRouteNW * 64) + threadIdx.x; i < level_words; i += threads) levels[i] = 0u;
+    // For the rows' largest values: the waves share out the tile's rows (n of them, span waves each), a wave's first
+    // load goes with those of the products.
+    __shared__ uint32_t s_top[kRowTile];
+    const int n = min(T - static_cast<int>(blockIdx.y) * kRowTile, kRowTile), span = kRouteNW / n;
+    const bool top = F16 && blockIdx.x == 0 && wave < n * span;   // uniform over a wave
+    const XT* row = x + static_cast<int64_t>(blockIdx.y * kRowTile + wave % n) * H;
+    const int h_top = (wave / n * kWave + lane) * V;
+    vec first = {};
+    if constexpr (F16) {
+        if (top && h_top < H) first = *reinterpret_cast<const vec*>(row + h_top);
+        if (threadIdx.x < kRowTile) s_top[threadIdx.x] = 0u;
+    }
     doublex4 acc = {0.0, 0.0, 0.0, 0.0};
+    vec xv[kRouteGroups][8 / V];
     for (int gb = g0; gb < groups; gb += kRouteGroups * step) {
         XT wv[kRouteGroups][8];
-        vec xv[kRouteGroups][8 / V];
 #pragma unroll
         for (int q = 0; q < kRouteGroups; ++q) {
             const int g = gb + q * step;
@@ -157,7 +186,7 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
             for (int j = 0; j < 8; ++j)
                 acc = __builtin_amdgcn_mfma_f64_16x16x4f64(widen<XT>(xv[q][j / V][j % V]), widen<XT>(wv[q][j]), acc, 0,
                                                            0, 0);
-            if constexpr (NPX > 0) {
+            if constexpr (NPX > 0 && !F16) {
                 if (blockIdx.x == 0 && t < T) {
                     const int h0 = (gb + q * step) * 32 + kq * 8;
 #pragma unroll
@@ -174,6 +203,45 @@ __global__ __launch_bounds__(kRouteNW * 64) void few_route_kernel(const XT* __re
 #pragma unroll
     for (int v = 0; v < 4; ++v) s_red[wave][v][lane] = acc[v];
     __syncthreads();
+    if constexpr (F16) {
+        if (top) {
+            float m = 0.0f;
+            auto take = [&](const vec& v) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(v[i]));   // past NaN
+            };
+            take(first);
+#pragma unroll 4
+            for (int h = h_top + span * kWave * V; h < H; h += span * kWave * V)
+                take(*reinterpret_cast<const vec*>(row + h));
+            const uint32_t most = row_max(__float_as_uint(fminf(m, 65504.0f)));
+            if (r == 0) atomicMax(&s_top[wave % n], most);
+        }
+        if (blockIdx.x == 0) __syncthreads();          // uniform over the workgroup
+        if (blockIdx.x == 0 && t < T) {
+            const int exp = 14 + 127 - static_cast<int>(s_top[r] >> 23);
+            if (blockIdx.z == 0 && wave == 0 && kq == 0) xe[t] = exp;
+            const bool held = groups <= step;          // the wave's only group is still in registers
+            for (int g = g0; g < groups; g += step) {
+                const int h0 = g * 32 + kq * 8;
+                const int64_t at = static_cast<int64_t>(t) * H + h0;
+                uint32_t part[NPX][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = held ? xv[0][j / V][j % V] : x[at + j], c = fminf(fmaxf(v, -65504.0f), 65504.0f);
+                    uint16_t q[NPX];
+                    split_parts<NPX, true>(ldexpf(v == v ? c : v, exp), q);
+#pragma unroll
+                    for (int i = 0; i < NPX; ++i) part[i][j] = q[i];
+                }
+#pragma unroll
+                for (int i = 0; i < NPX; ++i)
+                    *reinterpret_cast<u32x4*>(xp + i * xp_part + at) =
+                        u32x4{part[i][0] | part[i][1] << 16, part[i][2] | part[i][3] << 16,
+                              part[i][4] | part[i][5] << 16, part[i][6] | part[i][7] << 16};
+            }
+        }
+    }
     if (threadIdx.x < 256) {
         const int v = threadIdx.x >> 6;
         double s = 0.0;
@@ -206,11 +274,6 @@ __device__ __forceinline__ double unordered(uint64_t u) {
     return __builtin_bit_cast(double, u ^ ((u >> 63) ? (1ull << 63) : ~0ull));
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
-    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
-}
-
 // The better of this lane's (key, index) and the one N lanes on in its row of 16.
 template <int CTRL>
 __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
@@ -224,11 +287,7 @@ __device__ __forceinline__ void row_best(uint64_t& key, int& index) {
 
 // The highest level at which a row's 16 columns, one to each of 16 lanes, stay below 2^15.
 __device__ __forceinline__ int level_of(float v, int top) {
-    uint32_t m = __float_as_uint(fabsf(v));            // ordered as the numbers, NaN above them
-    m = max(m, row_rotate<0x128>(m));
-    m = max(m, row_rotate<0x124>(m));
-    m = max(m, row_rotate<0x122>(m));
-    m = max(m, row_rotate<0x121>(m));
+    const uint32_t m = row_max(__float_as_uint(fabsf(v)));   // ordered as the numbers, NaN above them
     const int room = 127 + 14 - static_cast<int>(m >> 23);
     return room < kLevelBits ? 0 : min(room / kLevelBits, top);
 }
@@ -251,12 +310,7 @@ __device__ __forceinline__ void held_rounds(int E, int K, bool on, uint64_t* min
             key = take ? held[q] : key;
             index = take ? q * 16 + c : index;
         }
-        uint32_t m = static_cast<uint32_t>(key >> 32);
-        const uint32_t own = m;
-        m = max(m, row_rotate<0x128>(m));      // row_ror:8, :4, :2, :1
-        m = max(m, row_rotate<0x124>(m));
-        m = max(m, row_rotate<0x122>(m));
-        m = max(m, row_rotate<0x121>(m));
+        const uint32_t own = static_cast<uint32_t>(key >> 32), m = row_max(own);
         const uint32_t best = static_cast<uint32_t>(__ballot(own == m) >> (lane & 48)) & 0xFFFFu;
         bool win = own == m;
         if (__ballot((best & (best - 1u)) != 0u) != 0ull) {   // some row's upper words agree
@@ -483,6 +537,12 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
         }
     build_tables(tb, p);
 
+    // the token that this thread finishes: a unit's thread -> (row tile, register, lane), row 4 (lane / 16) + register,
+    // column lane % 16
+    const int token = (tid >> 8) * kRowTile + (lane >> 4) * 4 + ((tid >> 6) & 3);
+    int a_exp = 0;
+    if constexpr (NP == 2)
+        if (token < p.T) a_exp = p.a_exp[token];
     const int nb = p.I / kRowTile;                     // units per expert
     const int units = *tb.count * nb;
     const int nk = p.H / 64;                           // steps of a unit
@@ -535,16 +595,18 @@ __global__ __launch_bounds__(kNW * 64, gate_up_waves(NP, MX, MT)) void few_gate_
 #pragma unroll
                 for (int v = 0; v < 4; ++v) s_red[wave][m][c][v][lane] = acc.value(m, c, v);
         lds_barrier();
-        // thread -> (row tile, register, lane): row 4 (lane / 16) + register, column lane % 16
         if (tid < MT * 256) {
             const int a = done / nb, u = done - a * nb;
-            const int m = tid >> 8, v = (tid >> 6) & 3;
-            const int t = m * kRowTile + (lane >> 4) * 4 + v;
+            const int m = tid >> 8, v = (tid >> 6) & 3, t = token;
             float g = 0.0f, up = 0.0f;
 #pragma unroll
             for (int q = 0; q < kNW; ++q) {
                 g += s_red[q][m][0][v][lane];
                 up += s_red[q][m][1][v][lane];
+            }
+            if constexpr (NP == 2) {
+                g = ldexpf(g, -a_exp);
+                up = ldexpf(up, -a_exp);
             }
             const int j = t < p.T ? tb.slot[a * p.T + t] : -1;
             if (j >= 0) {
@@ -1004,6 +1066,7 @@ size_t few_tokens_workspace(const moe_shape& s, void* base, FewWs* w) {
     z.idx = reinterpret_cast<int32_t*>(take(pairs * 4));
     z.w = reinterpret_cast<float*>(take(pairs * 4));
     z.x = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(3) * s.T * s.H * 2));
+    z.x_exp = reinterpret_cast<int*>(take(static_cast<size_t>(s.T) * 4));
     const size_t h_parts = std::max(3, 2 * (top_level(s) + 1));    // three (MXFP8), or two at each level
     z.h = reinterpret_cast<uint16_t*>(take(h_parts * pairs * s.I * 2));
     z.sums = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxParts) * s.T * s.H * 4));
@@ -1040,6 +1103,7 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     p.top = top_level(s);
     p.a = x_dtype == MOE_BF16 ? static_cast<const uint16_t*>(x) : z.x;
     p.a_part = static_cast<int64_t>(s.T) * s.H;
+    p.a_exp = z.x_exp;
     const uint8_t* b = static_cast<const uint8_t*>(packed);
     p.gu = b;
     if (mx) {
@@ -1052,16 +1116,16 @@ int launch_few_tokens(const moe_shape& s, const void* x, int x_dtype, const void
     const dim3 g((s.E + kRowTile - 1) / kRowTile, (s.T + kRowTile - 1) / kRowTile, p.S), block(kRouteNW * 64);
     if (x_dtype == MOE_BF16)
         hipLaunchKernelGGL((few_route_kernel<uint16_t, 0, false>), g, block, 0, st, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
-                           z.levels, mx ? 0 : level_words + 1);
+                           static_cast<const uint16_t*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part,
+                           z.x_exp, z.arrived, z.levels, mx ? 0 : level_words + 1);
     else if (mx)
         hipLaunchKernelGGL((few_route_kernel<float, 3, false>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
-                           z.levels, mx ? 0 : level_words + 1);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part,
+                           z.x_exp, z.arrived, z.levels, mx ? 0 : level_words + 1);
     else
         hipLaunchKernelGGL((few_route_kernel<float, 2, true>), g, block, 0, st, static_cast<const float*>(x),
-                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part, z.arrived,
-                           z.levels, mx ? 0 : level_words + 1);
+                           static_cast<const float*>(w_router), s.T, s.H, s.E, z.part, z.x, p.a_part,
+                           z.x_exp, z.arrived, z.levels, mx ? 0 : level_words + 1);
     MOE_CHECK_LAUNCH();
     MOE_TRY(s.T <= kRowTile ? launch_gate_up<1>(p, x_dtype, mx, st) : launch_gate_up<2>(p, x_dtype, mx, st));
     const int parts = down_parts(s, mx);

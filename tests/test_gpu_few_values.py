@@ -88,7 +88,7 @@ SHAPES = [(1, 64, 4, 1, 64, 0, 4), (3, 256, 16, 4, 256, 2, 14), (8, 512, 64, 8, 
 
 
 @pytest.mark.parametrize("shape", SHAPES)
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("std", [1e-2, 1e-3, 1e-4, 1e-7, 1e-12, 30.0])
 def test_rows_of_any_size(shape, dtype, std):
     """x of std 1e-12 makes rows of 1e-25 and smaller."""
@@ -99,7 +99,7 @@ def test_rows_of_any_size(shape, dtype, std):
 
 
 @pytest.mark.parametrize("T", [1, 7, 12, 32])
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_of_every_size_together(T, dtype):
     """A call whose tokens lie 2^46 apart, a zero row among them, and experts whose weights shrink their rows."""
     s = B.Shape(T, 256, 24, 4, 256, 1, 23)
@@ -112,7 +112,7 @@ def test_rows_of_every_size_together(T, dtype):
     check(s, d, call(s, d, pack(s, d, dtype)), 2)
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_large_value_in_a_small_row(dtype):
     """One large x in a row of small ones, and one expert's row far above the others of its token."""
     s = B.Shape(6, 512, 16, 4, 256, 0, 16)
