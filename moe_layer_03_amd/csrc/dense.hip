@@ -28,23 +28,56 @@ struct DenseArgs {
 
 // ---- epilogue ------------------------------------------------------------------
 
-// v / (1 + exp(-c v')): the hardware's exp2 and reciprocal, an ulp each, and the
-// rounding of the exponent, (|v'| + 3) 2^-24 of the result in all.  (With expf and
-// a division, 6000 x 4096 x 4096 with bias and SiLU took 206 us; so 196.)  The
-// reciprocal underflows below v' = -87, where the result is under 1e-36: zero.
-__device__ __forceinline__ float over_one_plus_exp(float v, float minus_x_log2e) {
-    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(minus_x_log2e));
+// v / (1 + exp(-y)).  16-bit outputs take the hardware's exp2 and reciprocal (6000 x
+// 4096 x 4096 with bias and SiLU to bf16 186 us, against 199 for the float32 form
+// below and output): an ulp each, which is 2 u (u = 2^-24), one rounding in 1 + e and one in the
+// product are 6 u, and the exponent's own roundings, 1.3 |y| u, make (1.3 |y| + 6) u
+// of the result, against half a step of 2^16 u (bf16) or 2^13 u (fp16).  The
+// reciprocal underflows below y = -87, where the result is under 1e-36: zero.
+__device__ __forceinline__ float over_one_plus_exp_fast(float v, float y) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * y));
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {                                     // uniform
-        case MOE_EPI_SILU: return over_one_plus_exp(v, v * -1.4426950408889634f);
-        case MOE_EPI_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-        // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)): no cancellation for negative z
+// The same for float32 outputs.  exp(-y) = 2^(-y / ln 2), whose product's rounding
+// and the constant's own are put back to first order (3 u with the last rounding),
+// the sum, a Newton step of the reciprocal and the product round once each: 6 u.
+// Far below zero it is v exp(y), in two factors (6 u), down to float32's last digit.
+__device__ __forceinline__ float over_one_plus_exp(float v, float y) {
+    if (y < -80.0f) {
+        const float e = expf(0.5f * y);
+        return v * e * e;
+    }
+    constexpr float kLog2e = 1.4426950408889634f, kRest = static_cast<float>(1.4426950408889634 - kLog2e);
+    const float z = -fminf(y, 128.0f), x = z * kLog2e;      // 1 + exp(-128) is 1, and y may be infinite
+    const float lost = fmaf(z, kLog2e, -x) + z * kRest;
+    float e = __builtin_amdgcn_exp2f(x);
+    e = fmaf(e, lost * 0.69314718055994531f, e);
+    const float s = 1.0f + e, r = __builtin_amdgcn_rcpf(s);
+    return v * fmaf(r, fmaf(-s, r, 1.0f), r);
+}
+
+// N values at once.  tanh-GELU is v / (1 + exp(-2 z)), without (1 + tanh z)'s
+// cancellation for negative z; y = 2 z has seven roundings, 7 |y| u of the result.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act, bool fast) {
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = f(v[i]);
+    };
+    auto tanh_y = [](float x) { return 1.5957691216057308f * (x + 0.044715f * x * x * x); };
+    switch (act) {                                     // uniform, as fast is
+        case MOE_EPI_SWIGLU:                           // the gate's
+        case MOE_EPI_SILU:
+            if (fast) each([](float x) { return over_one_plus_exp_fast(x, x); });
+            else each([](float x) { return over_one_plus_exp(x, x); });
+            break;
+        case MOE_EPI_GELU: each([](float x) { return 0.5f * x * erfcf(x * -0.70710678118654752f); }); break;
         case MOE_EPI_GELU_TANH:
-            return over_one_plus_exp(v, -2.3022081981443250f * (v + 0.044715f * v * v * v));
-        case MOE_EPI_RELU: return v < 0.0f ? 0.0f : v;       // NaN stays
-        default: return v;
+            if (fast) each([&](float x) { return over_one_plus_exp_fast(x, tanh_y(x)); });
+            else each([&](float x) { return over_one_plus_exp(x, tanh_y(x)); });
+            break;
+        case MOE_EPI_RELU: each([](float x) { return x < 0.0f ? 0.0f : x; }); break;   // NaN stays
+        default: break;
     }
 }
 
@@ -64,11 +97,12 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v)
 __device__ __forceinline__ void finish(const DenseArgs& p, int row, int col, float v, float u) {
     if (row >= p.M || col >= p.N) return;
     if (p.bias != nullptr) v += p.bias[col];
+    float g[1] = {v};
+    activate(g, p.act, p.c_dtype != MOE_F32);
+    v = g[0];
     if (p.gated) {
         if (p.bias != nullptr) u += p.bias[p.N + col];
-        v = activate(v, MOE_EPI_SILU) * u;
-    } else {
-        v = activate(v, p.act);
+        v *= u;
     }
     if (p.r != nullptr) v += load_as(p.r, row * p.ldr + col, p.r_dtype);
     store_as(p.c, row * p.ldc + col, p.c_dtype, v);
@@ -80,13 +114,10 @@ __device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, fl
                                         const floatx4& b0, const floatx4& b1) {
     if (row >= p.M || col >= p.N) return;
     v += b0;
-    if (p.gated) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], MOE_EPI_SILU) * (u[i] + b1[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], p.act);
-    }
+    float g[4] = {v[0], v[1], v[2], v[3]};
+    activate(g, p.act, p.c_dtype != MOE_F32);
+    v = floatx4{g[0], g[1], g[2], g[3]};
+    if (p.gated) v *= u + b1;
     const bool whole = col + 4 <= p.N;
     if (p.r != nullptr) {
         const int64_t at = row * p.ldr + col;

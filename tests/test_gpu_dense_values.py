@@ -1,5 +1,7 @@
-"""What the dense product does at the ends of its types: NaN of every payload, the 16-bit rounding.  A is zero, so that
-the sum is the bias and the residual exactly."""
+"""What the dense product does at the ends of its types: NaN of every payload, the 16-bit rounding, float32 activations
+far from zero.  A is zero, so that the sum is the bias and the residual exactly."""
+import math
+
 import pytest
 import torch
 
@@ -8,6 +10,7 @@ from moe_layer_03_amd import binding as B
 pytestmark = pytest.mark.gpu
 
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+U = 2.0 ** -24
 # M, N, K, extra elements per row of A: weight streaming (16-byte rows and others), tiles, any alignment
 SIZES = [(3, 70, 64, 0), (20, 132, 65, 0), (130, 260, 64, 0), (700, 128, 264, 0), (600, 100, 65, 0)]
 NANS = [0x7FC00000, 0x7FFFFFFF, 0x7F800001, 0xFFC00000, 0xFFFFFFFF, 0xFF800001]
@@ -72,3 +75,28 @@ def test_rounding_to_16_bits(size, c):
     got = zero_product(M, N, K, pad, residual=r, c_dtype=TYPES[c])
     r = r.cpu() if c == "bf16" else r.cpu().clamp(-65504, 65504)
     assert torch.equal(got.cpu(), r.to(TYPES[c]))
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "swiglu"])
+def test_float32_activations(size, act):
+    """v / (1 + exp(-y)) to a few units of float32 (u = 2^-24) wherever it is a normal number.
+
+    An exponential to an ulp (2 u) with a rounding, the sum, the reciprocal and the product: 6 u; below y = -80 exp(y) is
+    taken as two factors exp(y / 2), 2 u each, with two products: 6 u (SwiGLU's product one more).  SiLU's y is v itself;
+    tanh-GELU's y = c (v + d v^3) has seven roundings, of which exp makes 7 u |y|."""
+    M, N, K, pad = size
+    gated = act == "swiglu"
+    v = torch.linspace(-100, 40, N) if act != "gelu_tanh" else torch.linspace(-11, 5, N)
+    bias = torch.stack([v, torch.full((N,), 0.75)] if gated else [v]).cuda()
+    s = B.DenseShape(M, N, K, gated=gated)
+    a = torch.zeros((M, K + pad), dtype=torch.bfloat16, device="cuda")[:, :K]
+    w = torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    epi = {"silu": B.MOE_EPI_SILU, "gelu_tanh": B.MOE_EPI_GELU_TANH, "swiglu": B.MOE_EPI_SWIGLU}[act]
+    got = B.moe_dense_gemm(s, a, B.moe_pack_dense(s, w, w if gated else None), epi, bias=bias, c_dtype=torch.float32)
+    x = bias[0].double()
+    y = math.sqrt(8 / math.pi) * (x + 0.044715 * x ** 3) if act == "gelu_tanh" else x
+    ref = x * torch.where(y < -30, torch.exp(y) / (1 + torch.exp(y)), 1 / (1 + torch.exp(-y))) * (0.75 if gated else 1)
+    units = (6 + gated + (7 * y.abs() if act == "gelu_tanh" else 0)) * 1.01     # 1.01: products of the small terms
+    # below the normal numbers a result is off by its own spacing, times at most one more factor
+    assert ((got.double() - ref).abs() <= units * U * ref.abs() + 2.0 ** -148).all()
