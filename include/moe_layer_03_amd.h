@@ -428,7 +428,7 @@ typedef struct moe_dense_shape {
     int32_t gated;       /* 1: gate and up weights, MOE_EPI_SWIGLU; 0: one weight, any other epilogue */
 } moe_dense_shape;
 
-/* Bytes of the packed weights of (N, K, gated); M does not matter (host-only). */
+/* Bytes of the packed weights of (N, K, gated); any M, here and in moe_pack_dense() (host-only). */
 size_t moe_packed_dense_bytes(const moe_dense_shape* s);
 
 /*

@@ -202,12 +202,19 @@ int layer_few_tokens(const moe_shape* s, const void* x, int x_dtype, const void*
                              static_cast<hipStream_t>(stream));
 }
 
+// The weights of a dense product, whatever M: the grid's limit is 65535 groups of 8 k.
+int check_dense_weights(const moe_dense_shape* s) {
+    if (s == nullptr || s->N < 1 || s->K < 1) return MOE_ERR_INVALID_ARG;
+    if (s->gated != 0 && s->gated != 1) return MOE_ERR_INVALID_ARG;
+    if (s->N > MOE_DENSE_MAX_COLS || s->K > MOE_DENSE_MAX_COLS) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
 // Dense products: the grid's limits are 2^31 - 1 column pairs and 65535 x 64 rows.
 int check_dense_shape(const moe_dense_shape* s) {
-    if (s == nullptr || s->M < 0 || s->N < 1 || s->K < 1) return MOE_ERR_INVALID_ARG;
-    if (s->gated != 0 && s->gated != 1) return MOE_ERR_INVALID_ARG;
-    if (s->M > MOE_DENSE_MAX_ROWS || s->N > MOE_DENSE_MAX_COLS || s->K > MOE_DENSE_MAX_COLS) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
+    if (s == nullptr || s->M < 0) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_dense_weights(s));
+    return s->M > MOE_DENSE_MAX_ROWS ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 }  // namespace
@@ -527,12 +534,12 @@ int moe_layer_few_tokens_mxfp8(const moe_shape* s, const void* x, int x_dtype, c
 }
 
 size_t moe_packed_dense_bytes(const moe_dense_shape* s) {
-    if (check_dense_shape(s) != MOE_OK) return 0;
+    if (check_dense_weights(s) != MOE_OK) return 0;
     return dense_packed_bytes(*s);
 }
 
 int moe_pack_dense(const moe_dense_shape* s, const void* w, const void* w_up, int dtype, void* packed, void* stream) {
-    MOE_TRY(check_dense_shape(s));
+    MOE_TRY(check_dense_weights(s));
     if (!out_dtype_ok(dtype)) return MOE_ERR_UNSUPPORTED;
     const size_t align = dtype == MOE_F32 ? 4 : 2;
     if (w == nullptr || !aligned(w, align) || !ok16(packed)) return MOE_ERR_INVALID_ARG;

@@ -63,3 +63,15 @@ def test_binding_refuses_host_tensors():
         B.moe_dense_gemm(s, torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(64 * 64 * 2, dtype=torch.uint8))
     with pytest.raises(ValueError):
         B.moe_dense_gemm(s, torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(64, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("M", [-1, -(1 << 31), (1 << 21) + 1, (1 << 31) - 1])
+def test_weights_do_not_depend_on_the_rows(M):
+    """The size query and the packer look at N, K and gated only; the product refuses such an M."""
+    assert B.moe_packed_dense_bytes(B.DenseShape(M, 65, 1)) == 128 * 64 * 2
+    s = B._CDenseShape(M, 40, 64, 0)
+    pack = B.load().moe_pack_dense
+    # what comes after the shape is what is refused, before any HIP call
+    assert pack(ctypes.byref(s), P, None, B.MOE_MXFP8, P, None) == UNS
+    assert pack(ctypes.byref(s), None, None, B.MOE_BF16, P, None) == BAD
+    assert _gemm(M=M) == (BAD if M < 0 else UNS)

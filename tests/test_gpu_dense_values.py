@@ -82,9 +82,9 @@ def test_rounding_to_16_bits(size, c):
 def test_float32_activations(size, act):
     """v / (1 + exp(-y)) to a few units of float32 (u = 2^-24) wherever it is a normal number.
 
-    An exponential to an ulp (2 u) with a rounding, the sum, the reciprocal and the product: 6 u; below y = -80 exp(y) is
-    taken as two factors exp(y / 2), 2 u each, with two products: 6 u (SwiGLU's product one more).  SiLU's y is v itself;
-    tanh-GELU's y = c (v + d v^3) has seven roundings, of which exp makes 7 u |y|."""
+    An exponential to an ulp (2 u) with a rounding, the sum, the reciprocal and the product: 6 u; below y = -80 exp(y)
+    is taken as two factors exp(y / 2), 2 u each, with two products: 6 u (SwiGLU's product one more).  SiLU's y is v
+    itself; tanh-GELU's y = c (v + d v^3) has seven roundings, of which exp makes 7 u |y|."""
     M, N, K, pad = size
     gated = act == "swiglu"
     v = torch.linspace(-100, 40, N) if act != "gelu_tanh" else torch.linspace(-11, 5, N)
