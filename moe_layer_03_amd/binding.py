@@ -687,11 +687,13 @@ def moe_dense_gemm(d: DenseShape, a: torch.Tensor, packed: torch.Tensor, epilogu
                    stream=None) -> torch.Tensor:
     """act(a @ W + bias) + residual on moe_pack_dense weights (gated: MOE_EPI_SWIGLU, bias [2, N]).
 
-    a [M, K], residual and c [M, N] may have any row stride; c may be residual.  c_dtype defaults to a's."""
+    a [M, K], residual and c [M, N] may have any row stride; c may be residual.  c_dtype is c's, or a's."""
     shape, need = _dense_of(d)
     if packed.numel() < need:
         raise ValueError(f"packed must hold {need} bytes, got {packed.numel()}")
     dev = a.device
+    if c is not None and c_dtype is not None and c.dtype != c_dtype:
+        raise TypeError(f"c is {c.dtype}, c_dtype {c_dtype}")
     if c is None:
         c = _empty((d.M, d.N), c_dtype or a.dtype, dev, stream)
     pa, lda = _rows(a, d.M, d.K, "a")

@@ -75,3 +75,12 @@ def test_weights_do_not_depend_on_the_rows(M):
     assert pack(ctypes.byref(s), P, None, B.MOE_MXFP8, P, None) == UNS
     assert pack(ctypes.byref(s), None, None, B.MOE_BF16, P, None) == BAD
     assert _gemm(M=M) == (BAD if M < 0 else UNS)
+
+
+def test_binding_refuses_an_output_of_another_type():
+    s = B.DenseShape(2, 64, 64)
+    a, packed = torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros(64 * 64 * 2, dtype=torch.uint8)
+    with pytest.raises(TypeError, match="c_dtype"):
+        B.moe_dense_gemm(s, a, packed, c=torch.zeros((2, 64), dtype=torch.float16), c_dtype=torch.float32)
+    with pytest.raises(ValueError, match="GPU"):         # the same type is no conflict: the host tensors are refused
+        B.moe_dense_gemm(s, a, packed, c=torch.zeros((2, 64)), c_dtype=torch.float32)
