@@ -386,8 +386,11 @@ int moe_layer_noalloc(const moe_shape* s, const void* x, int x_dtype, const void
  *   float32 are optional outputs.  Rows of tokens with no local expert are
  *   written as zeros.  float32 x saturates at 65504 (fp16 parts), as in
  *   moe_layer(); so do the weighted SwiGLU activations.
- *   A NaN in x makes its token's outputs NaN and reaches no other token; an
- *   infinite or NaN weight may reach tokens that did not choose its expert.
+ *   A NaN in x makes its token's logits NaN, which choose K experts like any
+ *   others: the token's outputs are NaN on the ranks that hold one of them and
+ *   zeros on the rest, so the sum over the ranks is NaN.  It reaches no other
+ *   token; an infinite or NaN weight may reach tokens that did not choose its
+ *   expert.
  *   ws: moe_layer_few_tokens_workspace_bytes(s) bytes of device scratch, any
  *   contents; calls that overlap in time need workspaces of their own.
  *   T > MOE_FEW_TOKENS_MAX, or T * K * I or T * H beyond 2^31 / 6:

@@ -166,3 +166,22 @@ def test_every_nan_stays_in_its_token(nan, mx):
     got = call(s, d, pack(s, d, "f32", mx), mx)
     assert torch.isnan(got[2]).all()
     assert torch.isfinite(got[[0, 1, 3, 4]]).all()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_nan_over_the_shards(mx):
+    """A token whose logits are NaN chooses K experts like any other: the ranks that hold one of them write NaN, the
+    rest zeros, and the sum over the ranks is NaN."""
+    full = B.Shape(5, 256, 24, 4, 256, 0, 24)
+    d = make(full, mx=mx, seed=98)
+    d["x"][2, 5] = math.nan
+    idx = torch.empty((5, 4), dtype=torch.int32, device="cuda")
+    total = torch.zeros((5, 256), device="cuda")
+    for b, e in ((0, 2), (2, 9), (9, 24)):
+        s = B.Shape(5, 256, 24, 4, 256, b, e)
+        part = dict(d, **{k: d[k][b:e].contiguous() for k in ("gate", "up", "down")})
+        got = call(s, part, pack(s, part, mx=mx), mx, topk_idx=idx)
+        here = ((idx[2] >= b) & (idx[2] < e)).any().item()
+        assert torch.isnan(got[2]).all() if here else (got[2] == 0).all()
+        total += got
+    assert torch.isnan(total[2]).all() and torch.isfinite(total[[0, 1, 3, 4]]).all()
