@@ -1014,9 +1014,12 @@ size_t down_lds(const moe_shape& s) {
 template <int NP, bool F16, bool MX>
 int launch_down(const FewArgs& p, int parts, size_t lds, hipStream_t st) {
     const dim3 g(p.H / kRowTile, parts), block(kNW * 64);
-    // one tile of MFMA rows while the tokens, or the rows an evenly routed expert gets, fit its segments about twice over
+    // One tile of MFMA rows while the tokens fit it, or an evenly routed expert gets at most half of its rows; with more
+    // rows to an expert, two tiles save reading its weights again.  Hidden 4096, expert 1536, one tile and two: 16 tokens
+    // to 4 of 32 experts (2 rows each) 178 and 182 us, of 16 (4) 108.7 and 110.9, of 12 (5.3) 90.1 and 90.0, of 8 (8)
+    // 68.9 and 66.3; MXFP8, with half the rows to a tile, 16 tokens to 4 of 32 (2) 127 and 136, of 16 (4) 91.6 and 89.2.
     constexpr int RV = RowMap<NP, 1>::RV;
-    const bool narrow = p.T <= RV || (p.T > RowMap<NP, 2>::RV && p.T * p.K <= p.E * RV / 2);
+    const bool narrow = p.T <= RV || p.T * p.K <= p.E * RV / 2;
     if (narrow) hipLaunchKernelGGL((few_down_kernel<NP, F16, MX, 1>), g, block, lds, st, p);
     else hipLaunchKernelGGL((few_down_kernel<NP, F16, MX, 2>), g, block, lds, st, p);
     MOE_CHECK_LAUNCH();

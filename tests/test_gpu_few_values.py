@@ -185,3 +185,14 @@ def test_nan_over_the_shards(mx):
         assert torch.isnan(got[2]).all() if here else (got[2] == 0).all()
         total += got
     assert torch.isnan(total[2]).all() and torch.isfinite(total[[0, 1, 3, 4]]).all()
+
+
+@pytest.mark.parametrize("shape", [(4, 8, 8), (8, 8, 8), (6, 8, 4), (12, 8, 8), (12, 64, 4), (16, 8, 3), (16, 32, 8),
+                                   (32, 8, 8), (32, 64, 4)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_down_tiles(shape, mx):
+    """T, E, K: one MFMA tile and two, rows that are the tokens throughout and rows by segments."""
+    T, E, K = shape
+    s = B.Shape(T, 256, E, K, 512, 0, E)
+    d = make(s, mx=mx, seed=100 + T)
+    check(s, d, call(s, d, pack(s, d, mx=mx), mx), 3 if mx else 2)
