@@ -172,8 +172,8 @@ __device__ __forceinline__ u32x4 load_tail(const uint16_t* row, int k, int K) {
 // 16 columns of each half.  Direct copies to LDS need aligned rows, so A goes
 // through registers, and a stage is 128 k long to have as few waits as possible:
 // the next stage's rows and weights are on their way while one is multiplied.
-// Bound by the latency of a stage, 1.65 us: 283 x 1516 x 1396 16.5 us (a library
-// product of the same sizes 14.7).
+// Bound by the latency of a stage, 1.65 us: 283 x 1516 x 1396 18.4 us (streaming,
+// which the rule takes there, 18.8; 500 x 515 x 2011 28.5 and 26.1).
 constexpr int kAnyK = 128;
 constexpr int kAnyLd = kAnyK + 8;                      // LDS row, 16 of them in distinct banks
 
@@ -411,13 +411,14 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
 // M and k past K copy zeros.
 //
 // Bound by the matrix unit at the clock the power limit leaves it (random inputs
-// hold 1.7 GHz; zeros run a fifth faster): 8192^3 851 us, 1292 TFLOP/s (a library product 775 to
-// 812); 6000 x 4096 x 4096 195 us, 1035 TFLOP/s (167), 192 x 256 tiles, of which
-// 512 fill the chip exactly twice.  Besides the clock LDS bounds it: a stage of
-// the 256 x 256 tile reads 96 KB and copies 32 KB while the MFMAs take 1024
+// hold 1.7 GHz; zeros run a fifth faster): 8192^3 833 us, 1320 TFLOP/s (a library
+// product 792); 6000 x 4096 x 4096 182 us, 1106 TFLOP/s (164), with bias and SiLU
+// 186 (164 and two passes over C: 207), 192 x 256 tiles, of which 512 fill the chip
+// exactly twice.  Besides the clock LDS bounds it: a stage of the 256 x 256 tile
+// reads 96 KB and copies 32 KB while the MFMAs take 1024
 // cycles (without the MFMAs 685 us, without the copies 775, then 899 in all).
-// Tried at 8192^3: 4 waves of 128 x 128 each 897 us, weights straight to registers
-// 893, copies issued in the multiplying phase 929.
+// Tried at 8192^3, then 851 us: 4 waves of 128 x 128 each 897 us, weights straight
+// to registers 893, copies issued in the multiplying phase 929.
 constexpr int kTileNB = 4;
 constexpr int kTileBK = 32;
 

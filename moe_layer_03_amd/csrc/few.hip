@@ -8,8 +8,8 @@
 // With so few rows the layer is bound by reading the chosen experts' weights
 // once: 6 H I bytes per expert (16-bit) against 6 H I operations per row.
 //
-// Three launches (hidden 4096, expert 1536, top 8 of 128, one token: 5.0, 40.2
-// and 20.4 us with 16-bit weights, 4.6, 26.7 and 16.5 us with MXFP8; 62 and 47 us
+// Three launches (hidden 4096, expert 1536, top 8 of 128, one token: 4.9, 39.6
+// and 20.5 us with 16-bit weights, 4.6, 27.3 and 16.6 us with MXFP8; 63 and 47 us
 // in all, where the weights alone take 46 and 24 at 6.6 TB/s):
 //   route    partial logits over slices of H, double-precision MFMA;
 //   gate/up  every workgroup sums the partials and selects the experts itself
@@ -71,7 +71,9 @@ constexpr int kMaxParts = 8;
 // they stay below 2^15: level 0 always, and no other where one is 2^-9 or more, as
 // rows commonly have.  The down step takes the highest level that all units of the
 // token have.  Its largest value there is 2^-9 or more, and 2^-36 at most 2^-27 of
-// it, for any largest value that float32 holds.
+// it, for any largest value that float32 holds.  Small rows cost the writing and the
+// reading of their levels: inputs of 1e-3 instead of 1, one token 64.6 us against
+// 62.7, 32 tokens 726 against 699.
 constexpr int kLevelBits = 24;
 constexpr int kLevels = 6;
 
@@ -119,8 +121,10 @@ template <> __device__ __forceinline__ double widen<uint16_t>(uint16_t v) { retu
 template <> __device__ __forceinline__ double widen<float>(float v) { return v; }
 
 // Bound by latency: one round of loads, at most 16 double-precision MFMAs per wave
-// and a reduction through LDS, 3.4 us (tiny) to 6.2 (32 tokens of 4096 to 128
-// experts, 1 MB of router weights) of which an empty launch takes 1.6.
+// and a reduction through LDS, 4.9 us (one token of 4096 to 128 experts, 1 MB of
+// router weights) to 6.1 (32), of which an empty launch takes 1.6.  float32 rows
+// and weights are twice the bytes and have their parts to write: 5.4 us (one token)
+// to 15.7 (16), and 21.3 (13) with the MXFP8 form's three parts.
 // One workgroup: 16 experts x 16 tokens x one slice of H; its waves take 32-h
 // groups in turn, at most kRouteGroups each, all loads issued before the first
 // product.  v_mfma_f64_16x16x4: lane l holds row (column) l % 16 and k = l / 16;
@@ -485,8 +489,8 @@ __device__ __forceinline__ void build_tables(const Tables& s, const FewArgs& p) 
 
 // ---- gate and up ------------------------------------------------------------------
 // Bound by the weights' arrival once the launch has started and selected (about
-// 5 us): 32 tokens, who choose 111 of 128 experts, read 2.8 GB in 444 us (6.3
-// TB/s); one token 201 MB in 40.2 us (5.0), with MXFP8 104 MB in 26.7 (3.9).
+// 5 us): 32 tokens, who choose 111 of 128 experts, read 2.8 GB in 443 us (6.3
+// TB/s); one token 201 MB in 39.6 us (5.1), with MXFP8 104 MB in 27.3 (3.8).
 // An even number of units for every workgroup (384 of them, two each, for 768
 // units) was slower than 512 workgroups of which half take two: 53 us against 47
 // for the MXFP8 layer.
@@ -852,8 +856,8 @@ struct DownCursor {
 };
 
 // Bound as gate/up is, behind the segments' tables (about 3 us) and the handing
-// over of partial sums (3 us): 32 tokens 1.4 GB in 222 us (6.4 TB/s), one token
-// 101 MB in 20.4 us (4.9), with MXFP8 52 MB in 16.5 (3.1).
+// over of partial sums (3 us): 32 tokens 1.4 GB in 220 us (6.4 TB/s), one token
+// 101 MB in 20.5 us (4.9), with MXFP8 52 MB in 16.6 (3.1).
 // A workgroup owns 16 output columns and part blockIdx.y of the steps, each wave a
 // contiguous run of them.  A wave adds its rows' sums to its own [T][16] in LDS
 // where the segment ends (or once at its end, where MFMA rows are tokens all
@@ -863,7 +867,9 @@ struct DownCursor {
 template <int NP, bool F16, bool MX, int RT>
 __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
     typedef RowMap<NP, RT> Map;
-    constexpr int D = MX ? (RT == 1 ? 6 : 4) : (RT == 1 ? 4 : 3);   // steps in flight, 1 KiB (MXFP8) or 2 of weights each
+    // Steps in flight, 1 KiB (MXFP8) or 2 of weights each.  Not a close choice: from three on, calls of one to 32
+    // tokens took the same within 1 %; fewer cost 8 MXFP8 tokens 2 % (212 us, 207), more would spill registers.
+    constexpr int D = MX ? (RT == 1 ? 6 : 4) : (RT == 1 ? 4 : 3);
     extern __shared__ __attribute__((aligned(16))) char smem[];
     float* s_out = reinterpret_cast<float*>(smem);     // [kNW][T][16]
     const Segments sg = carve_segments(smem + kNW * p.T * 64, p);
@@ -945,12 +951,14 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
         }
         return;
     }
-    // Partial sums and the counter move by agent-scope relaxed atomics, which act
-    // where all workgroups see them, past the caches that XCDs do not share.  A
-    // thread's stores are complete once its vector-memory counter is zero, so
-    // with that wait and the barrier before the count, the workgroup that counts
-    // last reads complete sums.  (A release or acquire at agent scope would write
-    // back and invalidate a whole L2 per workgroup: 8 to 12 us here.)
+    // Partial sums and the counter move by agent-scope relaxed atomics.  What orders
+    // them is not the language's memory model (relaxed atomics have no order) but
+    // two properties of gfx950: the vector-memory counter counts an agent-scope store
+    // as outstanding until it is where every XCD sees it, and an agent-scope load
+    // issued after that returns no older copy.  With the wait for the counter and
+    // the barrier before the count, the workgroup that counts last reads complete
+    // sums.  (A release or acquire at agent scope would write back and invalidate a
+    // whole L2 per workgroup: 8 to 12 us here.)
     for (int i = tid; i < cells; i += kNW * 64) {
         float s = 0.0f;
 #pragma unroll
@@ -977,7 +985,10 @@ __global__ __launch_bounds__(kNW * 64, 4) void few_down_kernel(FewArgs p) {
 
 // Slices of H in the route step: few enough that a wave has at most
 // kRouteGroups groups in flight at once and that every gate/up workgroup adds
-// them up quickly; one or two tokens take more, as their partials are short.
+// them up quickly; up to eight tokens take twice as many, as their partials are
+// short.  The layer with 8 of 128 experts of hidden 4096, more slices and fewer:
+// one token 24.5 and 24.8 us, 4 tokens 32.6 and 33.0, 8 tokens 36.0 and 35.5, 9
+// tokens 45.5 and 43.9, 32 tokens 75.0 and 69.0.
 int route_slices(int T, int H) {
     const int groups = H / 32;
     const int most = (groups + kRouteNW - 1) / kRouteNW;           // one group a wave
@@ -1014,10 +1025,10 @@ size_t down_lds(const moe_shape& s) {
 template <int NP, bool F16, bool MX>
 int launch_down(const FewArgs& p, int parts, size_t lds, hipStream_t st) {
     const dim3 g(p.H / kRowTile, parts), block(kNW * 64);
-    // One tile of MFMA rows while the tokens fit it, or an evenly routed expert gets at most half of its rows; with more
-    // rows to an expert, two tiles save reading its weights again.  Hidden 4096, expert 1536, one tile and two: 16 tokens
-    // to 4 of 32 experts (2 rows each) 178 and 182 us, of 16 (4) 108.7 and 110.9, of 12 (5.3) 90.1 and 90.0, of 8 (8)
-    // 68.9 and 66.3; MXFP8, with half the rows to a tile, 16 tokens to 4 of 32 (2) 127 and 136, of 16 (4) 91.6 and 89.2.
+    // One tile of MFMA rows while the tokens fit it, or an evenly routed expert gets at most half of its rows; with
+    // more rows to an expert, two tiles save reading its weights again.  Hidden 4096, expert 1536, one tile and two: 16
+    // tokens to 4 of 32 experts (2 rows each) 178 and 182 us, of 16 (4) 108.7 and 110.9, of 12 (5.3) 90.1 and 90.0, of
+    // 8 (8) 68.9 and 66.3; MXFP8, half the rows to a tile, to 4 of 32 (2) 127 and 136, of 16 (4) 91.6 and 89.2.
     constexpr int RV = RowMap<NP, 1>::RV;
     const bool narrow = p.T <= RV || p.T * p.K <= p.E * RV / 2;
     if (narrow) hipLaunchKernelGGL((few_down_kernel<NP, F16, MX, 1>), g, block, lds, st, p);

@@ -18,8 +18,9 @@
 // Rows are held as NP 16-bit parts whose sum is the row's value:
 //   1 part: the value itself;
 //   2 parts (fp16): v = p0 + 2^-11 p1, |error| <= 2^-22 |v| for 2^-14 <= |v| <=
-//     65504 (p1 is scaled up so that it stays a normal fp16 number); the parts
-//     have their own accumulators, joined at the end;
+//     65504 (p1 is scaled up so that it stays a normal fp16 number), 2^-36 below,
+//     so callers scale rows by a power of two; the parts have their own
+//     accumulators, joined at the end;
 //   3 parts (bf16): v = p0 + p1 + p2, exact for |v| >= 2^-102; one accumulator.
 // The MFMAs of the extra parts are free here: the weights' arrival bounds the
 // product, and a row held to 22 bits or more keeps the float32 output's digits.
