@@ -260,7 +260,7 @@ def _scratch(n, dtype, device, stream=None):
 def _empty(n, dtype, device, stream=None):
     """A result, allocated as scratch is; the caller's stream reads it, so it is not handed on before that has."""
     t = _scratch(n, dtype, device, stream)
-    if stream is not None:
+    if stream is not None and t.is_cuda:               # host tensors are refused by name later
         t.record_stream(torch.cuda.current_stream(device))
     return t
 

@@ -41,7 +41,9 @@ CALLS = {
 
 
 class Recorded(torch.Tensor):
-    """A tensor that notes which streams it is recorded for."""
+    """A tensor that notes which streams it is recorded for, and says that it is on the GPU."""
+    is_cuda = True
+
     def record_stream(self, stream):
         self.recorded = getattr(self, "recorded", []) + [stream]
 
@@ -93,6 +95,14 @@ def test_allocated_on_the_call_s_stream(name, allocations):
     results = {id(v) for v in (r if isinstance(r, tuple) else r.values() if isinstance(r, dict) else (r,))}
     for _, v in allocations:
         assert (id(v) in results) == (getattr(v, "recorded", []) == ["current"])
+
+
+def test_host_tensors_are_refused_with_a_stream_too(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    for call in (lambda: B.moe_layer(S, X, WR, PACKED, stream="side"),
+                 lambda: B.moe_dense_gemm(D, t(4, 64), PACKED, stream="side")):
+        with pytest.raises(ValueError, match="must be a GPU tensor"):
+            call()
 
 
 @pytest.mark.parametrize("name", list(CALLS))
