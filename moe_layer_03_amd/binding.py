@@ -228,11 +228,13 @@ def _stream(stream) -> Optional[int]:
 
 
 def _stream_on(device: torch.device, stream) -> Optional[int]:
-    """The given stream, or the device's current one.  The device has to be the current one, as its kernels are
-    launched there; moving a call to another device is the caller's ``torch.cuda.device``."""
+    """The given stream, or the device's current one.  The device has to be the current one and the stream's, as the
+    kernels are launched there; moving a call to another device is the caller's ``torch.cuda.device``."""
     if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on {device}, the current device is cuda:{torch._C._cuda_getDevice()}")
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"tensors are on {device}, the stream is on {stream.device}")
         return stream.cuda_stream or None
     return torch._C._cuda_getCurrentRawStream(device.index) or None
 

@@ -110,3 +110,15 @@ def test_allocated_on_the_current_stream(name, allocations):
     CALLS[name][0]()
     assert [s for s, _ in allocations] == [None] * CALLS[name][1]
     assert not any(hasattr(v, "recorded") for _, v in allocations)
+
+
+@pytest.mark.parametrize("current,stream,good", [(0, 0, True), (0, 1, False), (1, 0, False)])
+def test_the_stream_is_on_the_tensors_device(current, stream, good, monkeypatch):
+    """Tensors on cuda:0, whatever the current device and the stream's."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current)
+    given = type("Stream", (), {"cuda_stream": 0x40, "device": torch.device("cuda", stream)})()
+    if good:
+        assert B._stream_on(torch.device("cuda", 0), given) == 0x40
+    else:
+        with pytest.raises(ValueError, match="tensors are on cuda:0"):
+            B._stream_on(torch.device("cuda", 0), given)
