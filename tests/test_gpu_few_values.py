@@ -196,3 +196,34 @@ def test_down_tiles(shape, mx):
     s = B.Shape(T, 256, E, K, 512, 0, E)
     d = make(s, mx=mx, seed=100 + T)
     check(s, d, call(s, d, pack(s, d, mx=mx), mx), 3 if mx else 2)
+
+
+@pytest.mark.parametrize("T", [1, 8, 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_small_and_ordinary_rows_in_turn(T, dtype):
+    """One workspace, eager and in a graph, whose calls change between rows that need scales and rows that do not."""
+    s = B.Shape(T, 256, 32, 4, 256, 0, 30)
+    d = make(s, dtype, seed=110 + T)
+    packed = pack(s, d, dtype)
+    x = d["x"].clone()
+    mixed = torch.where(torch.arange(T, device="cuda")[:, None] % 2 == 0, 1.0, 1e-6)
+    inputs = [(x.float() * f).to(x.dtype) for f in (1.0, 1e-5, mixed, 1.0, 1e-9)]
+    refs = [call(s, dict(d, x=v), packed) for v in inputs]
+    ws = torch.empty(B.moe_layer_few_tokens_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    out = torch.empty((T, s.H), device="cuda")
+    args = (s, d["x"], d["w_router"], packed, d["bias"])
+    B.moe_layer_few_tokens(*args, out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_layer_few_tokens(*args, out=out, ws=ws)
+    for v, ref in zip(inputs + inputs, refs + refs):
+        d["x"].copy_(v)
+        out.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+        out.fill_(math.nan)
+        B.moe_layer_few_tokens(*args, out=out, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)

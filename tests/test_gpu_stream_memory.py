@@ -76,3 +76,20 @@ def test_a_result_outlives_its_reader():
         other(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, ref)
+
+
+def test_captured_on_its_own_stream():
+    """A capture whose call names the capturing stream and leaves everything to the binding, replayed between eager
+    calls."""
+    call = calls(False, 65)[1]
+    ref = call()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = call(stream=torch.cuda.current_stream())
+    for _ in range(3):
+        got.fill_(float("nan"))
+        g.replay()
+        assert torch.equal(call(), ref)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
