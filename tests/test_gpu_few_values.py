@@ -133,6 +133,14 @@ def test_fewest_levels():
     check(s, d, call(s, d, pack(s, d)), 2)
 
 
+def test_scaled_rows_up_to_2_gib():
+    """Scaled rows whose offsets come near the end of the range."""
+    s = B.Shape(32, 64, 64, 64, 44800, 0, 2)
+    d = make(s, seed=93)
+    d["x"] = (d["x"].float() * 1e-12).bfloat16()
+    check(s, d, call(s, d, pack(s, d)), 2)
+
+
 @pytest.mark.parametrize("std", [1e-3, 1e-7, 30.0])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_mxfp8_rows_of_any_size(std, dtype):
