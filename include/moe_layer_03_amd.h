@@ -48,11 +48,13 @@ extern "C" {
 #define MOE_ERR_HIP         (-4)   /* a HIP launch failed; see moe_last_hip_error() */
 
 /* Element types.  MOE_F16 appears only for intermediates and GEMM outputs;
- * MOE_MXFP8 only for MXFP8 GEMM outputs (codes plus scales, see below). */
+ * MOE_MXFP8 only for MXFP8 GEMM outputs and normed rows (codes plus scales,
+ * see below). */
 #define MOE_F32   0
 #define MOE_BF16  1
 #define MOE_F16   2
 #define MOE_MXFP8 3
+#define MOE_I8    4   /* int8 codes with float32 scales (the int8 entry points) */
 
 /* Grouped-GEMM operand selector and epilogues. */
 #define MOE_GEMM_GATE_UP 0   /* A = packed tokens [*, H], B = gate and up weights of each expert  */
@@ -466,6 +468,87 @@ int moe_pack_dense(const moe_dense_shape* s, const void* w, const void* w_up, in
 int moe_dense_gemm(const moe_dense_shape* s, const void* a, int a_dtype, int64_t lda, const void* packed, int epilogue,
                    const float* bias, const void* residual, int r_dtype, int64_t ldr, void* c, int c_dtype,
                    int64_t ldc, void* stream);
+
+/*
+ * moe_add_rmsnorm -- the root-mean-square norm of a residual stream, with the
+ * residual's addition before it and the 8-bit codes of its rows after it, in
+ * one pass:
+ *   h = x + residual, a float32 sum rounded to the residual's type; h = x
+ *       without one.  h is what is normed and what `sum` receives.
+ *   s = 1 / sqrt(mean(h^2) + eps), mean and root in double, s rounded to float32
+ *   v = (h * s) * weight, two float32 products (weight NULL: h * s)
+ *   y = v rounded to y_dtype; codes and scales are v's, not y's.
+ * x, residual, sum, y: rows of H values, ldx, ldr, lds, ldy >= H elements apart,
+ *   MOE_F32, MOE_BF16 or MOE_F16 each (sum has the residual's type); weight [H],
+ *   w_dtype one of those.  residual, sum, weight and y may be NULL (sum without
+ *   a residual may not be given); a type and stride beside a NULL do not matter.
+ * codes (or NULL): rows of H codes, ldq >= H apart, with
+ *   q_dtype MOE_I8: scales float32 [rows], scale = largest |v| of the row / 127,
+ *       at least 2^-126; code = the integer nearest to v / scale, ties to even,
+ *       within +-127.  A row with an infinity or NaN in v has the scale NaN and
+ *       zeros for codes, so that a product with it is NaN;
+ *   q_dtype MOE_MXFP8: scales uint8 [rows][H/32], H a multiple of 32, the rule of
+ *       moe_quantize_mxfp8().  A block with an infinity or NaN in v has the scale
+ *       byte 255 and codes 127, which are NaN.
+ *   With ldq == H they are what moe_grouped_gemm_mxfp8() reads (a_rows gathers).
+ * At least one of y and codes.  eps in [2^-126, 2^127].  fp16 sums and y saturate
+ * at 65504.
+ * sum may be x or residual, y may be x or residual (same type and stride; not
+ * both the same): in place.  Any other overlap of an output with an input or
+ * another output is undefined.  Pointers need their element's alignment only;
+ * rows that start on 16 bytes are fastest.
+ * 0 <= rows <= MOE_DENSE_MAX_ROWS (0: a no-op), 1 <= H <= MOE_DENSE_MAX_COLS, else
+ * MOE_ERR_UNSUPPORTED.
+ */
+int moe_add_rmsnorm(int64_t rows, int32_t H, const void* x, int x_dtype, int64_t ldx, const void* residual,
+                    int r_dtype, int64_t ldr, void* sum, int64_t lds, const void* weight, int w_dtype, double eps,
+                    void* y, int y_dtype, int64_t ldy, void* codes, int q_dtype, int64_t ldq, void* scales,
+                    void* stream);
+
+/*
+ * moe_quantize_int8 -- the int8 codes and scales of rows x [rows, K] (MOE_F32,
+ * MOE_BF16 or MOE_F16, ldx >= K elements apart), by the rule of moe_add_rmsnorm();
+ * codes ldq >= K apart.  Same limits and alignment.
+ */
+int moe_quantize_int8(int64_t rows, int32_t K, const void* x, int x_dtype, int64_t ldx, int8_t* codes, int64_t ldq,
+                      float* scales, void* stream);
+
+/*
+ * Dense products of int8 codes with a scale per row and per column:
+ *   C = act((A W) * sa * sw + bias) + R               (gated == 0)
+ *   C = silu(gate) * up + R, each of (A W) * sa * sw + bias     (gated == 1)
+ * A W summed exactly in int32 (K <= MOE_DENSE_INT8_MAX_K, else
+ * MOE_ERR_UNSUPPORTED; the other limits are moe_dense_gemm()'s), everything after
+ * it in float32, rounded once to C's type.
+ */
+#define MOE_DENSE_INT8_MAX_K 131071
+
+/* Bytes of the packed codes and scales of (N, K, gated); any M, here and in moe_pack_dense_int8() (host-only). */
+size_t moe_packed_dense_bytes_int8(const moe_dense_shape* s);
+
+/*
+ * moe_pack_dense_int8 -- static conversion of w [K, N] (gated: the gate weight,
+ * with w_up [K, N]; else w_up is NULL), contiguous, into the layout
+ * moe_dense_gemm_int8() reads:
+ *   MOE_I8: codes of any value (-128 too) with their scales, float32 [N] each
+ *       (up_scales NULL unless gated);
+ *   MOE_F32, MOE_BF16, MOE_F16: quantised here per column along K, by the rule of
+ *       moe_add_rmsnorm()'s rows; scales and up_scales NULL.
+ *   packed: moe_packed_dense_bytes_int8(s) bytes, 16-byte aligned, written; opaque.
+ */
+int moe_pack_dense_int8(const moe_dense_shape* s, const void* w, const void* w_up, int dtype, const float* scales,
+                        const float* up_scales, void* packed, void* stream);
+
+/*
+ * moe_dense_gemm_int8 -- the product on packed codes.
+ *   a: rows of K codes, lda >= K apart, any alignment (rows that all start on 16
+ *       bytes, with K a multiple of 16, take the fast paths); a_scales float32 [M].
+ *   epilogue, bias, residual, c and their types and strides as in
+ *   moe_dense_gemm(): the residual may be c itself.
+ */
+int moe_dense_gemm_int8(const moe_dense_shape* s, const int8_t* a, int64_t lda, const float* a_scales,
+                        const void* packed, int epilogue, const float* bias, const void* residual, int r_dtype,
+                        int64_t ldr, void* c, int c_dtype, int64_t ldc, void* stream);
 
 /*
  * Measurement helpers (not part of the layer).  moe_probe_mfma_bf16 launches

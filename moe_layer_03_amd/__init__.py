@@ -2,7 +2,8 @@
 
 Route -> dispatch -> grouped bf16 MFMA GEMMs (gate/up with SwiGLU, down) ->
 combine, as hand-written HIP kernels for gfx950 behind a C ABI
-(``include/moe_layer_03_amd.h``).  ``binding`` holds the ctypes wrappers;
+(``include/moe_layer_03_amd.h``).  ``binding`` holds the ctypes wrappers,
+``quantized`` those of the norm, the int8 quantiser and the int8 product;
 ``workloads`` the named workloads and the seeded input generator.
 
 The library is loaded on first use of the binding; importing the package
@@ -10,11 +11,11 @@ touches neither HIP nor the GPU.
 """
 from . import workloads  # noqa: F401
 
-__all__ = ["workloads", "binding"]
+__all__ = ["workloads", "binding", "quantized"]
 
 
 def __getattr__(name):
-    if name == "binding":
+    if name in ("binding", "quantized"):
         import importlib
-        return importlib.import_module(__name__ + ".binding")
+        return importlib.import_module(__name__ + "." + name)
     raise AttributeError(name)

@@ -32,6 +32,7 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_F16 = 2
 MOE_MXFP8 = 3
+MOE_I8 = 4
 
 MOE_GEMM_GATE_UP = 0
 MOE_GEMM_DOWN = 1
@@ -54,6 +55,9 @@ EXPORTED = [
     "moe_layer_few_tokens_workspace_bytes", "moe_layer_few_tokens",
     "moe_layer_few_tokens_workspace_bytes_mxfp8", "moe_layer_few_tokens_mxfp8",
     "moe_packed_dense_bytes", "moe_pack_dense", "moe_dense_gemm",
+    # wrapped in quantized.py
+    "moe_add_rmsnorm", "moe_quantize_int8", "moe_packed_dense_bytes_int8", "moe_pack_dense_int8",
+    "moe_dense_gemm_int8",
 ]
 
 MOE_FEW_TOKENS_MAX = 32
@@ -142,6 +146,7 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     sz = ctypes.c_size_t
     i32 = ctypes.c_int
+    i64 = ctypes.c_int64
     sigs = {
         "moe_dispatch_workspace_bytes": (sz, [_S]),
         "moe_route_workspace_bytes": (sz, [_S]),
@@ -172,6 +177,12 @@ def load() -> ctypes.CDLL:
         "moe_pack_dense": (i32, [_D, _P, _P, i32, _P, _P]),
         "moe_dense_gemm": (i32, [_D, _P, i32, ctypes.c_int64, _P, i32, _P, _P, i32, ctypes.c_int64, _P, i32,
                                  ctypes.c_int64, _P]),
+        "moe_add_rmsnorm": (i32, [i64, ctypes.c_int32, _P, i32, i64, _P, i32, i64, _P, i64, _P, i32, ctypes.c_double, _P,
+                                  i32, i64, _P, i32, i64, _P, _P]),
+        "moe_quantize_int8": (i32, [i64, ctypes.c_int32, _P, i32, i64, _P, i64, _P, _P]),
+        "moe_packed_dense_bytes_int8": (sz, [_D]),
+        "moe_pack_dense_int8": (i32, [_D, _P, _P, i32, _P, _P, _P, _P]),
+        "moe_dense_gemm_int8": (i32, [_D, _P, i64, _P, _P, i32, _P, _P, i32, i64, _P, i32, i64, _P]),
         "moe_probe_mfma_bf16_flops": (ctypes.c_int64, [i32, i32]),
         "moe_probe_mfma_bf16": (i32, [i32, i32, _P, _P]),
     }

@@ -217,6 +217,20 @@ int check_dense_shape(const moe_dense_shape* s) {
     return s->M > MOE_DENSE_MAX_ROWS ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// int8 products: sums of K products of 2^14 at most stay below 2^31.
+int check_dense_weights_int8(const moe_dense_shape* s) {
+    MOE_TRY(check_dense_weights(s));
+    return s->K > MOE_DENSE_INT8_MAX_K ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+inline size_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+// Rows of H elements: at most as many and as long as a dense product's.
+int check_rows(int64_t rows, int32_t H) {
+    if (rows < 0 || H < 1) return MOE_ERR_INVALID_ARG;
+    return rows > MOE_DENSE_MAX_ROWS || H > MOE_DENSE_MAX_COLS ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 }  // namespace
 
 void set_last_hip_error(hipError_t e) { g_last_hip_error = static_cast<int32_t>(e); }
@@ -564,6 +578,88 @@ int moe_dense_gemm(const moe_dense_shape* s, const void* a, int a_dtype, int64_t
     return launch_dense_gemm(*s, static_cast<const uint16_t*>(a), a_dtype, lda, static_cast<const uint16_t*>(packed),
                              epilogue, bias, residual, r_dtype, ldr, c, c_dtype, ldc,
                              static_cast<hipStream_t>(stream));
+}
+
+int moe_add_rmsnorm(int64_t rows, int32_t H, const void* x, int x_dtype, int64_t ldx, const void* residual,
+                    int r_dtype, int64_t ldr, void* sum, int64_t lds, const void* weight, int w_dtype, double eps,
+                    void* y, int y_dtype, int64_t ldy, void* codes, int q_dtype, int64_t ldq, void* scales,
+                    void* stream) {
+    MOE_TRY(check_rows(rows, H));
+    if (!out_dtype_ok(x_dtype) || (residual != nullptr && !out_dtype_ok(r_dtype)) ||
+        (weight != nullptr && !out_dtype_ok(w_dtype)) || (y != nullptr && !out_dtype_ok(y_dtype)))
+        return MOE_ERR_UNSUPPORTED;
+    if (codes != nullptr && q_dtype != MOE_I8 && q_dtype != MOE_MXFP8) return MOE_ERR_UNSUPPORTED;
+    if (codes != nullptr && q_dtype == MOE_MXFP8 && H % 32 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!(eps >= 0x1p-126 && eps <= 0x1p127)) return MOE_ERR_INVALID_ARG;   // nor a NaN
+    if (ldx < H || (residual != nullptr && ldr < H) || (sum != nullptr && lds < H) || (y != nullptr && ldy < H) ||
+        (codes != nullptr && ldq < H))
+        return MOE_ERR_INVALID_ARG;
+    if (sum != nullptr && residual == nullptr) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;   // no rows; empty tensors may have null pointers
+    if (y == nullptr && codes == nullptr) return MOE_ERR_INVALID_ARG;
+    if (x == nullptr || !aligned(x, elem_bytes(x_dtype))) return MOE_ERR_INVALID_ARG;
+    if (residual != nullptr && (!aligned(residual, elem_bytes(r_dtype)) || !aligned(sum, elem_bytes(r_dtype))))
+        return MOE_ERR_INVALID_ARG;
+    if (weight != nullptr && !aligned(weight, elem_bytes(w_dtype))) return MOE_ERR_INVALID_ARG;
+    if (y != nullptr && !aligned(y, elem_bytes(y_dtype))) return MOE_ERR_INVALID_ARG;
+    if (codes != nullptr && (scales == nullptr || !aligned(scales, q_dtype == MOE_I8 ? 4 : 1))) return MOE_ERR_INVALID_ARG;
+    // in place: an output over an input of the same type and stride, but not both outputs over one
+    if (sum != nullptr && ((sum == x && (r_dtype != x_dtype || lds != ldx)) || (sum == residual && lds != ldr) || sum == y))
+        return MOE_ERR_INVALID_ARG;
+    if (y != nullptr && ((y == x && (y_dtype != x_dtype || ldy != ldx)) ||
+                         (y == residual && (y_dtype != r_dtype || ldy != ldr))))
+        return MOE_ERR_INVALID_ARG;
+    return launch_add_rmsnorm(rows, H, x, x_dtype, ldx, residual, r_dtype, ldr, sum, lds, weight, w_dtype, eps, y,
+                              y_dtype, ldy, static_cast<uint8_t*>(codes), q_dtype, ldq, scales,
+                              static_cast<hipStream_t>(stream));
+}
+
+int moe_quantize_int8(int64_t rows, int32_t K, const void* x, int x_dtype, int64_t ldx, int8_t* codes, int64_t ldq,
+                      float* scales, void* stream) {
+    MOE_TRY(check_rows(rows, K));
+    if (!out_dtype_ok(x_dtype)) return MOE_ERR_UNSUPPORTED;
+    if (ldx < K || ldq < K) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (x == nullptr || !aligned(x, elem_bytes(x_dtype)) || codes == nullptr || !ok4(scales)) return MOE_ERR_INVALID_ARG;
+    return launch_quantize_int8(rows, K, x, x_dtype, ldx, reinterpret_cast<uint8_t*>(codes), ldq, scales,
+                                static_cast<hipStream_t>(stream));
+}
+
+size_t moe_packed_dense_bytes_int8(const moe_dense_shape* s) {
+    if (check_dense_weights_int8(s) != MOE_OK) return 0;
+    return dense_int8_packed_bytes(*s);
+}
+
+int moe_pack_dense_int8(const moe_dense_shape* s, const void* w, const void* w_up, int dtype, const float* scales,
+                        const float* up_scales, void* packed, void* stream) {
+    MOE_TRY(check_dense_weights_int8(s));
+    const bool codes = dtype == MOE_I8;
+    if (!codes && !out_dtype_ok(dtype)) return MOE_ERR_UNSUPPORTED;
+    const size_t align = codes ? 1 : elem_bytes(dtype);
+    if (w == nullptr || !aligned(w, align) || !ok16(packed)) return MOE_ERR_INVALID_ARG;
+    if (s->gated ? (w_up == nullptr || !aligned(w_up, align)) : w_up != nullptr) return MOE_ERR_INVALID_ARG;
+    if (codes ? !ok4(scales) : scales != nullptr) return MOE_ERR_INVALID_ARG;
+    if (codes && s->gated ? !ok4(up_scales) : up_scales != nullptr) return MOE_ERR_INVALID_ARG;
+    return launch_pack_dense_int8(*s, w, w_up, dtype, scales, up_scales, static_cast<uint8_t*>(packed),
+                                  static_cast<hipStream_t>(stream));
+}
+
+int moe_dense_gemm_int8(const moe_dense_shape* s, const int8_t* a, int64_t lda, const float* a_scales,
+                        const void* packed, int epilogue, const float* bias, const void* residual, int r_dtype,
+                        int64_t ldr, void* c, int c_dtype, int64_t ldc, void* stream) {
+    MOE_TRY(check_dense_shape(s));
+    MOE_TRY(check_dense_weights_int8(s));
+    if (epilogue < MOE_EPI_NONE || epilogue > MOE_EPI_RELU) return MOE_ERR_INVALID_ARG;
+    if ((epilogue == MOE_EPI_SWIGLU) != (s->gated == 1)) return MOE_ERR_INVALID_ARG;
+    if (!out_dtype_ok(c_dtype) || (residual != nullptr && !out_dtype_ok(r_dtype))) return MOE_ERR_UNSUPPORTED;
+    if (lda < s->K || ldc < s->N || (residual != nullptr && ldr < s->N)) return MOE_ERR_INVALID_ARG;
+    if (s->M == 0) return MOE_OK;
+    if (a == nullptr || !ok4(a_scales) || !ok16(packed) || !opt4(bias)) return MOE_ERR_INVALID_ARG;
+    if (c == nullptr || !aligned(c, elem_bytes(c_dtype))) return MOE_ERR_INVALID_ARG;
+    if (residual != nullptr && !aligned(residual, elem_bytes(r_dtype))) return MOE_ERR_INVALID_ARG;
+    if (residual == c && (r_dtype != c_dtype || ldr != ldc)) return MOE_ERR_INVALID_ARG;
+    return launch_dense_gemm_int8(*s, a, lda, a_scales, static_cast<const uint8_t*>(packed), epilogue, bias, residual,
+                                  r_dtype, ldr, c, c_dtype, ldc, static_cast<hipStream_t>(stream));
 }
 
 const char* moe_status_string(int status) {

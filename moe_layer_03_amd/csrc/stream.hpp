@@ -178,9 +178,9 @@ __device__ __forceinline__ void start_steps(int n, Cursor& cur, StepRegs<NP, MX,
         if (j < n) cur.load(ring[j]);                  // uniform
 }
 
-template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor, typename After>
+template <int D, int NP, bool MX, int MT, int CT, typename Cursor, typename Sum, typename After>
 __device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D],
-                                          Acc<NP, F16, MX, MT, CT>& acc, After&& after) {
+                                          Sum& acc, After&& after) {
     int i = 0;
     for (; i + 2 * D <= n; i += D) {
 #pragma unroll
@@ -199,9 +199,9 @@ __device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, M
         }
 }
 
-template <int D, int NP, bool F16, bool MX, int MT, int CT, typename Cursor>
+template <int D, int NP, bool MX, int MT, int CT, typename Cursor, typename Sum>
 __device__ __forceinline__ void run_steps(int n, Cursor& cur, StepRegs<NP, MX, MT, CT> (&ring)[D],
-                                          Acc<NP, F16, MX, MT, CT>& acc) {
+                                          Sum& acc) {
     run_steps(n, cur, ring, acc, [] {});
 }
 

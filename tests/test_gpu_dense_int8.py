@@ -1,0 +1,300 @@
+"""The int8 dense product on the GPU against the definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from moe_layer_03_amd import binding as B
+from moe_layer_03_amd import quantized as Q
+from quantized_reference import TYPES, U, around, int8_rows, placed
+
+pytestmark = pytest.mark.gpu
+
+EPI = {"none": B.MOE_EPI_NONE, "silu": B.MOE_EPI_SILU, "gelu": B.MOE_EPI_GELU, "gelu_tanh": B.MOE_EPI_GELU_TANH,
+       "relu": B.MOE_EPI_RELU, "swiglu": B.MOE_EPI_SWIGLU}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def act64(v, act):
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    if act == "gelu":
+        return 0.5 * v * torch.erfc(-v / math.sqrt(2))
+    if act == "gelu_tanh":
+        return v * torch.sigmoid(math.sqrt(8 / math.pi) * (v + 0.044715 * v ** 3))
+    return v.clamp(min=0) if act == "relu" else v
+
+
+def reference(a, sa, w, sw, bias, residual, act, c):
+    """(value, bound).  Sums are exact; the sum's conversion and two products round once each (3 u), the bias once more.
+    Activations as in the 16-bit products' tests: slopes up to 1.13 and 24 u of their own; then the residual's addition and
+    half a step of c's type."""
+    v = [(a.double() @ x.double()) * sa.double()[:, None] * s.double() for x, s in zip(w, sw)]
+    err = [3.01 * U * p.abs() for p in v]
+    if bias is not None:
+        v = [p + b.double() for p, b in zip(v, bias)]
+        err = [e + U * p.abs() for e, p in zip(err, v)]
+    if act == "swiglu":
+        s = act64(v[0], "silu")
+        out = s * v[1]
+        e = 1.1 * err[0] * v[1].abs() + s.abs() * err[1] + 1.1 * err[0] * err[1] + 24 * U * out.abs()
+    elif act == "none":
+        out, e = v[0], err[0]
+    else:
+        out = act64(v[0], act)
+        e = 1.13 * err[0] + 24 * U * out.abs()
+    if residual is not None:
+        out = out + residual.double()
+        e = e + U * out.abs()
+    t = TYPES[c]
+    if t == torch.float16:
+        out = out.clamp(-65504, 65504)
+    step = torch.finfo(t).eps / 2
+    return out, e * (1 + step) + step * out.abs() + (2.0 ** -25 if t == torch.float16 else 2.0 ** -133)
+
+
+def inputs(M, N, K, act="none", bias=False, residual=None, seed=0, pad=0, offset=0):
+    g = torch.Generator().manual_seed(seed)
+    n = 2 if act == "swiglu" else 1
+    codes = lambda *s: torch.randint(-128, 128, s, generator=g).to(torch.int8)   # noqa: E731
+    return dict(a=placed(codes(M, K), pad, offset, -128)[0], sa=(torch.rand((M,), generator=g) * 0.02).cuda(),
+                w=[codes(K, N).cuda() for _ in range(n)],
+                sw=[(torch.rand((N,), generator=g) * 0.02 / math.sqrt(K)).cuda() for _ in range(n)],
+                bias=torch.randn((n, N), generator=g).cuda() if bias else None,
+                residual=placed(torch.randn((M, N), generator=g).to(TYPES[residual]), pad, offset)[0] if residual else None)
+
+
+def pack(s, d):
+    return Q.moe_pack_dense_int8(s, *d["w"], scales=d["sw"][0], up_scales=d["sw"][1] if len(d["sw"]) == 2 else None)
+
+
+def run(M, N, K, act="none", c="bf16", bias=False, residual=None, seed=0, pad=0, offset=0):
+    d = inputs(M, N, K, act, bias, residual, seed, pad, offset)
+    s = B.DenseShape(M, N, K, gated=act == "swiglu")
+    out, buf = placed(torch.full((M, N), 77.0, dtype=TYPES[c]), pad, offset, 77.0)
+    got = Q.moe_dense_gemm_int8(s, d["a"], d["sa"], pack(s, d), EPI[act], bias=d["bias"], residual=d["residual"], c=out)
+    torch.cuda.synchronize()
+    assert around(buf, out, 77.0)
+    ref, bound = reference(d["a"], d["sa"], d["w"], d["sw"], d["bias"], d["residual"], act, c)
+    err = (got.double() - ref).abs()
+    assert torch.isfinite(got).all()
+    assert (err <= bound).all(), f"{(err - bound).max().item():.3e} over the bound"
+
+
+SIZES = [(1, 1, 1), (1, 64, 64), (2, 37, 16), (1, 1536, 1024), (3, 100, 144), (15, 256, 192), (16, 31, 256), (17, 128, 400),
+         (32, 33, 64), (33, 512, 512), (63, 96, 640), (64, 65, 80), (65, 1000, 272), (96, 192, 2192), (127, 160, 128),
+         (128, 256, 1024), (129, 130, 528), (200, 1003, 192), (255, 320, 256), (256, 256, 512), (257, 257, 128),
+         (300, 512, 384), (513, 640, 320), (1000, 192, 640)]
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_sizes(size, gated):
+    run(*size, act="swiglu" if gated else "none", c="f32", seed=sum(size))
+    run(*size, act="swiglu" if gated else "none", c="bf16", bias=True, residual="bf16", seed=1 + sum(size), pad=16)
+
+
+# sizes that take each unit and tile shape of the 16-bit products' rule, ungated and gated, in twice the codes
+SHAPES = [(5, 4100, 80), (17, 2050, 80), (17, 4100, 80), (48, 4100, 80), (200, 200, 80), (65, 16400, 528), (2050, 1000, 80),
+          (2050, 4100, 80), (600, 16400, 80), (513, 70, 1040), (513, 70, 80), (5, 4100, 263), (17, 2050, 263),
+          (17, 4100, 263), (48, 4100, 2063), (128, 4100, 263)]
+SHAPES_GATED = [(5, 2050, 80), (48, 2050, 80), (65, 8200, 528), (1030, 1000, 80), (300, 12300, 144), (200, 16400, 144),
+                (200, 200, 80), (513, 70, 1040), (513, 70, 80), (5, 2050, 263), (17, 2050, 263), (200, 200, 263),
+                (48, 2050, 2063), (128, 2050, 263)]
+
+
+@pytest.mark.parametrize("size,act", [(s, "relu") for s in SHAPES] + [(s, "swiglu") for s in SHAPES_GATED])
+def test_unit_and_tile_shapes(size, act):
+    run(*size, act, c="f32", bias=True, residual="bf16", pad=16, seed=sum(size))
+
+
+@pytest.mark.parametrize("act", list(EPI))
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_epilogues_and_types(act, M):
+    for i, (c, residual, bias) in enumerate([("f32", None, True), ("bf16", "f32", False), ("f16", "bf16", True),
+                                             ("f32", "f16", False), ("f16", None, False)]):
+        run(M, 136, 208, act=act, c=c, bias=bias, residual=residual, seed=i)
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 530])
+@pytest.mark.parametrize("K,pad,offset", [(63, 0, 0), (65, 3, 0), (100, 4, 0), (64, 0, 3), (64, 1, 0), (7, 0, 1), (130, 6, 2),
+                                          (257, 7, 0), (255, 1, 16), (120, 8, 0), (127, 1, 0), (136, 0, 8), (1, 0, 0), (2, 13, 5)])
+def test_rows_off_16_bytes(M, K, pad, offset):
+    """Odd reductions, odd strides, odd starts; codes of -128 lie between the rows."""
+    run(M, 70, K, c="f32", bias=True, residual="f32", pad=pad, offset=offset, seed=K)
+    run(M, 70, K, act="swiglu", c="f16", residual="f16", pad=pad, offset=offset, seed=K)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 100, 512, 777])
+@pytest.mark.parametrize("K", [16384, 16385])
+def test_sums_are_exact(M, K):
+    """Unit scales and sums below 2^24: the float32 result is the integer itself."""
+    g = torch.Generator().manual_seed(M)
+    N = 96
+    a, w = (torch.randint(-128, 128, n, generator=g).to(torch.int8).cuda() for n in ((M, K), (K, N)))
+    w[torch.rand((K, N), generator=g).cuda() < 0.9] = 0
+    s = B.DenseShape(M, N, K)
+    packed = Q.moe_pack_dense_int8(s, w, scales=torch.ones(N, device="cuda"))
+    got = Q.moe_dense_gemm_int8(s, a, torch.ones(M, device="cuda"), packed, c_dtype=torch.float32)
+    ref = a.double() @ w.double()
+    assert ref.abs().max() < 2 ** 24 and torch.equal(got.double(), ref)
+
+
+@pytest.mark.parametrize("M", [1, 33, 600])
+@pytest.mark.parametrize("sign", [-128, 127])
+def test_longest_reduction_of_the_largest_codes(M, sign):
+    """131071 products of -128 * -128 stay below 2^31; of -128 * 127 above -2^31."""
+    K, N = B_K, 64
+    s = B.DenseShape(M, N, K)
+    a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((K, N), sign, dtype=torch.int8, device="cuda")
+    packed = Q.moe_pack_dense_int8(s, w, scales=torch.ones(N, device="cuda"))
+    got = Q.moe_dense_gemm_int8(s, a, torch.ones(M, device="cuda"), packed, c_dtype=torch.float32)
+    want = torch.tensor(float(K * -128 * sign), dtype=torch.float64).float()
+    assert (got == want.item()).all()
+
+
+B_K = 131071
+
+
+@pytest.mark.parametrize("M", [3, 100, 600])
+@pytest.mark.parametrize("sa,sw", [(2.0 ** -126, 2.0 ** 100), (2.0 ** 115, 2.0 ** -126), (1e30, 1e-30), (1e-36, 1e36),
+                                   (1e-25, 1e-12), (2.0 ** 90, 1.0), (1.0, 2.0 ** 90), (0.0, 1.0), (1.5, 0.0), (-0.5, 2.0)])
+def test_scales_of_any_size(M, sa, sw):
+    """No product on the way over- or underflows where the result does not."""
+    N, K = 70, 144
+    d = inputs(M, N, K, seed=3)
+    d["sa"] = torch.full((M,), sa, device="cuda")
+    d["sw"] = [torch.full((N,), sw, device="cuda")]
+    s = B.DenseShape(M, N, K)
+    got = Q.moe_dense_gemm_int8(s, d["a"], d["sa"], pack(s, d), c_dtype=torch.float32)
+    ref, bound = reference(d["a"], d["sa"], d["w"], d["sw"], None, None, "none", "f32")
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M,K,pad", [(3, 144, 0), (20, 130, 1), (100, 128, 0), (130, 65, 0), (600, 192, 0)])
+def test_nan_scales(M, K, pad):
+    """A row's NaN scale makes its row NaN, a column's its column, whatever the codes; nothing else."""
+    N = 100
+    d = inputs(M, N, K, pad=pad, seed=4)
+    d["sa"][M // 2] = math.nan
+    d["sw"][0][7] = math.nan
+    d["a"][M // 2] = 0
+    s = B.DenseShape(M, N, K)
+    got = Q.moe_dense_gemm_int8(s, d["a"], d["sa"], pack(s, d))
+    want = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    want[M // 2] = True
+    want[:, 7] = True
+    assert torch.equal(torch.isnan(got), want)
+
+
+@pytest.mark.parametrize("M,c", [(4, "f32"), (33, "bf16"), (400, "f32"), (400, "f16")])
+def test_residual_in_place(M, c):
+    d = inputs(M, 200, 320, residual=c, seed=M, pad=16)
+    s = B.DenseShape(M, 200, 320)
+    ref, bound = reference(d["a"], d["sa"], d["w"], d["sw"], None, d["residual"], "none", c)
+    got = Q.moe_dense_gemm_int8(s, d["a"], d["sa"], pack(s, d), residual=d["residual"], c=d["residual"])
+    assert got.data_ptr() == d["residual"].data_ptr()
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("N,K", [(1, 1), (70, 130), (64, 128), (200, 1000), (33, 5)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_weights_quantised_when_packed(t, N, K, gated):
+    """The packer's codes and scales are the rule's along each column: the packed bytes are those of given codes."""
+    g = torch.Generator().manual_seed(N)
+    s = B.DenseShape(1, N, K, gated=gated)
+    w = [(torch.randn((K, N), generator=g) * 0.02).to(TYPES[t]) for _ in range(2 if gated else 1)]
+    w[0][:, N // 2] = 0
+    given = [int8_rows(x.float(), dim=0) for x in w]
+    want = Q.moe_pack_dense_int8(s, *(c.cuda() for c, _ in given), scales=given[0][1].cuda(),
+                                 up_scales=given[1][1].cuda() if gated else None)
+    got = Q.moe_pack_dense_int8(s, *(x.cuda() for x in w))
+    assert torch.equal(got, want)
+
+
+def test_weights_that_are_not_finite():
+    w = torch.randn((64, 40))
+    w[9, 3] = math.inf
+    w[0, 5] = math.nan
+    s = B.DenseShape(2, 40, 64)
+    a = torch.ones((2, 64), dtype=torch.int8, device="cuda")
+    got = Q.moe_dense_gemm_int8(s, a, torch.ones(2, device="cuda"), Q.moe_pack_dense_int8(s, w.cuda()))
+    assert torch.equal(torch.isnan(got[0]).nonzero()[:, 0].cpu(), torch.tensor([3, 5]))
+
+
+def test_offsets_past_32_bits():
+    """Rows of A, of the residual and of C whose byte or element offsets pass 2^31."""
+    M, K, N, ld = 70000, 64, 64, 33024
+    g = torch.Generator(device="cuda").manual_seed(2)
+    a = torch.empty((M, ld), dtype=torch.int8, device="cuda")[:, :K]
+    a.copy_(torch.randint(-128, 128, (M, K), generator=g, device="cuda"))
+    w = torch.randint(-128, 128, (K, N), generator=g, device="cuda").to(torch.int8)
+    sa, sw = torch.rand(M, generator=g, device="cuda") * 0.01, torch.rand(N, generator=g, device="cuda") * 0.01
+    c = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")[:, :N]
+    c.copy_(torch.randn((M, N), generator=g, device="cuda"))
+    ref, bound = reference(a, sa, [w], [sw], None, c, "none", "bf16")
+    s = B.DenseShape(M, N, K)
+    got = Q.moe_dense_gemm_int8(s, a, sa, Q.moe_pack_dense_int8(s, w, scales=sw), residual=c, c=c)
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_rows_far_apart(M, odd):
+    """A tile's rows further apart than a buffer reaches."""
+    ld, K, N = (1 << 23) + 16 + odd, 128, 70
+    buf = torch.empty(((M - 1) * ld + K,), dtype=torch.int8, device="cuda")
+    a = buf.as_strided((M, K), (ld, 1))
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a.copy_(torch.randint(-128, 128, (M, K), generator=g, device="cuda"))
+    d = inputs(1, N, K, seed=5)
+    d["a"], d["sa"] = a, torch.rand(M, generator=g, device="cuda")
+    s = B.DenseShape(M, N, K)
+    got = Q.moe_dense_gemm_int8(s, a, d["sa"], pack(s, d), c_dtype=torch.float32)
+    ref, bound = reference(d["a"], d["sa"], d["w"], d["sw"], None, None, "none", "f32")
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+def test_no_rows():
+    s = B.DenseShape(0, 40, 64)
+    d = inputs(1, 40, 64)
+    e = torch.empty((0, 64), dtype=torch.int8, device="cuda")
+    assert Q.moe_dense_gemm_int8(s, e, torch.empty(0, device="cuda"), pack(s, d)).shape == (0, 40)
+
+
+@pytest.mark.parametrize("M", [1, 48, 100, 640])
+def test_repeats_and_replays(M):
+    """Bit for bit again, on two streams at once, and from a captured graph on new inputs."""
+    d = inputs(M, 512, 512, "swiglu", bias=True, residual="bf16", seed=M)
+    s = B.DenseShape(M, 512, 512, gated=True)
+    packed = pack(s, d)
+
+    def call(c=None, stream=None):
+        return Q.moe_dense_gemm_int8(s, d["a"], d["sa"], packed, EPI["swiglu"], bias=d["bias"], residual=d["residual"], c=c,
+                                     stream=stream)
+    first = call()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    others = [call(stream=st) for _ in range(6) for st in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in others)
+    c = torch.empty_like(first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(c)
+    for i in range(3):
+        n = inputs(M, 512, 512, "swiglu", seed=100 + i)
+        d["a"].copy_(n["a"])
+        d["sa"].copy_(n["sa"])
+        eager = call()
+        c.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, eager)
