@@ -127,10 +127,7 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     p.lda = lda;
     p.Kh = s.K / 2;
     p.Kp = k_padded<kI8>(s);
-    const dim3 g(static_cast<unsigned>(pairs_of(s)), (p.M + 63) / 64);
-    hipLaunchKernelGGL((dense_any_kernel<kI8>), g, dim3(256), 0, st, p);
-    MOE_CHECK_LAUNCH();
-    return MOE_OK;
+    return launch_dense<kI8>(p, pairs_of(s), st);
 }
 
 }  // namespace moe
