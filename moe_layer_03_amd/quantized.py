@@ -18,10 +18,56 @@ from typing import Optional
 import torch
 
 from . import binding as _b
-from .binding import MOE_EPI_NONE, MOE_F32, MOE_I8, MOE_MXFP8, DenseShape
+from .binding import MOE_BF16, MOE_EPI_NONE, MOE_F16, MOE_F32, MOE_I8, MOE_MXFP8, DenseShape
 
 __all__ = ["MOE_I8", "MOE_MXFP8", "moe_add_rmsnorm", "moe_quantize_int8", "moe_packed_dense_bytes_int8",
            "moe_pack_dense_int8", "moe_dense_gemm_int8"]
+
+
+# Argument checks as binding's, with fewer calls into torch: a decode step's kernels are shorter than a careful call.
+
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+_CODES = {MOE_I8: torch.int8, MOE_MXFP8: torch.uint8}
+
+
+def _dt(t: torch.Tensor) -> int:
+    code = _DTYPES.get(t.dtype)
+    return _b._dt(t) if code is None else code         # which refuses it
+
+
+def _rows(t: torch.Tensor, m: int, n: int, index: int, name: str):
+    """(pointer, row stride) of an [m, n] tensor on GPU `index` whose rows are contiguous."""
+    if t.get_device() == index and t.shape == (m, n):
+        ld, one = t.stride()
+        if m <= 1:
+            ld = n
+        if (one == 1 or n <= 1) and ld >= n:
+            return t.data_ptr() or None, ld
+    r = _b._rows(t, m, n, name)                        # which says what is wrong
+    _b._same_device(torch.device("cuda", index), **{name: t})
+    return r
+
+
+def _flat(t: torch.Tensor, dtype, n: int, index: int, name: str):
+    """Pointer of n contiguous elements on GPU `index`."""
+    if t.get_device() == index and t.dtype == dtype and t.numel() == n and t.is_contiguous():
+        return t.data_ptr() or None
+    r = _b._ptr(t, dtype, n, name)
+    _b._same_device(torch.device("cuda", index), **{name: t})
+    return r
+
+
+def _index(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return index
+
+
+def _stream(index: int, stream):
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_getCurrentRawStream(index) or None
+    return _b._stream_on(torch.device("cuda", index), stream)
 
 
 def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -32,45 +78,53 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
 
     Returns (h, y, codes, scales).  y is computed where y or y_dtype is given, codes and scales where q_dtype is:
     MOE_I8 (int8 [rows, H], float32 [rows]) or MOE_MXFP8 (uint8 [rows, H], uint8 [rows, H/32]); with none of them y is
-    computed in x's type.  sum_out receives h and may be residual or x."""
+    computed in x's type.  sum_out receives h and may be residual or x, y may be x or residual (not both the same).
+    x, residual, sum_out, y and codes may have any row stride."""
     rows, H = x.shape
-    dev = x.device
-    if y is not None and y_dtype is not None and y.dtype != y_dtype:
-        raise TypeError(f"y is {y.dtype}, y_dtype {y_dtype}")
-    if q_dtype is None and (codes is not None or scales is not None):
-        raise ValueError("codes and scales need a q_dtype")
-    if q_dtype not in (None, MOE_I8, MOE_MXFP8):
-        raise ValueError("q_dtype is MOE_I8 or MOE_MXFP8")
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out needs a residual")
-    elif sum_out is None:
-        sum_out = _b._empty((rows, H), residual.dtype, dev, stream)
-    elif sum_out.dtype != residual.dtype:
-        raise TypeError(f"sum_out is {sum_out.dtype}, the residual {residual.dtype}")
-    if y is None and (y_dtype is not None or q_dtype is None):
-        y = _b._empty((rows, H), y_dtype or x.dtype, dev, stream)
-    pq = ps = None
-    ldq = 0
+    index = _index(x, "x")
+    pr = pt = pw = py = pq = ps = None
+    rd = wd = yd = MOE_F32
+    ldr = lds = ldy = ldq = 0
+    if residual is not None:
+        if sum_out is None:
+            sum_out = _b._empty((rows, H), residual.dtype, x.device, stream)
+        elif sum_out.dtype != residual.dtype:
+            raise TypeError(f"sum_out is {sum_out.dtype}, the residual {residual.dtype}")
+        rd = _dt(residual)
+        pr, ldr = _rows(residual, rows, H, index, "residual")
+        pt, lds = _rows(sum_out, rows, H, index, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if weight is not None:
+        wd = _dt(weight)
+        pw = _flat(weight, weight.dtype, H, index, "weight")
+    if y is not None:
+        if y_dtype is not None and y.dtype != y_dtype:
+            raise TypeError(f"y is {y.dtype}, y_dtype {y_dtype}")
+    elif y_dtype is not None or q_dtype is None:
+        y = _b._empty((rows, H), y_dtype or x.dtype, x.device, stream)
+    if y is not None:
+        yd = _dt(y)
+        py, ldy = _rows(y, rows, H, index, "y")
     if q_dtype is not None:
+        kind = _CODES.get(q_dtype)
+        if kind is None:
+            raise ValueError("q_dtype is MOE_I8 or MOE_MXFP8")
         int8 = q_dtype == MOE_I8
         if codes is None:
-            codes = _b._empty((rows, H), torch.int8 if int8 else torch.uint8, dev, stream)
+            codes = _b._empty((rows, H), kind, x.device, stream)
+        elif codes.dtype != kind:
+            raise TypeError(f"codes must be {kind}, got {codes.dtype}")
         if scales is None:
-            scales = _b._empty((rows,) if int8 else (rows, H // 32), torch.float32 if int8 else torch.uint8, dev, stream)
-        if codes.dtype != (torch.int8 if int8 else torch.uint8):
-            raise TypeError(f"codes must be {'int8' if int8 else 'uint8'}, got {codes.dtype}")
-        pq, ldq = _b._rows(codes, rows, H, "codes")
-        ps = _b._ptr(scales, torch.float32 if int8 else torch.uint8, rows if int8 else rows * (H // 32), "scales")
-    px, ldx = _b._rows(x, rows, H, "x")
-    pr, ldr = _b._rows(residual, rows, H, "residual")
-    pt, lds = _b._rows(sum_out, rows, H, "sum_out")
-    py, ldy = _b._rows(y, rows, H, "y")
-    args = (rows, H, px, _b._dt(x), ldx, pr, _b._dt(residual) if residual is not None else MOE_F32, ldr, pt, lds,
-            _b._ptr(weight, None, H, "weight"), _b._dt(weight) if weight is not None else MOE_F32, eps, py,
-            _b._dt(y) if y is not None else MOE_F32, ldy, pq, q_dtype or 0, ldq, ps)
-    _b._same_device(dev, residual=residual, sum_out=sum_out, weight=weight, y=y, codes=codes, scales=scales)
-    st = _b.load().moe_add_rmsnorm(*args, _b._stream_on(dev, stream))
+            scales = _b._empty((rows,) if int8 else (rows, H // 32), torch.float32 if int8 else torch.uint8, x.device,
+                               stream)
+        pq, ldq = _rows(codes, rows, H, index, "codes")
+        ps = _flat(scales, torch.float32 if int8 else torch.uint8, rows if int8 else rows * (H // 32), index, "scales")
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales need a q_dtype")
+    px, ldx = _rows(x, rows, H, index, "x")
+    st = _b.load().moe_add_rmsnorm(rows, H, px, _dt(x), ldx, pr, rd, ldr, pt, lds, pw, wd, eps, py, yd, ldy, pq,
+                                   q_dtype or 0, ldq, ps, _stream(index, stream))
     if st:
         _b._check("moe_add_rmsnorm", st)
     return x if residual is None else sum_out, y, codes, scales
@@ -80,18 +134,17 @@ def moe_quantize_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, sca
                       stream=None):
     """x [rows, K], any row stride, fp32, bf16 or fp16 -> (codes int8 [rows, K], scales float32 [rows])."""
     rows, K = x.shape
-    dev = x.device
+    index = _index(x, "x")
     if codes is None:
-        codes = _b._empty((rows, K), torch.int8, dev, stream)
-    if scales is None:
-        scales = _b._empty((rows,), torch.float32, dev, stream)
-    if codes.dtype != torch.int8:
+        codes = _b._empty((rows, K), torch.int8, x.device, stream)
+    elif codes.dtype != torch.int8:
         raise TypeError(f"codes must be int8, got {codes.dtype}")
-    px, ldx = _b._rows(x, rows, K, "x")
-    pq, ldq = _b._rows(codes, rows, K, "codes")
-    args = (rows, K, px, _b._dt(x), ldx, pq, ldq, _b._ptr(scales, torch.float32, rows, "scales"))
-    _b._same_device(dev, codes=codes, scales=scales)
-    st = _b.load().moe_quantize_int8(*args, _b._stream_on(dev, stream))
+    if scales is None:
+        scales = _b._empty((rows,), torch.float32, x.device, stream)
+    px, ldx = _rows(x, rows, K, index, "x")
+    pq, ldq = _rows(codes, rows, K, index, "codes")
+    st = _b.load().moe_quantize_int8(rows, K, px, _dt(x), ldx, pq, ldq, _flat(scales, torch.float32, rows, index, "scales"),
+                                     _stream(index, stream))
     if st:
         _b._check("moe_quantize_int8", st)
     return codes, scales
@@ -136,24 +189,29 @@ def moe_dense_gemm_int8(d: DenseShape, a: torch.Tensor, a_scales: torch.Tensor, 
 
     a [M, K] int8, residual and c [M, N] may have any row stride; c may be residual.  c_dtype is c's, or bfloat16."""
     shape, need = _dense_int8_of(d)
-    if packed.numel() < need:
-        raise ValueError(f"packed must hold {need} bytes, got {packed.numel()}")
-    dev = a.device
+    M, N = d.M, d.N
+    index = _index(a, "a")
     if a.dtype != torch.int8:
         raise TypeError(f"a must be int8, got {a.dtype}")
+    size = packed.numel()
+    if size < need:
+        raise ValueError(f"packed must hold {need} bytes, got {size}")
     if c is None:
-        c = _b._empty((d.M, d.N), c_dtype or torch.bfloat16, dev, stream)
+        c = _b._empty((M, N), c_dtype or torch.bfloat16, a.device, stream)
     elif c_dtype is not None and c.dtype != c_dtype:
         raise TypeError(f"c is {c.dtype}, c_dtype {c_dtype}")
-    pa, lda = _b._rows(a, d.M, d.K, "a")
-    pr, ldr = _b._rows(residual, d.M, d.N, "residual")
-    pc, ldc = _b._rows(c, d.M, d.N, "c")
-    args = (shape, pa, lda, _b._ptr(a_scales, torch.float32, d.M, "a_scales"),
-            _b._ptr(packed, torch.uint8, None, "packed"), epilogue,
-            _b._ptr(bias, torch.float32, d.N * (2 if d.gated else 1), "bias"), pr,
-            _b._dt(residual) if residual is not None else MOE_F32, ldr, pc, _b._dt(c), ldc)
-    _b._same_device(dev, a_scales=a_scales, packed=packed, bias=bias, residual=residual, c=c)
-    st = _b.load().moe_dense_gemm_int8(*args, _b._stream_on(dev, stream))
+    pb = pr = None
+    rd, ldr = MOE_F32, 0
+    if bias is not None:
+        pb = _flat(bias, torch.float32, 2 * N if d.gated else N, index, "bias")
+    if residual is not None:
+        rd = _dt(residual)
+        pr, ldr = _rows(residual, M, N, index, "residual")
+    pa, lda = _rows(a, M, d.K, index, "a")
+    pc, ldc = _rows(c, M, N, index, "c")
+    st = _b.load().moe_dense_gemm_int8(shape, pa, lda, _flat(a_scales, torch.float32, M, index, "a_scales"),
+                                       _flat(packed, torch.uint8, size, index, "packed"), epilogue, pb, pr, rd, ldr, pc,
+                                       _dt(c), ldc, _stream(index, stream))
     if st:
         _b._check("moe_dense_gemm_int8", st)
     return c

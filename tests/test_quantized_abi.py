@@ -129,17 +129,42 @@ def test_binding_refuses_host_tensors(name, stream, monkeypatch):
         CALLS[name][0](stream=stream)
 
 
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on the first GPU: what is refused here is refused before anything is launched."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def g(*shape, dtype=torch.bfloat16):
+    return t(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
 @pytest.mark.parametrize("call,error", [
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), codes=t(4, 64, dtype=torch.int8)), ValueError),
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), q_dtype=B.MOE_BF16), ValueError),
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), sum_out=t(4, 64)), ValueError),
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), None, t(4, 64), sum_out=t(4, 64, dtype=torch.float32)), TypeError),
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), y=t(4, 64), y_dtype=torch.float32), TypeError),
-    (lambda: Q.moe_add_rmsnorm(t(4, 64), q_dtype=Q.MOE_I8, codes=t(4, 64, dtype=torch.uint8)), TypeError),
-    (lambda: Q.moe_quantize_int8(t(4, 64), codes=t(4, 64, dtype=torch.uint8)), TypeError),
-    (lambda: Q.moe_dense_gemm_int8(D, t(4, 64), SA, PACKED), TypeError),
-    (lambda: Q.moe_dense_gemm_int8(D, A8, SA, t(64, dtype=torch.uint8)), ValueError),
-    (lambda: Q.moe_dense_gemm_int8(D, A8, SA, PACKED, c=t(4, 64), c_dtype=torch.float32), TypeError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), y=g(4, 64), codes=g(4, 64, dtype=torch.int8)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), q_dtype=B.MOE_BF16), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), sum_out=g(4, 64)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), None, g(4, 64), sum_out=g(4, 64, dtype=torch.float32)), TypeError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), None, g(4, 32)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), None, t(4, 64)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), g(32)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), g(128)[::2]), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), g(64, dtype=torch.float64)), TypeError),
+    (lambda: Q.moe_add_rmsnorm(g(64, 4).t(), y=g(4, 64)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), y=g(1, 64).expand(4, 64)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), y=g(4, 64), y_dtype=torch.float32), TypeError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), q_dtype=Q.MOE_I8, codes=g(4, 64, dtype=torch.uint8)), TypeError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64), q_dtype=Q.MOE_I8, codes=g(4, 64, dtype=torch.int8),
+                               scales=g(3, dtype=torch.float32)), ValueError),
+    (lambda: Q.moe_add_rmsnorm(g(4, 64, dtype=torch.int8), y=g(4, 64)), TypeError),
+    (lambda: Q.moe_quantize_int8(g(4, 64), codes=g(4, 64, dtype=torch.uint8)), TypeError),
+    (lambda: Q.moe_quantize_int8(g(4, 64), codes=g(4, 64, dtype=torch.int8), scales=g(4)), TypeError),
+    (lambda: Q.moe_dense_gemm_int8(D, g(4, 64), SA, PACKED), TypeError),
+    (lambda: Q.moe_dense_gemm_int8(D, g(4, 64, dtype=torch.int8), SA, g(64, dtype=torch.uint8)), ValueError),
+    (lambda: Q.moe_dense_gemm_int8(D, g(4, 64, dtype=torch.int8), SA, PACKED, c=g(4, 64), c_dtype=torch.float32), TypeError),
+    (lambda: Q.moe_dense_gemm_int8(D, g(4, 64, dtype=torch.int8), SA, PACKED, c=g(4, 64), bias=g(64)), TypeError),
+    (lambda: Q.moe_dense_gemm_int8(D, g(4, 32, dtype=torch.int8), SA, PACKED, c=g(4, 64)), ValueError),
     (lambda: Q.moe_pack_dense_int8(D, t(64, 64), packed=t(64, dtype=torch.uint8)), ValueError),
 ])
 def test_binding_refusals(call, error):
@@ -174,9 +199,10 @@ def test_what_a_call_allocates_belongs_to_its_stream(name, stream, monkeypatch):
         log.append((active[-1] if active else None, v))
         return v
     monkeypatch.setattr(B, "load", Library)
-    for fn in ("_ptr", "_stream_on", "_same_device"):
-        monkeypatch.setattr(B, fn, lambda *a, **k: None)
-    monkeypatch.setattr(B, "_rows", lambda *a: (None, 0))
+    for module, fn in ((B, "_ptr"), (B, "_stream_on"), (B, "_same_device"), (Q, "_flat"), (Q, "_stream")):
+        monkeypatch.setattr(module, fn, lambda *a, **k: None)
+    monkeypatch.setattr(Q, "_rows", lambda *a: (None, 0))
+    monkeypatch.setattr(Q, "_index", lambda *a: 0)
     monkeypatch.setattr(Q, "_dense_int8_of", Q._dense_int8_of.__wrapped__)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
@@ -185,6 +211,19 @@ def test_what_a_call_allocates_belongs_to_its_stream(name, stream, monkeypatch):
     call(stream=stream)
     assert [s for s, _ in log] == [stream] * count
     assert all(getattr(v, "recorded", None) == (["current"] if stream else None) for _, v in log)
+
+
+@pytest.mark.parametrize("current,stream,good", [(0, None, True), (0, 0, True), (0, 1, False), (1, None, False), (1, 0, False)])
+def test_the_stream_is_on_the_tensors_device(current, stream, good, monkeypatch):
+    """Tensors on cuda:0, whatever the current device and the stream's."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0x40 + i)
+    given = None if stream is None else type("Stream", (), {"cuda_stream": 0x40, "device": torch.device("cuda", stream)})()
+    if good:
+        assert Q._stream(0, given) == 0x40
+    else:
+        with pytest.raises(ValueError, match="tensors are on cuda:0"):
+            Q._stream(0, given)
 
 
 def test_every_entry_point_is_here():
