@@ -48,7 +48,7 @@ struct DenseArgs {
     int M, N, K;
     int Kh, Kp;                // K in whole 16-bit units, and padded as the weights are
     int gated, act, r_dtype, c_dtype;
-    int r_vec, c_vec;          // rows of R (C) start on four elements: four columns move at once
+    int vec;                   // rows of R and C start on four elements, of which N is a multiple
 };
 
 // ---- epilogue ------------------------------------------------------------------
@@ -83,25 +83,30 @@ __device__ __forceinline__ float over_one_plus_exp(float v, float y) {
 
 // N values at once.  tanh-GELU is v / (1 + exp(-2 z)), without (1 + tanh z)'s
 // cancellation for negative z; y = 2 z has seven roundings, 7 |y| u of the result.
-template <int N>
-__device__ __forceinline__ void activate(float (&v)[N], int act, bool fast) {
-    auto each = [&](auto&& f) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = f(v[i]);
-    };
+template <int ACT, bool FAST, int N>
+__device__ __forceinline__ void activate_as(float (&v)[N]) {
     auto tanh_y = [](float x) { return 1.5957691216057308f * (x + 0.044715f * x * x * x); };
-    switch (act) {                                     // uniform, as fast is
-        case MOE_EPI_SWIGLU:                           // the gate's
-        case MOE_EPI_SILU:
-            if (fast) each([](float x) { return over_one_plus_exp_fast(x, x); });
-            else each([](float x) { return over_one_plus_exp(x, x); });
-            break;
-        case MOE_EPI_GELU: each([](float x) { return 0.5f * x * erfcf(x * -0.70710678118654752f); }); break;
-        case MOE_EPI_GELU_TANH:
-            if (fast) each([&](float x) { return over_one_plus_exp_fast(x, tanh_y(x)); });
-            else each([&](float x) { return over_one_plus_exp(x, tanh_y(x)); });
-            break;
-        case MOE_EPI_RELU: each([](float x) { return x < 0.0f ? 0.0f : x; }); break;   // NaN stays
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = v[i];
+        if constexpr (ACT == MOE_EPI_SWIGLU || ACT == MOE_EPI_SILU)   // SwiGLU: the gate's
+            v[i] = FAST ? over_one_plus_exp_fast(x, x) : over_one_plus_exp(x, x);
+        else if constexpr (ACT == MOE_EPI_GELU)
+            v[i] = 0.5f * x * erfcf(x * -0.70710678118654752f);
+        else if constexpr (ACT == MOE_EPI_GELU_TANH)
+            v[i] = FAST ? over_one_plus_exp_fast(x, tanh_y(x)) : over_one_plus_exp(x, tanh_y(x));
+        else if constexpr (ACT == MOE_EPI_RELU)
+            v[i] = x < 0.0f ? 0.0f : x;                // NaN stays
+    }
+}
+template <bool FAST, int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    switch (act) {                                     // uniform
+        case MOE_EPI_SWIGLU:
+        case MOE_EPI_SILU: activate_as<MOE_EPI_SILU, FAST>(v); break;
+        case MOE_EPI_GELU: activate_as<MOE_EPI_GELU, FAST>(v); break;
+        case MOE_EPI_GELU_TANH: activate_as<MOE_EPI_GELU_TANH, FAST>(v); break;
+        case MOE_EPI_RELU: activate_as<MOE_EPI_RELU, FAST>(v); break;
         default: break;
     }
 }
@@ -142,7 +147,8 @@ __device__ __forceinline__ void finish(const DenseArgs& p, int row, int col, typ
     }
     if (p.bias != nullptr) v += p.bias[col];
     float g[1] = {v};
-    activate(g, p.act, p.c_dtype != MOE_F32);
+    if (p.c_dtype == MOE_F32) activate<false>(g, p.act);
+    else activate<true>(g, p.act);
     v = g[0];
     if (p.gated) {
         if (p.bias != nullptr) u += p.bias[p.N + col];
@@ -152,64 +158,169 @@ __device__ __forceinline__ void finish(const DenseArgs& p, int row, int col, typ
     store_as(p.c, row * p.ldc + col, p.c_dtype, v);
 }
 
-// Four columns col .. col + 3 of a row at once (bias already loaded: b0 the
-// gate's or the only one, b1 the up's; s0 and s1 the columns' scales).
+// ---- four columns at once -----------------------------------------------------------
+// A lane finishes columns col .. col + 3 of one row after another, in a loop made for the activation: 24 rows of four
+// a lane for a 192 x 256 tile, where a branch or a conversion more in each step shows.  Nothing in a step branches on a
+// lane: rows past M and columns past N have offsets that load zeros and store nothing.  So the compiler knows what is
+// in flight, and a step that needs a part of the residual waits for that and not for the stores behind it.
+// VEC: rows of R and C start on four elements and N is a multiple of four, so that four columns move at once.
+struct Columns {
+    floatx4 b0, b1, s0, s1;    // bias and scales of the gate's or only weight, and of the up's
+};
+
 template <int KIND>
-__device__ __forceinline__ void finish4(const DenseArgs& p, int row, int col, const typename Sums<KIND>::four& v0,
-                                        const typename Sums<KIND>::four& u0, const floatx4& b0, const floatx4& b1,
-                                        const floatx4& s0, const floatx4& s1) {
-    if (row >= p.M || col >= p.N) return;
-    floatx4 v, u;
-    if constexpr (KIND == kI8) {
-        const float sa = p.sa[row];
+__device__ __forceinline__ Columns load_columns(const DenseArgs& p, int col) {
+    Columns c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = scaled(v0[i], sa, s0[i]);
-            u[i] = p.gated ? scaled(u0[i], sa, s1[i]) : 0.0f;
-        }
-    } else {
-        v = v0;
-        u = u0;
+    for (int i = 0; i < 4; ++i) {
+        const int at = min(col + i, p.N - 1);          // past N: never stored
+        c.b0[i] = p.bias != nullptr ? p.bias[at] : 0.0f;
+        c.b1[i] = p.bias != nullptr && p.gated ? p.bias[p.N + at] : 0.0f;
+        c.s0[i] = KIND == kI8 ? p.sb[at] : 0.0f;
+        c.s1[i] = KIND == kI8 && p.gated ? p.sb[p.sb_up + at] : 0.0f;
     }
-    v += b0;
-    float g[4] = {v[0], v[1], v[2], v[3]};
-    activate(g, p.act, p.c_dtype != MOE_F32);
-    v = floatx4{g[0], g[1], g[2], g[3]};
-    if (p.gated) v *= u + b1;
-    const bool whole = col + 4 <= p.N;
-    if (p.r != nullptr) {
-        const int64_t at = row * p.ldr + col;
-        if (whole && p.r_vec) {
-            if (p.r_dtype == MOE_F32) {
-                v += *reinterpret_cast<const floatx4*>(static_cast<const float*>(p.r) + at);
+    return c;
+}
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Four sums with their scales, in the order of scaled().
+__device__ __forceinline__ floatx4 scaled4(const intx4& v, float sa, const floatx4& sw) {
+    floatx4 f = __builtin_convertvector(v, floatx4);
+    if (__builtin_amdgcn_ballot_w64(sa > 1.0f) == 0) return f * sa * sw;
+    const bool big = sa > 1.0f;
+    const floatx4 all = {sa, sa, sa, sa};
+    return f * (big ? sw : all) * (big ? all : sw);
+}
+
+// C and R from the first row of a tile on, as buffers: the launcher keeps a tile's offsets below the range.
+template <int KIND, bool VEC>
+struct Finisher {
+    const DenseArgs& p;
+    __amdgpu_buffer_rsrc_t c, r;
+    int rows;                  // rows of the tile that exist
+    int c_row, r_row;          // bytes of a row
+    bool c_wide, r_wide;
+
+    __device__ __forceinline__ Finisher(const DenseArgs& args, int row0) : p(args) {
+        c_wide = p.c_dtype == MOE_F32;
+        r_wide = p.r_dtype == MOE_F32;
+        c_row = static_cast<int>(p.ldc) * (c_wide ? 4 : 2);
+        r_row = static_cast<int>(p.ldr) * (r_wide ? 4 : 2);
+        auto buffer = [](const void* base, int64_t bytes) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + bytes, 0,
+                                                     kBufferRange, kBufferFlags);
+        };
+        c = buffer(p.c, static_cast<int64_t>(row0) * c_row);
+        r = buffer(p.r, static_cast<int64_t>(row0) * r_row);
+        rows = p.M - row0;
+    }
+    // The residual's four elements of a row of the tile: a word each, or (16-bit, VEC) two to a word.
+    __device__ __forceinline__ u32x4 load(int row, int col) const {
+        u32x4 q = {0u, 0u, 0u, 0u};
+        if (p.r == nullptr) return q;                  // uniform, as the types are
+        if (r_wide) {
+            const uint32_t off = row * r_row + col * 4;
+            if constexpr (VEC) {
+                q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  r, row < rows && col < p.N ? off : kOutOfRange, 0, 0));
             } else {
-                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.r) + at);
-                const uint16_t h[4] = {static_cast<uint16_t>(r.x), static_cast<uint16_t>(r.x >> 16),
-                                       static_cast<uint16_t>(r.y), static_cast<uint16_t>(r.y >> 16)};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += p.r_dtype == MOE_BF16 ? bf16_to_f32(h[i]) : f16_to_f32(h[i]);
+                for (int i = 0; i < 4; ++i)
+                    q[i] = __builtin_amdgcn_raw_buffer_load_b32(r, row < rows && col + i < p.N ? off + 4 * i : kOutOfRange, 0, 0);
             }
+        } else {
+            const uint32_t off = row * r_row + col * 2;
+            if constexpr (VEC) {
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                                                  r, row < rows && col < p.N ? off : kOutOfRange, 0, 0));
+                q[0] = v[0];
+                q[1] = v[1];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[i] = __builtin_amdgcn_raw_buffer_load_b16(r, row < rows && col + i < p.N ? off + 2 * i : kOutOfRange, 0, 0);
+            }
+        }
+        return q;
+    }
+    template <int ACT>
+    __device__ __forceinline__ void finish(int row, int col, const typename Sums<KIND>::four& v0,
+                                           const typename Sums<KIND>::four& u0, const Columns& k, float sa,
+                                           const u32x4& q) const {
+        floatx4 v, u;
+        if constexpr (KIND == kI8) v = scaled4(v0, sa, k.s0);
+        else v = v0;
+        v += k.b0;
+        if constexpr (ACT != MOE_EPI_NONE) {
+            float g[4] = {v[0], v[1], v[2], v[3]};
+            if (c_wide) activate_as<ACT, false>(g);
+            else activate_as<ACT, true>(g);
+            v = floatx4{g[0], g[1], g[2], g[3]};
+        }
+        if constexpr (ACT == MOE_EPI_SWIGLU) {
+            if constexpr (KIND == kI8) u = scaled4(u0, sa, k.s1);
+            else u = u0;
+            v *= u + k.b1;
+        }
+        if (p.r != nullptr) {
+            if (r_wide) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(q[i]);
+            } else {
+                uint32_t e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = VEC ? q[i >> 1] >> (16 * (i & 1)) : q[i];
+                if (p.r_dtype == MOE_BF16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(e[i] << 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += f16_to_f32(static_cast<uint16_t>(e[i]));
+                }
+            }
+        }
+        if (c_wide) {
+            const uint32_t off = row * c_row + col * 4;
+            if constexpr (VEC) {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), c,
+                                                       row < rows && col < p.N ? off : kOutOfRange, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), c,
+                                                          row < rows && col + i < p.N ? off + 4 * i : kOutOfRange, 0, 0);
+            }
+            return;
+        }
+        u32x2_t h;
+        if (p.c_dtype == MOE_BF16)
+            h = u32x2_t{pack_bf16x2_or_nan(v[0], v[1]), pack_bf16x2_or_nan(v[2], v[3])};
+        else
+            h = u32x2_t{f32_to_f16_or_nan(v[0]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[1])) << 16,
+                        f32_to_f16_or_nan(v[2]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[3])) << 16};
+        const uint32_t off = row * c_row + col * 2;
+        if constexpr (VEC) {
+            __builtin_amdgcn_raw_buffer_store_b64(h, c, row < rows && col < p.N ? off : kOutOfRange, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (col + i < p.N) v[i] += load_as(p.r, at + i, p.r_dtype);
+                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1))), c,
+                                                      row < rows && col + i < p.N ? off + 2 * i : kOutOfRange, 0, 0);
         }
     }
-    const int64_t at = row * p.ldc + col;
-    if (whole && p.c_vec) {
-        if (p.c_dtype == MOE_F32)
-            *reinterpret_cast<floatx4*>(static_cast<float*>(p.c) + at) = v;
-        else if (p.c_dtype == MOE_BF16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
-                make_uint2(pack_bf16x2_or_nan(v[0], v[1]), pack_bf16x2_or_nan(v[2], v[3]));
-        else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + at) =
-                make_uint2(f32_to_f16_or_nan(v[0]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[1])) << 16,
-                           f32_to_f16_or_nan(v[2]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[3])) << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (col + i < p.N) store_as(p.c, at + i, p.c_dtype, v[i]);
+};
+
+// f(activation), a constant for it (uniform).
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+    switch (act) {
+        case MOE_EPI_SWIGLU: f(IntC<MOE_EPI_SWIGLU>{}); break;
+        case MOE_EPI_SILU: f(IntC<MOE_EPI_SILU>{}); break;
+        case MOE_EPI_GELU: f(IntC<MOE_EPI_GELU>{}); break;
+        case MOE_EPI_GELU_TANH: f(IntC<MOE_EPI_GELU_TANH>{}); break;
+        case MOE_EPI_RELU: f(IntC<MOE_EPI_RELU>{}); break;
+        default: f(IntC<MOE_EPI_NONE>{}); break;
     }
 }
 
@@ -258,8 +369,11 @@ __device__ __forceinline__ typename Sums<KIND>::four mfma16k(const u32x4& a, con
 // which the rule takes there, 18.8; 500 x 515 x 2011 28.5 and 26.1).
 constexpr int kAnyK = 128;
 constexpr int kAnyLd = kAnyK + 8;                      // LDS row, 16 of them in distinct banks
+constexpr int kAnyOut = 64 + 4;                        // row of sums on the way out
+// Rows of R and C: four elements at once, one at a time, or so far apart that a tile's pass a buffer's range.
+enum OutRows { kByFour = 0, kByOne = 1, kFarRows = 2 };
 
-template <int KIND>
+template <int KIND, int OUT>
 __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
     __shared__ __attribute__((aligned(16))) uint16_t s_a[2][64 * kAnyLd];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -322,18 +436,53 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) rb[q][h] = nb[q][h];
     }
+    // through LDS, so that a thread has four columns of a row; one copy of the code for all of them (48 KB, which a cold
+    // launch has to fetch, were it once per register)
+    typedef typename Sums<KIND>::one Sum;
+    static_assert(sizeof(s_a) >= 64 * kAnyOut * sizeof(Sum), "");
+    Sum* s_c = reinterpret_cast<Sum*>(&s_a[0][0]);
+    __syncthreads();                                   // the last stage has been read
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row0 + r0 + m * 16 + (lane >> 4) * 4 + i, cc = c0 + (lane & 15);
-            if (p.gated) {
-                finish<KIND>(p, r, pair * 32 + cc, acc[m][0][i], acc[m][1][i]);
-            } else {
-                finish<KIND>(p, r, pair * 64 + cc, acc[m][0][i], 0);
-                finish<KIND>(p, r, pair * 64 + 32 + cc, acc[m][1][i], 0);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                s_c[(r0 + m * 16 + (lane >> 4) * 4 + i) * kAnyOut + h * 32 + c0 + (lane & 15)] = acc[m][h][i];
+    const int lc = p.gated ? (tid & 7) * 4 : (tid & 15) * 4, dr = p.gated ? 32 : 16;
+    const int col = pair * (p.gated ? 32 : 64) + lc;
+    int r = p.gated ? tid >> 3 : tid >> 4;
+    if constexpr (OUT == kFarRows) {
+        __syncthreads();
+#pragma unroll 1
+        for (; r < 64; r += dr)
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const Sum* e = s_c + r * kAnyOut + lc + i;
+                finish<KIND>(p, row0 + r, col + i, *e, p.gated ? e[32] : 0);
             }
+        return;
+    }
+    typedef typename Sums<KIND>::four Sum4;
+    const Finisher<KIND, OUT == kByFour> f(p, row0);
+    const Columns columns = load_columns<KIND>(p, col);
+    float sa = 0.0f;                                   // of row tid % 64
+    if constexpr (KIND == kI8) sa = p.sa[min(row0 + lane, p.M - 1)];
+    __syncthreads();
+    with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        u32x4 part = f.load(r, col);
+#pragma unroll 1
+        for (int i = r; i < 64; i += dr) {
+            const u32x4 now = part;
+            part = f.load(i + dr, col);
+            const Sum* e = s_c + i * kAnyOut + lc;
+            Sum4 u = {0, 0, 0, 0};
+            if constexpr (ACT == MOE_EPI_SWIGLU) u = *reinterpret_cast<const Sum4*>(e + 32);
+            f.template finish<ACT>(i, col, *reinterpret_cast<const Sum4*>(e), u, columns, KIND == kI8 ? __shfl(sa, i, kWave) : 0.0f,
+                                   now);
         }
+    });
 }
 
 // ---- few rows: weight streaming ------------------------------------------------------
@@ -363,7 +512,14 @@ struct DenseCursor {
 
     __device__ __forceinline__ void load_b(StepRegs<1, false, MT, CT>& s) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c) load_weights<false>(b + c * 1024, s.b[c]);
+        for (int c = 0; c < CT; ++c) {
+            if constexpr (KIND == kI8) {
+                s.b[c][0] = *reinterpret_cast<const u32x4*>(b + c * 1024);
+                s.b[c][1] = *reinterpret_cast<const u32x4*>(b + c * 1024 + 512);
+            } else {
+                load_weights<false>(b + c * 1024, s.b[c]);
+            }
+        }
     }
     __device__ __forceinline__ void load(StepRegs<1, false, MT, CT>& s) {
         load_b(s);
@@ -574,7 +730,7 @@ __device__ __forceinline__ void phase_end_lds() {
     phase_end();
 }
 
-template <int KIND, int MW, int NW, int NA, int SL>
+template <int KIND, bool VEC, int MW, int NW, int NA, int SL>
 __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
     constexpr int KG = 8 / (MW * NW);                  // wave groups along k
     constexpr int WS = SL * 2 / KG;                    // k-steps of 16 of a wave per stage
@@ -672,6 +828,20 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     for (;;) {
         const bool more = tile + G < total;            // uniform
         const Source next = source(more ? tile + G : tile);
+        // what the epilogue needs of this tile's columns and rows, loaded ahead where registers are left for it
+        int m_tile, n_tile;
+        place(tile, m_tile, n_tile);
+        const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4, lr = p.gated ? lane >> 3 : lane >> 4;
+        const int first = mh * NA * 32, col = (n_tile * NW + nq) * (p.gated ? 32 : 64) + lc;   // of the wave's part
+        Columns columns;
+        float sa[(NA + 1) / 2];                        // of the wave's rows lane, lane + 64
+        auto load_scales = [&]() __attribute__((always_inline)) {
+            columns = load_columns<KIND>(p, col);
+#pragma unroll
+            for (int i = 0; i < (NA + 1) / 2; ++i)
+                sa[i] = KIND == kI8 ? p.sa[min(m_tile * UM + first + i * 64 + lane, p.M - 1)] : 0.0f;
+        };
+        if constexpr (NA < 4) load_scales();
         typename Sums<KIND>::sixteen acc[NA][2];
 #pragma unroll
         for (int i = 0; i < NA; ++i)
@@ -732,49 +902,71 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         // 32 x 32 tile; 16 rows at a time go through LDS (columns XORed by 32 in every other group
         // of four rows, against bank conflicts), so that a lane ends up with four columns of a row;
         // the k groups' partial sums are added there, in group order
-        int m_tile, n_tile;
-        place(tile, m_tile, n_tile);
-        const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
-        const int lr = p.gated ? lane >> 3 : lane >> 4, dr = p.gated ? 8 : 4;   // rows a wave takes at once
-        const int col = (n_tile * NW + nq) * (p.gated ? 32 : 64) + lc;
-        floatx4 b0, b1, s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+        if constexpr (NA >= 4) load_scales();
+        const Finisher<KIND, VEC> f(p, m_tile * UM);
+        auto put = [&](auto i, auto hf) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (KIND == kI8 && col + i < p.N) {
-                s0[i] = p.sb[col + i];
-                if (p.gated) s1[i] = p.sb[p.sb_up + col + i];
-            }
-            const bool on = p.bias != nullptr && col + i < p.N;
-            b0[i] = on ? p.bias[col + i] : 0.0f;
-            b1[i] = on && p.gated ? p.bias[p.N + col + i] : 0.0f;
-        }
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < NA; ++i)
+                for (int v = 0; v < 8; ++v) {
+                    const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                    s_e[wave][r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] =
+                        acc[decltype(i)::value][j][decltype(hf)::value * 8 + v];
+                }
+            // keeps the compiler from making one block of two cases, whose registers would have to lie in memory
+            asm volatile("; rows %0" ::"n"(decltype(i)::value * 2 + decltype(hf)::value));
+        };
+        with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+            constexpr int dr = ACT == MOE_EPI_SWIGLU ? 8 : 4;      // rows a wave takes at once
+            constexpr int R = KG * dr < 16 ? 16 / (KG * dr) : 1;   // times that for its share of 16
+            const int mine = kg * dr;                              // the first of it; 16 and more: none
+            u32x4 part[R];
+            auto load = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                        s_e[wave][r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] = acc[i][j][hf * 8 + v];
-                    }
-                if constexpr (KG > 1) phase_end_lds();
-                const int base = m_tile * UM + (mh * NA + i) * 32 + hf * 16;
+                for (int i = 0; i < R; ++i) part[i] = f.load(first + g * 16 + mine + i * KG * dr + lr, col);
+            };
+            if (mine < 16) load(0);
 #pragma unroll 1
-                for (int r0 = kg * dr; r0 < 16; r0 += KG * dr) {
-                    const int r = r0 + lr, x = (r & 4) * 8;
-                    Sum4 v = {0, 0, 0, 0}, u = v;
+            for (int g = 0; g < NA * 2; ++g) {
+                switch (g) {                           // uniform
+                    case 0: put(IntC<0>{}, IntC<0>{}); break;
+                    case 1: put(IntC<0>{}, IntC<1>{}); break;
+                    case 2: if constexpr (NA > 1) put(IntC<1>{}, IntC<0>{}); break;
+                    case 3: if constexpr (NA > 1) put(IntC<1>{}, IntC<1>{}); break;
+                    case 4: if constexpr (NA > 2) put(IntC<2>{}, IntC<0>{}); break;
+                    case 5: if constexpr (NA > 2) put(IntC<2>{}, IntC<1>{}); break;
+                    case 6: if constexpr (NA > 3) put(IntC<3>{}, IntC<0>{}); break;
+                    default: if constexpr (NA > 3) put(IntC<3>{}, IntC<1>{}); break;
+                }
+                if constexpr (KG > 1) phase_end_lds();
+                if (mine < 16) {
+                    u32x4 now[R];
 #pragma unroll
-                    for (int q = 0; q < KG; ++q) {
-                        const Sum* e = &s_e[q * MW * NW + mh * NW + nq][r][0];
-                        v += *reinterpret_cast<const Sum4*>(e + (lc ^ x));
-                        if (p.gated) u += *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
+                    for (int i = 0; i < R; ++i) now[i] = part[i];
+                    if (g + 1 < NA * 2) load(g + 1);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const int r = mine + i * KG * dr + lr, x = (r & 4) * 8;
+                        Sum4 v = {0, 0, 0, 0}, u = v;
+#pragma unroll
+                        for (int q = 0; q < KG; ++q) {
+                            const Sum* e = &s_e[q * MW * NW + mh * NW + nq][r][0];
+                            v += *reinterpret_cast<const Sum4*>(e + (lc ^ x));
+                            if constexpr (ACT == MOE_EPI_SWIGLU) u += *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
+                        }
+                        const int row = g * 16 + r;
+                        float scale = 0.0f;
+                        if constexpr (KIND == kI8) {
+                            scale = __shfl(sa[0], row, kWave);
+                            if constexpr (NA > 2) scale = g < 4 ? scale : __shfl(sa[1], row, kWave);
+                        }
+                        f.template finish<ACT>(first + row, col, v, u, columns, scale, now[i]);
                     }
-                    finish4<KIND>(p, base + r, col, v, u, b0, b1, s0, s1);
                 }
                 if constexpr (KG > 1) phase_end_lds();
             }
+        });
         if (!more) break;
         tile += G;
         cur = next;
@@ -820,6 +1012,7 @@ struct UnitShape {
     int mt, ct;
 };
 constexpr UnitShape kUnitShapes[] = {{4, 2}, {2, 2}, {2, 1}, {1, 2}, {1, 1}};   // 4, 1 reads more than 2, 2 always
+constexpr int kUnitShape11 = 4;
 
 Choice stream_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
     Choice best{0, 0.0};
@@ -845,13 +1038,13 @@ int launch_stream(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) 
     }
 }
 
-template <int KIND, int MW, int NW, int NA, int SL>
+template <int KIND, bool VEC, int MW, int NW, int NA, int SL>
 int launch_tile(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     constexpr int UM = MW * NA * 32;
     const int ntiles = static_cast<int>((pairs + NW - 1) / NW), mtiles = (p.M + UM - 1) / UM;
     const int64_t tiles = static_cast<int64_t>(mtiles) * ntiles;
     const unsigned grid = static_cast<unsigned>(tiles < kCUs ? tiles : kCUs);   // persistent, one to a CU
-    hipLaunchKernelGGL((dense_tile_kernel<KIND, MW, NW, NA, SL>), dim3(grid), dim3(512), 0, st, p, mtiles, ntiles,
+    hipLaunchKernelGGL((dense_tile_kernel<KIND, VEC, MW, NW, NA, SL>), dim3(grid), dim3(512), 0, st, p, mtiles, ntiles,
                        static_cast<int>(pairs));
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -878,43 +1071,63 @@ Choice tile_choice(const DenseArgs& p, int64_t pairs) {
     return best;
 }
 
-template <int KIND>
+template <int KIND, bool VEC>
 int launch_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
     switch (shape) {
-        case 0: return launch_tile<KIND, 2, 4, 4, 1>(p, pairs, st);
-        case 1: return launch_tile<KIND, 2, 4, 3, 1>(p, pairs, st);
-        case 2: return launch_tile<KIND, 2, 4, 2, 1>(p, pairs, st);
-        case 3: return launch_tile<KIND, 2, 2, 2, 2>(p, pairs, st);
-        case 4: return launch_tile<KIND, 1, 2, 2, 2>(p, pairs, st);
-        default: return launch_tile<KIND, 1, 1, 2, 4>(p, pairs, st);
+        case 0: return launch_tile<KIND, VEC, 2, 4, 4, 1>(p, pairs, st);
+        case 1: return launch_tile<KIND, VEC, 2, 4, 3, 1>(p, pairs, st);
+        case 2: return launch_tile<KIND, VEC, 2, 4, 2, 1>(p, pairs, st);
+        case 3: return launch_tile<KIND, VEC, 2, 2, 2, 2>(p, pairs, st);
+        case 4: return launch_tile<KIND, VEC, 1, 2, 2, 2>(p, pairs, st);
+        default: return launch_tile<KIND, VEC, 1, 1, 2, 4>(p, pairs, st);
     }
 }
 
+// Whether the rows of a tile, of A, R and C, lie within a buffer's range.
+inline bool rows_near(const DenseArgs& p) {
+    const int64_t widest = std::max(p.ldc * (p.c_dtype == MOE_F32 ? 4 : 2), p.r == nullptr ? 0 : p.ldr * (p.r_dtype == MOE_F32 ? 4 : 2));
+    return p.lda * 256 <= kBufferRange && widest * 256 + MOE_DENSE_MAX_COLS * 4 <= kBufferRange;
+}
+
+template <int KIND>
+int launch_any(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+    const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
+    if (KIND == kI8 || !rows_near(p))                  // int8 rows within reach take another kernel
+        hipLaunchKernelGGL((dense_any_kernel<KIND, kFarRows>), g, dim3(256), 0, st, p);
+    else if constexpr (KIND != kI8) {
+        if (p.vec) hipLaunchKernelGGL((dense_any_kernel<KIND, kByFour>), g, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((dense_any_kernel<KIND, kByOne>), g, dim3(256), 0, st, p);
+    }
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+// 16-bit operands.
 template <int KIND>
 int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     // direct copies to LDS and 16-byte buffer loads need every row to start on 16
     // bytes, and a k group to end within the row
-    const bool rows16 = reinterpret_cast<uintptr_t>(p.a) % 16 == 0 && p.lda % 16 == 0 &&
-                        p.K % (8 * codes_per_unit<KIND>()) == 0;
-    // byte offsets within a tile of rows stay below the buffer range
+    const bool rows16 = reinterpret_cast<uintptr_t>(p.a) % 16 == 0 && p.lda % 16 == 0 && p.K % 8 == 0;
+    // byte offsets within a tile of rows stay below the buffer range (streaming finishes an element at a time, at any
+    // address of C and R)
     const bool near = p.lda * 256 <= kBufferRange;
     const Choice stream = stream_choice(p, pairs, rows16);
     const bool few = near && p.M <= kStreamRows;
-    if (rows16 && near) {
+    if (rows16 && rows_near(p)) {
         // 96 x 12288 x 4096: tiles 38.5 us, streaming 64.8; 256 x 1024 x 4096: 19.6 and 13.6
         const Choice tile = tile_choice(p, pairs);
-        return few && stream.ns <= tile.ns ? launch_stream<KIND, true>(p, pairs, stream.shape, st)
-                                           : launch_tiles<KIND>(p, pairs, tile.shape, st);
+        if (!few || stream.ns > tile.ns)
+            return p.vec ? launch_tiles<KIND, true>(p, pairs, tile.shape, st)
+                         : launch_tiles<KIND, false>(p, pairs, tile.shape, st);
+        return launch_stream<KIND, true>(p, pairs, stream.shape, st);
     }
-    const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
     // a stage of the any-alignment kernel takes about 1.65 us while its workgroups fit the chip twice over.
     // 128 x 1003 x 1091: streaming 8.2 us, 16.2 there; 128 x 4099 x 1091: 26.3 and 16.4
-    const double rounds = std::max(1.0, static_cast<double>(g.x) * g.y / (2 * kCUs));
+    const double rounds = std::max(1.0, static_cast<double>(pairs) * ((p.M + 63) / 64) / (2 * kCUs));
     if (few && stream.ns <= (p.Kp + kAnyK - 1) / kAnyK * 1650.0 * rounds)
-        return launch_stream<KIND, false>(p, pairs, stream.shape, st);
-    hipLaunchKernelGGL((dense_any_kernel<KIND>), g, dim3(256), 0, st, p);
-    MOE_CHECK_LAUNCH();
-    return MOE_OK;
+        return rows16 ? launch_stream<KIND, true>(p, pairs, stream.shape, st)
+                      : launch_stream<KIND, false>(p, pairs, stream.shape, st);
+    return launch_any<KIND>(p, pairs, st);
 }
 
 // All of a product but its operands.
@@ -936,8 +1149,7 @@ inline DenseArgs dense_args(const moe_dense_shape& s, int epilogue, const float*
     auto on_four = [](const void* q, int64_t ld, int dtype) {
         return reinterpret_cast<uintptr_t>(q) % (dtype == MOE_F32 ? 16 : 8) == 0 && ld % 4 == 0;
     };
-    p.r_vec = on_four(r, ldr, r_dtype);
-    p.c_vec = on_four(c, ldc, c_dtype);
+    p.vec = s.N % 4 == 0 && on_four(c, ldc, c_dtype) && (r == nullptr || on_four(r, ldr, r_dtype));
     return p;
 }
 

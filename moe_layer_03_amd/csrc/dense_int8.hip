@@ -77,6 +77,242 @@ __global__ __launch_bounds__(256) void pack_dense_int8_kernel(const ST* __restri
     *reinterpret_cast<u32x4*>(d) = v;
 }
 
+// ---- some rows: weight streaming with the rows through LDS ----------------------------------
+// As dense_stream_kernel: a workgroup owns MT * 16 rows x 16 columns of CT column halves (CT = 4: all of a 64-column
+// pair), its eight waves take every eighth step of 128 k, and the weights go straight to registers.  There A's rows do
+// too, and a quarter of a wave, 16 lanes, reads 16 bytes of 16 rows: 64 accesses to the L1 for a KiB, which bound it
+// (128 x 4096 x 4096: 19 thousand accesses on each CU in 14.1 us).  Here each wave copies its rows' 128 bytes of a step
+// to LDS, eight lanes to a row, 8 accesses for a KiB, into a ring of its own: no barrier until the sums are joined.
+// A granule of 16 bytes lies at its place XOR row % 8, so that the 16 rows of a fragment read fall into all banks.
+// Two steps are in flight (three and four: no faster, and fewer workgroups fit a CU); weights are loaded as others are
+// (past the caches 9.7 us at 128 x 4096 x 4096, against 7.8).
+// Bound by what a CU reads, some 106 bytes/ns once it has several workgroups and 80 with one: 64 x 4096 x 4096 6.6 us,
+// 128 rows 7.8, 256 rows 10.6, of which a launch is 2.3.
+// ROWS16: rows on 16 bytes and K a multiple of 16, copied directly.  Otherwise they go through registers.
+constexpr int kDepth = 2;
+
+// Bytes n .. 15 of v moved down to 0 .., zeros behind them; n uniform, 0 to 15.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
+    if (n & 8) v = u32x4{v[2], v[3], 0u, 0u};
+    if (n & 4) v = u32x4{v[1], v[2], v[3], 0u};
+    const uint32_t b = n & 3;
+    return u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], b), __builtin_amdgcn_alignbyte(v[2], v[1], b),
+                 __builtin_amdgcn_alignbyte(v[3], v[2], b), __builtin_amdgcn_alignbyte(0u, v[3], b)};
+}
+
+template <bool VEC, bool ROWS16, int MT, int CT>
+__global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(DenseArgs p) {
+    constexpr int kStep = MT * 16 * 128;               // bytes of the rows' part of a step
+    constexpr int D = kDepth, kRing = kNW * D * kStep, kRed = kNW * MT * CT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t s_all[kRing > kRed ? kRing : kRed];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int unit = blockIdx.x, row0 = blockIdx.y * MT * kRowTile;
+    const int pair = CT == 4 ? unit : unit >> 1, c0 = CT == 4 ? 0 : (unit & 1) * 16;
+    const int nk = (p.K + 127) / 128, steps = nk > wave ? (nk - wave + kNW - 1) / kNW : 0;
+    // rows through registers: the step that K ends in is its wave's first, so that what it costs more is in no loop (the
+    // order of the steps does not matter to exact sums)
+    const bool ends_here = !ROWS16 && p.K % 128 != 0 && (nk - 1) % kNW == wave;
+    // weights: this lane's bytes of the step; tile c: half c % 2, columns c0 + c / 2 * 16
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) +
+                       (static_cast<int64_t>(pair) * (p.Kp / 64) + wave) * step_bytes<false>() + (lane >> 5) * 2048 +
+                       (((lane >> 4) & 1) * 32 + c0 + (lane & 15)) * 16;
+    // rows: copy i brings rows 8 i .. 8 i + 7, lane: row lane / 8, place lane % 8
+    uint8_t* const first = reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.a)) + row0 * p.lda;
+    const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(first, 0, kBufferRange, kBufferFlags);
+    const int granule = (lane & 7) ^ (lane >> 3);      // row % 8 is lane / 8
+    uint32_t off[MT * 2];
+#pragma unroll
+    for (int i = 0; i < MT * 2; ++i) {
+        const int row = i * 8 + (lane >> 3);
+        const uint32_t at = static_cast<uint32_t>(min(row, p.M - 1 - row0) * static_cast<int>(p.lda) + granule * 16);
+        off[i] = ROWS16 && row0 + row >= p.M ? kOutOfRange : at;   // rows past M: zeros, or the last row's; not stored
+    }
+    uint8_t* ring = s_all + wave * (D * kStep);
+    u32x4 wb[D][CT][2], ra[ROWS16 ? 1 : D][MT * 2];
+    int next = wave;                                   // the step that is loaded next
+    auto load_weights_of = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int l = 0; l < 2; ++l)
+                wb[slot][c][l] = *reinterpret_cast<const u32x4*>(b + (c & 1) * 1024 + (c >> 1) * 256 + l * 4096);
+    };
+    auto load = [&](int slot) __attribute__((always_inline)) {
+        const bool last = ROWS16 && (next + 1) * 128 > p.K;   // uniform: K ends in the step
+#pragma unroll
+        for (int i = 0; i < MT * 2; ++i) {
+            if constexpr (ROWS16) {
+                uint32_t o = off[i];
+                if (last) o = next * 128 + granule * 16 < p.K ? o : kOutOfRange;
+                copy_to_lds(rows, ring + slot * kStep + i * 1024, static_cast<int>(o), next * 128);
+            } else {
+                ra[slot][i] = load_any<kI8>(first + next * 128 + off[i]);
+            }
+        }
+        load_weights_of(slot);
+        b += kNW * step_bytes<false>();
+        next += kNW;
+    };
+    intx4 acc[MT][CT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[m][c] = intx4{0, 0, 0, 0};
+    constexpr int LOADS = MT * 2 + CT * 2;
+    // operand l of row tile m: row m * 16 + lane % 16, granule l * 4 + lane / 16
+    const int fr = (lane & 15) * 128 + ((lane >> 4) ^ (lane & 7)) * 16;
+    auto multiply = [&](int slot) __attribute__((always_inline)) {
+        if constexpr (!ROWS16) {
+#pragma unroll
+            for (int i = 0; i < MT * 2; ++i) *reinterpret_cast<u32x4*>(ring + slot * kStep + i * 1024 + lane * 16) = ra[slot][i];
+        }
+        u32x4 a[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int l = 0; l < 2; ++l)
+                a[m][l] = *reinterpret_cast<const u32x4*>(ring + slot * kStep + m * 2048 + (fr ^ (l * 64)));
+#pragma unroll
+        for (int l = 0; l < 2; ++l)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[m][c] = mfma16k<kI8>(a[m][l], wb[slot][c][l], acc[m][c]);
+    };
+    // the oldest step has landed, n younger ones may be on their way (what goes to registers the compiler waits for)
+    auto landed = [&](auto n) __attribute__((always_inline)) {
+        if constexpr (ROWS16) wait_vmcnt<LOADS * decltype(n)::value>();
+        asm volatile("" ::: "memory");
+    };
+    // the fragments are read: their place may be filled again
+    auto read = [&]() __attribute__((always_inline)) {
+        if constexpr (ROWS16) wait_lgkmcnt0();
+        asm volatile("" ::: "memory");
+    };
+    if constexpr (!ROWS16) {
+        if (ends_here) {                               // whole granules, and the row's last 16 bytes for the one K ends in
+            const int k = (nk - 1) * 128 + granule * 16;
+            const uint8_t* start = b;
+            b += static_cast<int64_t>(nk - 1 - wave) * step_bytes<false>();
+            load_weights_of(0);
+            b = start;
+#pragma unroll
+            for (int i = 0; i < MT * 2; ++i) {
+                const uint8_t* row = first + off[i] - granule * 16;
+                if (p.K < 16) {                        // uniform
+                    ra[0][i] = load_tail<kI8>(row, granule * 8, p.K);
+                } else {
+                    const u32x4 v = load_any<kI8>(row + min(k, p.K - 16)), end = shift_down(v, (16 - p.K % 16) & 15);
+                    ra[0][i] = k + 16 <= p.K ? v : k < p.K ? end : u32x4{0u, 0u, 0u, 0u};
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (j < steps && !(j == 0 && ends_here)) load(j);   // uniform
+    int i = 0;
+    for (; i + 2 * D <= steps; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            landed(IntC<D - 1>{});
+            multiply(j);
+            read();
+            load(j);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * D - 1; ++j)
+        if (i + j < steps) {                           // uniform
+            if (i + j + D <= steps) landed(IntC<D - 1>{});
+            else landed(IntC<0>{});
+            multiply(j % D);
+            if (j < D && i + j + D < steps) {
+                read();
+                load(j % D);
+            }
+        }
+    // the waves' sums are joined in LDS: [wave][m][c][v][lane], where lane is column lane % 16, row (lane / 16) * 4 + v
+    __syncthreads();
+    int* red = reinterpret_cast<int*>(s_all);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[((wave * MT + m) * CT + c) * 256 + v * 64 + lane] = acc[m][c][v];
+    __syncthreads();
+    // four lanes are four columns of a row; gated: the up's are the tile after the gate's
+    with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        constexpr bool kGated = ACT == MOE_EPI_SWIGLU;
+        const Finisher<kI8, VEC> f(p, row0);
+        for (int i = tid; i < MT * CT * (kGated ? 32 : 64); i += kNW * 64) {
+            const int q = i & 15, v = (i >> 4) & 3, t = i >> 6;        // lanes 4 q .. 4 q + 3
+            const int m = kGated ? t / (CT / 2) : t / CT, c = kGated ? t % (CT / 2) * 2 : t % CT;
+            const int row = m * 16 + (q >> 2) * 4 + v, in = c0 + (c >> 1) * 16 + (q & 3) * 4;
+            const int col = kGated ? pair * 32 + in : pair * 64 + (c & 1) * 32 + in;
+            const float sa = p.sa[min(row0 + row, p.M - 1)];
+            const Columns columns = load_columns<kI8>(p, col);
+            const u32x4 part = f.load(row, col);
+            intx4 s = {0, 0, 0, 0}, u = s;
+#pragma unroll
+            for (int w = 0; w < kNW; ++w) {
+                const int* e = red + ((w * MT + m) * CT + c) * 256 + v * 64 + q * 4;
+                s += *reinterpret_cast<const intx4*>(e);
+                if constexpr (kGated) u += *reinterpret_cast<const intx4*>(e + 256);
+            }
+            f.template finish<ACT>(row, col, s, u, columns, sa, part);
+        }
+    });
+}
+
+// Unit shapes of int8_rows_kernel, and the time expected of each: a launch, what the shape takes at the ends (ns), and
+// what the busiest CU reads (bytes/ns), its first unit and then the others at the rate they reach together; rows off 16
+// bytes pass through registers, more slowly (32 rows x 64 columns then leave room for one workgroup on a CU: not taken).
+// Mostly within 15 % of measured times from 3.5 to 60 us, and the shape chosen within 8 % of the best.
+struct RowsShape {
+    int mt, ct;
+    double ends, rate, rate_any;
+};
+constexpr RowsShape kRowsShapes[] = {
+    {1, 2, 800, 106, 60}, {2, 2, 800, 106, 58}, {1, 4, 1000, 106, 75}, {2, 4, 950, 106, 0}, {4, 4, 2000, 62, 45}};
+
+Choice rows_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
+    Choice best{0, 0.0};
+    for (int i = 0; i < 5; ++i) {
+        const RowsShape& u = kRowsShapes[i];
+        if (!rows16 && u.rate_any == 0) continue;
+        const int rows = u.mt * kRowTile;
+        const int64_t groups = pairs * (4 / u.ct) * ((p.M + rows - 1) / rows), each = (groups + kCUs - 1) / kCUs;
+        const double bytes = (std::min(rows, p.M) + u.ct * kRowTile) * 2.0 * p.Kp;
+        const double ns = 2300.0 + u.ends + bytes / (rows16 ? 80 : 65) +
+                          (each - 1) * (bytes / (rows16 ? u.rate : u.rate_any) + u.ends / 4);
+        if (best.ns == 0.0 || ns < best.ns) best = Choice{i, ns};
+    }
+    return best;
+}
+
+template <bool VEC, bool ROWS16>
+int launch_rows(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
+    const RowsShape& u = kRowsShapes[shape];
+    const dim3 g(static_cast<unsigned>(pairs * (4 / u.ct)), (p.M + u.mt * kRowTile - 1) / (u.mt * kRowTile));
+    switch (shape) {
+        case 0: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 1, 2>), g, dim3(kNW * 64), 0, st, p); break;
+        case 1: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 2, 2>), g, dim3(kNW * 64), 0, st, p); break;
+        case 2: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 1, 4>), g, dim3(kNW * 64), 0, st, p); break;
+        case 3:
+            if constexpr (ROWS16) hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 2, 4>), g, dim3(kNW * 64), 0, st, p);
+            break;
+        default: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 4, 4>), g, dim3(kNW * 64), 0, st, p); break;
+    }
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+constexpr int kVeryFewRows = 8;
+
 inline size_t code_bytes(const moe_dense_shape& s) {
     return static_cast<size_t>(pairs_of(s)) * k_padded<kI8>(s) * 128;
 }
@@ -127,7 +363,22 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     p.lda = lda;
     p.Kh = s.K / 2;
     p.Kp = k_padded<kI8>(s);
-    return launch_dense<kI8>(p, pairs_of(s), st);
+    const int64_t pairs = pairs_of(s);
+    if (!rows_near(p)) return launch_any<kI8>(p, pairs, st);
+    const bool rows16 = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda % 16 == 0 && s.K % 16 == 0;
+    const Choice rows = rows_choice(p, pairs, rows16);
+    if (!rows16)
+        return p.vec ? launch_rows<true, false>(p, pairs, rows.shape, st) : launch_rows<false, false>(p, pairs, rows.shape, st);
+    // a few rows need no detour through LDS, and units of 16 columns: 1 x 4096 x 1536 3.1 us, 3.5 through LDS
+    if (s.M <= kVeryFewRows) {
+        if (stream_choice(p, pairs, true).shape == kUnitShape11) return launch_stream_tiles<kI8, true, 1, 1>(p, pairs, st);
+        return launch_stream_tiles<kI8, true, 1, 2>(p, pairs, st);
+    }
+    // 1024 x 4096 x 4096: tiles 26.8 us, 33.6 by rows; 512 x 1536 x 4096: 15.2 and 10.9
+    const Choice tile = tile_choice(p, pairs);
+    if (tile.ns < rows.ns)
+        return p.vec ? launch_tiles<kI8, true>(p, pairs, tile.shape, st) : launch_tiles<kI8, false>(p, pairs, tile.shape, st);
+    return p.vec ? launch_rows<true, true>(p, pairs, rows.shape, st) : launch_rows<false, true>(p, pairs, rows.shape, st);
 }
 
 }  // namespace moe

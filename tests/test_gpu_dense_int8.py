@@ -262,6 +262,24 @@ def test_rows_far_apart(M, odd):
     assert ((got.double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("c,N", [("f32", 72), ("f16", 70)])
+@pytest.mark.parametrize("far", ["c", "residual"])
+def test_output_rows_far_apart(M, c, N, far):
+    """Rows of C or of the residual further apart than a buffer reaches in a tile."""
+    ld, K = (1 << 22) + 4, 256
+    d = inputs(M, N, K, residual=c, seed=M)
+    s = B.DenseShape(M, N, K)
+    rows = torch.full(((M - 1) * ld + N,), 7.0, dtype=TYPES[c], device="cuda").as_strided((M, N), (ld, 1))
+    out = rows if far == "c" else None
+    if far == "residual":
+        rows.copy_(d["residual"])
+        d["residual"] = rows
+    got = Q.moe_dense_gemm_int8(s, d["a"], d["sa"], pack(s, d), residual=d["residual"], c=out, c_dtype=TYPES[c])
+    ref, bound = reference(d["a"], d["sa"], d["w"], d["sw"], None, d["residual"], "none", c)
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
 def test_no_rows():
     s = B.DenseShape(0, 40, 64)
     d = inputs(1, 40, 64)
