@@ -28,6 +28,8 @@ __all__ = ["MOE_I8", "MOE_MXFP8", "moe_add_rmsnorm", "moe_quantize_int8", "moe_p
 
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
 _CODES = {MOE_I8: torch.int8, MOE_MXFP8: torch.uint8}
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -35,22 +37,22 @@ def _dt(t: torch.Tensor) -> int:
     return _b._dt(t) if code is None else code         # which refuses it
 
 
-def _rows(t: torch.Tensor, m: int, n: int, index: int, name: str):
-    """(pointer, row stride) of an [m, n] tensor on GPU `index` whose rows are contiguous."""
-    if t.get_device() == index and t.shape == (m, n):
+def _rows(t: torch.Tensor, shape, index: int, name: str):
+    """(pointer, row stride) of a tensor of `shape`, (rows, n), on GPU `index` whose rows are contiguous."""
+    if t.shape == shape and t.get_device() == index:
+        if t.is_contiguous():
+            return t.data_ptr() or None, shape[1]
         ld, one = t.stride()
-        if m <= 1:
-            ld = n
-        if (one == 1 or n <= 1) and ld >= n:
+        if one == 1 and ld >= shape[1]:
             return t.data_ptr() or None, ld
-    r = _b._rows(t, m, n, name)                        # which says what is wrong
+    r = _b._rows(t, shape[0], shape[1], name)          # which says what is wrong
     _b._same_device(torch.device("cuda", index), **{name: t})
     return r
 
 
 def _flat(t: torch.Tensor, dtype, n: int, index: int, name: str):
     """Pointer of n contiguous elements on GPU `index`."""
-    if t.get_device() == index and t.dtype == dtype and t.numel() == n and t.is_contiguous():
+    if t.dtype == dtype and t.numel() == n and t.get_device() == index and t.is_contiguous():
         return t.data_ptr() or None
     r = _b._ptr(t, dtype, n, name)
     _b._same_device(torch.device("cuda", index), **{name: t})
@@ -65,8 +67,8 @@ def _index(t: torch.Tensor, name: str) -> int:
 
 
 def _stream(index: int, stream):
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return torch._C._cuda_getCurrentRawStream(index) or None
+    if stream is None and _current_device() == index:
+        return _current_stream(index) or None
     return _b._stream_on(torch.device("cuda", index), stream)
 
 
@@ -80,7 +82,8 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
     MOE_I8 (int8 [rows, H], float32 [rows]) or MOE_MXFP8 (uint8 [rows, H], uint8 [rows, H/32]); with none of them y is
     computed in x's type.  sum_out receives h and may be residual or x, y may be x or residual (not both the same).
     x, residual, sum_out, y and codes may have any row stride."""
-    rows, H = x.shape
+    shape = x.shape
+    rows, H = shape
     index = _index(x, "x")
     pr = pt = pw = py = pq = ps = None
     rd = wd = yd = MOE_F32
@@ -91,8 +94,8 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
         elif sum_out.dtype != residual.dtype:
             raise TypeError(f"sum_out is {sum_out.dtype}, the residual {residual.dtype}")
         rd = _dt(residual)
-        pr, ldr = _rows(residual, rows, H, index, "residual")
-        pt, lds = _rows(sum_out, rows, H, index, "sum_out")
+        pr, ldr = _rows(residual, shape, index, "residual")
+        pt, lds = _rows(sum_out, shape, index, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if weight is not None:
@@ -105,7 +108,7 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
         y = _b._empty((rows, H), y_dtype or x.dtype, x.device, stream)
     if y is not None:
         yd = _dt(y)
-        py, ldy = _rows(y, rows, H, index, "y")
+        py, ldy = _rows(y, shape, index, "y")
     if q_dtype is not None:
         kind = _CODES.get(q_dtype)
         if kind is None:
@@ -118,11 +121,11 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
         if scales is None:
             scales = _b._empty((rows,) if int8 else (rows, H // 32), torch.float32 if int8 else torch.uint8, x.device,
                                stream)
-        pq, ldq = _rows(codes, rows, H, index, "codes")
+        pq, ldq = _rows(codes, shape, index, "codes")
         ps = _flat(scales, torch.float32 if int8 else torch.uint8, rows if int8 else rows * (H // 32), index, "scales")
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales need a q_dtype")
-    px, ldx = _rows(x, rows, H, index, "x")
+    px, ldx = _rows(x, shape, index, "x")
     st = _b.load().moe_add_rmsnorm(rows, H, px, _dt(x), ldx, pr, rd, ldr, pt, lds, pw, wd, eps, py, yd, ldy, pq,
                                    q_dtype or 0, ldq, ps, _stream(index, stream))
     if st:
@@ -133,7 +136,8 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, resi
 def moe_quantize_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                       stream=None):
     """x [rows, K], any row stride, fp32, bf16 or fp16 -> (codes int8 [rows, K], scales float32 [rows])."""
-    rows, K = x.shape
+    shape = x.shape
+    rows, K = shape
     index = _index(x, "x")
     if codes is None:
         codes = _b._empty((rows, K), torch.int8, x.device, stream)
@@ -141,8 +145,8 @@ def moe_quantize_int8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, sca
         raise TypeError(f"codes must be int8, got {codes.dtype}")
     if scales is None:
         scales = _b._empty((rows,), torch.float32, x.device, stream)
-    px, ldx = _rows(x, rows, K, index, "x")
-    pq, ldq = _rows(codes, rows, K, index, "codes")
+    px, ldx = _rows(x, shape, index, "x")
+    pq, ldq = _rows(codes, shape, index, "codes")
     st = _b.load().moe_quantize_int8(rows, K, px, _dt(x), ldx, pq, ldq, _flat(scales, torch.float32, rows, index, "scales"),
                                      _stream(index, stream))
     if st:
@@ -188,7 +192,7 @@ def moe_dense_gemm_int8(d: DenseShape, a: torch.Tensor, a_scales: torch.Tensor, 
     bias [2, N]).
 
     a [M, K] int8, residual and c [M, N] may have any row stride; c may be residual.  c_dtype is c's, or bfloat16."""
-    shape, need = _dense_int8_of(d)
+    cshape, need = _dense_int8_of(d)
     M, N = d.M, d.N
     index = _index(a, "a")
     if a.dtype != torch.int8:
@@ -206,10 +210,10 @@ def moe_dense_gemm_int8(d: DenseShape, a: torch.Tensor, a_scales: torch.Tensor, 
         pb = _flat(bias, torch.float32, 2 * N if d.gated else N, index, "bias")
     if residual is not None:
         rd = _dt(residual)
-        pr, ldr = _rows(residual, M, N, index, "residual")
-    pa, lda = _rows(a, M, d.K, index, "a")
-    pc, ldc = _rows(c, M, N, index, "c")
-    st = _b.load().moe_dense_gemm_int8(shape, pa, lda, _flat(a_scales, torch.float32, M, index, "a_scales"),
+        pr, ldr = _rows(residual, (M, N), index, "residual")
+    pa, lda = _rows(a, (M, d.K), index, "a")
+    pc, ldc = _rows(c, (M, N), index, "c")
+    st = _b.load().moe_dense_gemm_int8(cshape, pa, lda, _flat(a_scales, torch.float32, M, index, "a_scales"),
                                        _flat(packed, torch.uint8, size, index, "packed"), epilogue, pb, pr, rd, ldr, pc,
                                        _dt(c), ldc, _stream(index, stream))
     if st:

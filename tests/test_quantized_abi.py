@@ -217,7 +217,8 @@ def test_what_a_call_allocates_belongs_to_its_stream(name, stream, monkeypatch):
 def test_the_stream_is_on_the_tensors_device(current, stream, good, monkeypatch):
     """Tensors on cuda:0, whatever the current device and the stream's."""
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0x40 + i)
+    monkeypatch.setattr(Q, "_current_device", lambda: current)
+    monkeypatch.setattr(Q, "_current_stream", lambda i: 0x40 + i)
     given = None if stream is None else type("Stream", (), {"cuda_stream": 0x40, "device": torch.device("cuda", stream)})()
     if good:
         assert Q._stream(0, given) == 0x40
