@@ -730,6 +730,84 @@ __device__ __forceinline__ void phase_end_lds() {
     phase_end();
 }
 
+// The end of a wave's NA * 32 rows x 64 columns: a register holds column lane % 32, row 8 (v / 4) + 4 (lane / 32) + v % 4
+// of a 32 x 32 tile; 16 rows at a time go through LDS (columns XORed by 32 in every other group of four rows, against
+// bank conflicts), so that a lane ends up with four columns of a row.  KG waves hold sums of the same rows, added in
+// LDS in their order: `mine` is the wave's place, `parts` the first's, the others' STRIDE places apart.  One copy of the
+// code for all of the registers: rows are loaded and finished in a loop, and only the way to LDS is written out.
+template <int KIND, int NA, int KG, int STRIDE, bool VEC>
+__device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const typename Sums<KIND>::sixteen (&acc)[NA][2],
+                                            typename Sums<KIND>::one (*mine)[64], const typename Sums<KIND>::one (*parts)[64],
+                                            int kg, int first, int col, const Columns& columns,
+                                            const float (&sa)[(NA + 1) / 2]) {
+    typedef typename Sums<KIND>::one Sum;
+    typedef typename Sums<KIND>::four Sum4;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int lc = f.p.gated ? (lane & 7) * 4 : (lane & 15) * 4, lr = f.p.gated ? lane >> 3 : lane >> 4;
+    auto put = [&](auto i, auto hf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                mine[r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] = acc[decltype(i)::value][j][decltype(hf)::value * 8 + v];
+            }
+        // keeps the compiler from making one block of two cases, whose registers would have to lie in memory
+        asm volatile("; rows %0" ::"n"(decltype(i)::value * 2 + decltype(hf)::value));
+    };
+    with_activation(f.p.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        constexpr int dr = ACT == MOE_EPI_SWIGLU ? 8 : 4;      // rows a wave takes at once
+        constexpr int R = KG * dr < 16 ? 16 / (KG * dr) : 1;   // times that for its share of 16
+        const int mine0 = kg * dr;                             // the first of it; 16 and more: none
+        u32x4 part[R];
+        auto load = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) part[i] = f.load(first + g * 16 + mine0 + i * KG * dr + lr, col);
+        };
+        if (mine0 < 16) load(0);
+#pragma unroll 1
+        for (int g = 0; g < NA * 2; ++g) {
+            switch (g) {                               // uniform
+                case 0: put(IntC<0>{}, IntC<0>{}); break;
+                case 1: put(IntC<0>{}, IntC<1>{}); break;
+                case 2: if constexpr (NA > 1) put(IntC<1>{}, IntC<0>{}); break;
+                case 3: if constexpr (NA > 1) put(IntC<1>{}, IntC<1>{}); break;
+                case 4: if constexpr (NA > 2) put(IntC<2>{}, IntC<0>{}); break;
+                case 5: if constexpr (NA > 2) put(IntC<2>{}, IntC<1>{}); break;
+                case 6: if constexpr (NA > 3) put(IntC<3>{}, IntC<0>{}); break;
+                default: if constexpr (NA > 3) put(IntC<3>{}, IntC<1>{}); break;
+            }
+            if constexpr (KG > 1) phase_end_lds();
+            if (mine0 < 16) {
+                u32x4 now[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) now[i] = part[i];
+                if (g + 1 < NA * 2) load(g + 1);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int r = mine0 + i * KG * dr + lr, x = (r & 4) * 8;
+                    Sum4 v = {0, 0, 0, 0}, u = v;
+#pragma unroll
+                    for (int q = 0; q < KG; ++q) {
+                        const Sum* e = &parts[q * STRIDE * 16 + r][0];
+                        v += *reinterpret_cast<const Sum4*>(e + (lc ^ x));
+                        if constexpr (ACT == MOE_EPI_SWIGLU) u += *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
+                    }
+                    const int row = g * 16 + r;
+                    float scale = 0.0f;
+                    if constexpr (KIND == kI8) {
+                        scale = __shfl(sa[0], row, kWave);
+                        if constexpr (NA > 2) scale = g < 4 ? scale : __shfl(sa[1], row, kWave);
+                    }
+                    f.template finish<ACT>(first + row, col, v, u, columns, scale, now[i]);
+                }
+            }
+            if constexpr (KG > 1) phase_end_lds();
+        }
+    });
+}
+
 template <int KIND, bool VEC, int MW, int NW, int NA, int SL>
 __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
     constexpr int KG = 8 / (MW * NW);                  // wave groups along k
@@ -744,7 +822,6 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][AC * 8 * 16 * kTileBK];   // [slice][row][32]
     __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][SL * NW * 4][512];        // [slice][pair][4]
     typedef typename Sums<KIND>::one Sum;
-    typedef typename Sums<KIND>::four Sum4;
     __shared__ __attribute__((aligned(16))) Sum s_e[8][16][64];     // epilogue: 16 rows of each wave
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -831,7 +908,7 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         // what the epilogue needs of this tile's columns and rows, loaded ahead where registers are left for it
         int m_tile, n_tile;
         place(tile, m_tile, n_tile);
-        const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4, lr = p.gated ? lane >> 3 : lane >> 4;
+        const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
         const int first = mh * NA * 32, col = (n_tile * NW + nq) * (p.gated ? 32 : 64) + lc;   // of the wave's part
         Columns columns;
         float sa[(NA + 1) / 2];                        // of the wave's rows lane, lane + 64
@@ -898,75 +975,9 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         }
         if (!late) phase_end();                        // the late waves' last multiply
 
-        // epilogue: a register holds column lane % 32, row 8 (v / 4) + 4 (lane / 32) + v % 4 of a
-        // 32 x 32 tile; 16 rows at a time go through LDS (columns XORed by 32 in every other group
-        // of four rows, against bank conflicts), so that a lane ends up with four columns of a row;
-        // the k groups' partial sums are added there, in group order
         if constexpr (NA >= 4) load_scales();
         const Finisher<KIND, VEC> f(p, m_tile * UM);
-        auto put = [&](auto i, auto hf) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                    s_e[wave][r][((lane & 31) + 32 * j) ^ ((lane >> 5) * 32)] =
-                        acc[decltype(i)::value][j][decltype(hf)::value * 8 + v];
-                }
-            // keeps the compiler from making one block of two cases, whose registers would have to lie in memory
-            asm volatile("; rows %0" ::"n"(decltype(i)::value * 2 + decltype(hf)::value));
-        };
-        with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
-            constexpr int ACT = decltype(act)::value;
-            constexpr int dr = ACT == MOE_EPI_SWIGLU ? 8 : 4;      // rows a wave takes at once
-            constexpr int R = KG * dr < 16 ? 16 / (KG * dr) : 1;   // times that for its share of 16
-            const int mine = kg * dr;                              // the first of it; 16 and more: none
-            u32x4 part[R];
-            auto load = [&](int g) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < R; ++i) part[i] = f.load(first + g * 16 + mine + i * KG * dr + lr, col);
-            };
-            if (mine < 16) load(0);
-#pragma unroll 1
-            for (int g = 0; g < NA * 2; ++g) {
-                switch (g) {                           // uniform
-                    case 0: put(IntC<0>{}, IntC<0>{}); break;
-                    case 1: put(IntC<0>{}, IntC<1>{}); break;
-                    case 2: if constexpr (NA > 1) put(IntC<1>{}, IntC<0>{}); break;
-                    case 3: if constexpr (NA > 1) put(IntC<1>{}, IntC<1>{}); break;
-                    case 4: if constexpr (NA > 2) put(IntC<2>{}, IntC<0>{}); break;
-                    case 5: if constexpr (NA > 2) put(IntC<2>{}, IntC<1>{}); break;
-                    case 6: if constexpr (NA > 3) put(IntC<3>{}, IntC<0>{}); break;
-                    default: if constexpr (NA > 3) put(IntC<3>{}, IntC<1>{}); break;
-                }
-                if constexpr (KG > 1) phase_end_lds();
-                if (mine < 16) {
-                    u32x4 now[R];
-#pragma unroll
-                    for (int i = 0; i < R; ++i) now[i] = part[i];
-                    if (g + 1 < NA * 2) load(g + 1);
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int r = mine + i * KG * dr + lr, x = (r & 4) * 8;
-                        Sum4 v = {0, 0, 0, 0}, u = v;
-#pragma unroll
-                        for (int q = 0; q < KG; ++q) {
-                            const Sum* e = &s_e[q * MW * NW + mh * NW + nq][r][0];
-                            v += *reinterpret_cast<const Sum4*>(e + (lc ^ x));
-                            if constexpr (ACT == MOE_EPI_SWIGLU) u += *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
-                        }
-                        const int row = g * 16 + r;
-                        float scale = 0.0f;
-                        if constexpr (KIND == kI8) {
-                            scale = __shfl(sa[0], row, kWave);
-                            if constexpr (NA > 2) scale = g < 4 ? scale : __shfl(sa[1], row, kWave);
-                        }
-                        f.template finish<ACT>(first + row, col, v, u, columns, scale, now[i]);
-                    }
-                }
-                if constexpr (KG > 1) phase_end_lds();
-            }
-        });
+        finish_tile<KIND, NA, KG, MW * NW>(f, acc, s_e[wave], s_e[mh * NW + nq], kg, first, col, columns, sa);
         if (!more) break;
         tile += G;
         cur = next;

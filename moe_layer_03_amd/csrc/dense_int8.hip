@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void pack_dense_int8_kernel(const ST* __restri
 // too, and a quarter of a wave, 16 lanes, reads 16 bytes of 16 rows: 64 accesses to the L1 for a KiB, which bound it
 // (128 x 4096 x 4096: 19 thousand accesses on each CU in 14.1 us).  Here each wave copies its rows' 128 bytes of a step
 // to LDS, eight lanes to a row, 8 accesses for a KiB, into a ring of its own: no barrier until the sums are joined.
-// A granule of 16 bytes lies at its place XOR row % 8, so that the 16 rows of a fragment read fall into all banks.
+// A granule of 16 bytes lies at its place XOR row / 2 % 8, so that the 16 rows of a fragment read fall into all banks.
 // Two steps are in flight (three and four: no faster, and fewer workgroups fit a CU); weights are loaded as others are
 // (past the caches 9.7 us at 128 x 4096 x 4096, against 7.8).
 // Bound by what a CU reads, some 106 bytes/ns once it has several workgroups and 80 with one: 64 x 4096 x 4096 6.6 us,
@@ -120,12 +120,13 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
     // rows: copy i brings rows 8 i .. 8 i + 7, lane: row lane / 8, place lane % 8
     uint8_t* const first = reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.a)) + row0 * p.lda;
     const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(first, 0, kBufferRange, kBufferFlags);
-    const int granule = (lane & 7) ^ (lane >> 3);      // row % 8 is lane / 8
+    const int granule0 = (lane & 7) ^ (lane >> 4);
+    auto granule = [&](int i) { return granule0 ^ ((i & 1) * 4); };   // row / 2 % 8 is lane / 16, and 4 more for odd i
     uint32_t off[MT * 2];
 #pragma unroll
     for (int i = 0; i < MT * 2; ++i) {
         const int row = i * 8 + (lane >> 3);
-        const uint32_t at = static_cast<uint32_t>(min(row, p.M - 1 - row0) * static_cast<int>(p.lda) + granule * 16);
+        const uint32_t at = static_cast<uint32_t>(min(row, p.M - 1 - row0) * static_cast<int>(p.lda) + granule(i) * 16);
         off[i] = ROWS16 && row0 + row >= p.M ? kOutOfRange : at;   // rows past M: zeros, or the last row's; not stored
     }
     uint8_t* ring = s_all + wave * (D * kStep);
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
         for (int i = 0; i < MT * 2; ++i) {
             if constexpr (ROWS16) {
                 uint32_t o = off[i];
-                if (last) o = next * 128 + granule * 16 < p.K ? o : kOutOfRange;
+                if (last) o = next * 128 + granule(i) * 16 < p.K ? o : kOutOfRange;
                 copy_to_lds(rows, ring + slot * kStep + i * 1024, static_cast<int>(o), next * 128);
             } else {
                 ra[slot][i] = load_any<kI8>(first + next * 128 + off[i]);
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
         for (int c = 0; c < CT; ++c) acc[m][c] = intx4{0, 0, 0, 0};
     constexpr int LOADS = MT * 2 + CT * 2;
     // operand l of row tile m: row m * 16 + lane % 16, granule l * 4 + lane / 16
-    const int fr = (lane & 15) * 128 + ((lane >> 4) ^ (lane & 7)) * 16;
+    const int fr = (lane & 15) * 128 + ((lane >> 4) ^ ((lane & 15) >> 1)) * 16;
     auto multiply = [&](int slot) __attribute__((always_inline)) {
         if constexpr (!ROWS16) {
 #pragma unroll
@@ -192,16 +193,16 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
     };
     if constexpr (!ROWS16) {
         if (ends_here) {                               // whole granules, and the row's last 16 bytes for the one K ends in
-            const int k = (nk - 1) * 128 + granule * 16;
             const uint8_t* start = b;
             b += static_cast<int64_t>(nk - 1 - wave) * step_bytes<false>();
             load_weights_of(0);
             b = start;
 #pragma unroll
             for (int i = 0; i < MT * 2; ++i) {
-                const uint8_t* row = first + off[i] - granule * 16;
+                const int k = (nk - 1) * 128 + granule(i) * 16;
+                const uint8_t* row = first + off[i] - granule(i) * 16;
                 if (p.K < 16) {                        // uniform
-                    ra[0][i] = load_tail<kI8>(row, granule * 8, p.K);
+                    ra[0][i] = load_tail<kI8>(row, granule(i) * 8, p.K);
                 } else {
                     const u32x4 v = load_any<kI8>(row + min(k, p.K - 16)), end = shift_down(v, (16 - p.K % 16) & 15);
                     ra[0][i] = k + 16 <= p.K ? v : k < p.K ? end : u32x4{0u, 0u, 0u, 0u};
@@ -268,6 +269,176 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
     });
 }
 
+// ---- many rows: two workgroups to a CU -------------------------------------------------------
+// A workgroup of 4 waves owns NA * 32 rows x four 64-column pairs, a pair to a wave: NA x 2 tiles of
+// v_mfma_i32_32x32x32.  A stage is 128 k.  The rows reach LDS by direct copies into a ring of four stages (granules XORed
+// by row / 2 % 8, as above: no bank conflicts), one barrier a stage; each weight belongs to one wave and goes straight to
+// its registers, two stages of it.  Two workgroups share a CU, and while one is at its barrier, its loads or its
+// epilogue, which at 6000 x 4096 x 4096 is a seventh of its time, the other multiplies.
+// The loop has no branch around a load and the fragments of a step are asked for before the step before is multiplied:
+// 6000 x 4096 x 4096 97.8 us (2060 TOP/s; a library product 101.7), with bias and SiLU 100.1, 107 with such branches;
+// gated, 1536 columns, 77; the 16-bit products' kernel, one workgroup of 8 waves to a CU: 109, 110 and 97 on the same
+// card.  Bound by the matrix unit at the clock that the power limit leaves (1.75 GHz: half of the cycles multiply) and the
+// latency of the weights.
+template <bool VEC, int NA>
+__global__ __launch_bounds__(256, 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+    constexpr int UM = NA * 32, kStage = UM * 128, kStages = 4;
+    __shared__ __attribute__((aligned(16))) uint8_t s_a[kStages * kStage > 16384 ? kStages * kStage : 16384];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = gridDim.x, blk = blockIdx.x;
+    // one contiguous range of tiles per XCD, 8 row tiles x 4 column tiles of it at a time
+    const int lid = (G % 8 == 0) ? (blk % 8) * (G / 8) + (blk / 8) : blk;
+    constexpr int kGroup = 8;
+    const int group = lid / (kGroup * ntiles), in = lid - group * kGroup * ntiles;
+    const int gm = min(kGroup, mtiles - group * kGroup);
+    const int n_tile = in / gm, m_tile = group * kGroup + in - n_tile * gm;
+    const int row0 = m_tile * UM, pair = n_tile * 4 + wave;
+    const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.a)) + static_cast<int64_t>(row0) * p.lda, 0, kBufferRange, kBufferFlags);
+    uint32_t off[NA];
+    int granule[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+        const int row = (wave * NA + i) * 8 + (lane >> 3);
+        granule[i] = (lane & 7) ^ ((row >> 1) & 7);
+        off[i] = row0 + row < p.M ? static_cast<uint32_t>(row * static_cast<int>(p.lda) + granule[i] * 16) : kOutOfRange;
+    }
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) +
+                       static_cast<int64_t>(min(pair, pairs - 1)) * (p.Kp / 64) * step_bytes<false>() + lane * 16;
+    const int nk = p.Kp / 64;
+    u32x4 wb[2][4][2];                                 // [stage % 2][32 k][column half]
+    auto load_a = [&](int s, auto inside) __attribute__((always_inline)) {
+        const bool last = !decltype(inside)::value && s * 64 + 64 > p.Kh;   // uniform: K ends in the stage
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            uint32_t o = off[i];
+            if (last) o = s * 64 + granule[i] * 8 < p.Kh ? o : kOutOfRange;
+            copy_to_lds(rows, s_a + (s & 3) * kStage + (wave * NA + i) * 1024, static_cast<int>(o), s * 128);
+        }
+    };
+    auto load_bk = [&](int s, auto buf, int k) __attribute__((always_inline)) {
+        const uint8_t* at = b + static_cast<int64_t>(s) * step_bytes<false>();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            wb[decltype(buf)::value][k][h] = *reinterpret_cast<const u32x4*>(at + k * 2048 + h * 1024);
+    };
+    auto load_b = [&](int s, auto buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load_bk(s, buf, k);
+    };
+    intx16 acc[NA][2];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    const int fr = (lane & 31) * 128;
+    // Stage s, its weights in buffer s % 2.  Loads are issued in the order A(s + 1), B(s), A(s + 2), B(s + 1), ..., so when all
+    // but A(s + 2) and B(s + 1) have landed, stage s is here; behind the barrier every wave's part of it is, and the place of
+    // stage s - 1, A(s + 3)'s, is no longer read.
+    auto stage = [&](int s, auto buf, auto inside) __attribute__((always_inline)) {
+        constexpr int B = decltype(buf)::value;
+        constexpr bool kInside = decltype(inside)::value;
+        if (kInside || s + 2 < nk) wait_vmcnt<NA + 8>();
+        else if (s + 1 < nk) wait_vmcnt<8>();
+        else wait_vmcnt<0>();
+        phase_end();
+        if (kInside || s + 3 < nk) load_a(s + 3, inside);
+        const uint8_t* at = s_a + (s & 3) * kStage + fr;
+        u32x4 a[2][NA];
+        auto read = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+                a[k & 1][i] = *reinterpret_cast<const u32x4*>(at + i * 4096 + (((k * 2 + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16));
+        };
+        read(0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < 3) read(k + 1);
+            __builtin_amdgcn_sched_barrier(0);         // the next fragments are asked for before these are multiplied
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                acc[i][0] = mfma32d<kI8>(a[k & 1][i], wb[B][k][0], acc[i][0]);
+                acc[i][1] = mfma32d<kI8>(a[k & 1][i], wb[B][k][1], acc[i][1]);
+            }
+            if (kInside || s + 2 < nk) load_bk(s + 2, buf, k);
+        }
+    };
+    int s = 0;
+    if (nk > 5) {                                      // no branch around a load, here and in the loop: the compiler counts
+        load_a(0, IntC<1>{});
+        load_a(1, IntC<1>{});
+        load_b(0, IntC<0>{});
+        load_a(2, IntC<1>{});
+        load_b(1, IntC<1>{});
+        do {
+            stage(s, IntC<0>{}, IntC<1>{});
+            stage(s + 1, IntC<1>{}, IntC<1>{});
+            s += 2;
+        } while (s + 5 < nk);
+    } else {
+        load_a(0, IntC<0>{});
+        if (nk > 1) load_a(1, IntC<0>{});
+        load_b(0, IntC<0>{});
+        if (nk > 2) load_a(2, IntC<0>{});
+        if (nk > 1) load_b(1, IntC<1>{});
+    }
+    for (; s < nk; s += 2) {
+        stage(s, IntC<0>{}, IntC<0>{});
+        if (s + 1 < nk) stage(s + 1, IntC<1>{}, IntC<0>{});
+    }
+    phase_end_lds();
+    const int col = pair * (p.gated ? 32 : 64) + (p.gated ? lane & 7 : lane & 15) * 4;
+    const Columns columns = load_columns<kI8>(p, col);
+    float sa[(NA + 1) / 2];                            // of the rows lane, lane + 64
+#pragma unroll
+    for (int i = 0; i < (NA + 1) / 2; ++i) sa[i] = p.sa[min(row0 + i * 64 + lane, p.M - 1)];
+    int(*mine)[64] = reinterpret_cast<int(*)[64]>(s_a + wave * 4096);
+    finish_tile<kI8, NA, 1, 1>(Finisher<kI8, VEC>(p, row0), acc, mine, mine, 0, 0, col, columns, sa);
+}
+
+// Rows of a tile: the least time expected.  Tiles take a launch, and the busiest CU's tiles one after another, each a fixed
+// part and a part by the reduction (ns, of 4096 k); a CU's only tile waits for its loads a little longer.  Within 12 % of
+// measured times from 18 to 480 us.
+struct TileCost {
+    double ends, whole;
+};
+constexpr TileCost kTileCosts[] = {{1100, 12500}, {2100, 17900}, {5300, 23300}, {8500, 30000}};   // 32, 64, 96, 128 rows
+
+Choice int8_tile_choice(const DenseArgs& p, int64_t pairs) {
+    Choice best{0, 0.0};
+    for (int i = 0; i < 4; ++i) {
+        const int rows = (i + 1) * 32;
+        const int64_t tiles = (p.M + rows - 1) / rows * ((pairs + 3) / 4), each = (tiles + kCUs - 1) / kCUs;
+        if (tiles >= 1 << 24) continue;                // a grid's limit is 2^32 threads
+        const double one = kTileCosts[i].ends + (kTileCosts[i].whole - kTileCosts[i].ends) * p.Kp / 2048;
+        const double ns = 5000.0 + each * one * (each == 1 ? 1.15 : 1.0);
+        if (best.ns == 0.0 || ns < best.ns) best = Choice{i, ns};
+    }
+    return best;
+}
+
+template <bool VEC, int NA>
+int launch_int8_tile(const DenseArgs& p, int64_t pairs, hipStream_t st) {
+    const int ntiles = static_cast<int>((pairs + 3) / 4), mtiles = (p.M + NA * 32 - 1) / (NA * 32);
+    hipLaunchKernelGGL((int8_tile_kernel<VEC, NA>), dim3(static_cast<unsigned>(mtiles * ntiles)), dim3(256), 0, st, p, mtiles,
+                       ntiles, static_cast<int>(pairs));
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+template <bool VEC>
+int launch_int8_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
+    switch (shape) {
+        case 0: return launch_int8_tile<VEC, 1>(p, pairs, st);
+        case 1: return launch_int8_tile<VEC, 2>(p, pairs, st);
+        case 2: return launch_int8_tile<VEC, 3>(p, pairs, st);
+        default: return launch_int8_tile<VEC, 4>(p, pairs, st);
+    }
+}
+
 // Unit shapes of int8_rows_kernel, and the time expected of each: a launch, what the shape takes at the ends (ns), and
 // what the busiest CU reads (bytes/ns), its first unit and then the others at the rate they reach together; rows off 16
 // bytes pass through registers, more slowly (32 rows x 64 columns then leave room for one workgroup on a CU: not taken).
@@ -285,6 +456,7 @@ Choice rows_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
         const RowsShape& u = kRowsShapes[i];
         if (!rows16 && u.rate_any == 0) continue;
         const int rows = u.mt * kRowTile;
+        if ((p.M + rows - 1) / rows > 65535) continue; // the grid's limit; the tallest shape stays within it
         const int64_t groups = pairs * (4 / u.ct) * ((p.M + rows - 1) / rows), each = (groups + kCUs - 1) / kCUs;
         const double bytes = (std::min(rows, p.M) + u.ct * kRowTile) * 2.0 * p.Kp;
         const double ns = 2300.0 + u.ends + bytes / (rows16 ? 80 : 65) +
@@ -374,10 +546,10 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
         if (stream_choice(p, pairs, true).shape == kUnitShape11) return launch_stream_tiles<kI8, true, 1, 1>(p, pairs, st);
         return launch_stream_tiles<kI8, true, 1, 2>(p, pairs, st);
     }
-    // 1024 x 4096 x 4096: tiles 26.8 us, 33.6 by rows; 512 x 1536 x 4096: 15.2 and 10.9
-    const Choice tile = tile_choice(p, pairs);
-    if (tile.ns < rows.ns)
-        return p.vec ? launch_tiles<kI8, true>(p, pairs, tile.shape, st) : launch_tiles<kI8, false>(p, pairs, tile.shape, st);
+    // 1024 x 4096 x 4096: tiles 27 us, 34 by rows; 512 x 1536 x 4096: 18 and 10.9
+    const Choice tile = int8_tile_choice(p, pairs);
+    if (tile.ns > 0.0 && tile.ns < rows.ns)
+        return p.vec ? launch_int8_tiles<true>(p, pairs, tile.shape, st) : launch_int8_tiles<false>(p, pairs, tile.shape, st);
     return p.vec ? launch_rows<true, true>(p, pairs, rows.shape, st) : launch_rows<false, true>(p, pairs, rows.shape, st);
 }
 
