@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 // card.  Bound by the matrix unit at the clock that the power limit leaves (1.75 GHz: half of the cycles multiply) and the
 // latency of the weights.
 template <bool VEC, int NA>
-__global__ __launch_bounds__(256, 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+__global__ __launch_bounds__(256, NA == 1 ? 4 : NA == 2 ? 3 : 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
     constexpr int UM = NA * 32, kStage = UM * 128, kStages = 4;
     __shared__ __attribute__((aligned(16))) uint8_t s_a[kStages * kStage > 16384 ? kStages * kStage : 16384];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -440,15 +440,16 @@ int launch_int8_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t 
 }
 
 // Unit shapes of int8_rows_kernel, and the time expected of each: a launch, what the shape takes at the ends (ns), and
-// what the busiest CU reads (bytes/ns), its first unit and then the others at the rate they reach together; rows off 16
-// bytes pass through registers, more slowly (32 rows x 64 columns then leave room for one workgroup on a CU: not taken).
-// Mostly within 15 % of measured times from 3.5 to 60 us, and the shape chosen within 8 % of the best.
+// what the busiest CU reads (bytes/ns), its first unit and then the others at the rate they reach together, but no less
+// than a unit takes anyhow; rows off 16 bytes pass through registers, more slowly (32 rows x 64 columns then leave room
+// for one workgroup on a CU: not taken).  Mostly within 15 % of measured times from 3.5 to 60 us, and the shape chosen
+// within 8 % of the best.
 struct RowsShape {
     int mt, ct;
-    double ends, rate, rate_any;
+    double ends, rate, rate_any, least;
 };
-constexpr RowsShape kRowsShapes[] = {
-    {1, 2, 800, 106, 60}, {2, 2, 800, 106, 58}, {1, 4, 1000, 106, 75}, {2, 4, 950, 106, 0}, {4, 4, 2000, 62, 45}};
+constexpr RowsShape kRowsShapes[] = {{1, 2, 800, 106, 60, 500}, {2, 2, 800, 106, 58, 950}, {1, 4, 1000, 106, 75, 900},
+                                     {2, 4, 950, 95, 0, 1150}, {4, 4, 2000, 62, 45, 3600}};
 
 Choice rows_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
     Choice best{0, 0.0};
@@ -460,7 +461,7 @@ Choice rows_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
         const int64_t groups = pairs * (4 / u.ct) * ((p.M + rows - 1) / rows), each = (groups + kCUs - 1) / kCUs;
         const double bytes = (std::min(rows, p.M) + u.ct * kRowTile) * 2.0 * p.Kp;
         const double ns = 2300.0 + u.ends + bytes / (rows16 ? 80 : 65) +
-                          (each - 1) * (bytes / (rows16 ? u.rate : u.rate_any) + u.ends / 4);
+                          (each - 1) * std::max(bytes / (rows16 ? u.rate : u.rate_any) + u.ends / 8, u.least);
         if (best.ns == 0.0 || ns < best.ns) best = Choice{i, ns};
     }
     return best;

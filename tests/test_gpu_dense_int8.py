@@ -99,18 +99,30 @@ def test_sizes(size, gated):
     run(*size, act="swiglu" if gated else "none", c="bf16", bias=True, residual="bf16", seed=1 + sum(size), pad=16)
 
 
-# sizes that take each unit and tile shape of the 16-bit products' rule, ungated and gated, in twice the codes
-SHAPES = [(5, 4100, 80), (17, 2050, 80), (17, 4100, 80), (48, 4100, 80), (200, 200, 80), (65, 16400, 528), (2050, 1000, 80),
-          (2050, 4100, 80), (600, 16400, 80), (513, 70, 1040), (513, 70, 80), (5, 4100, 263), (17, 2050, 263),
-          (17, 4100, 263), (48, 4100, 2063), (128, 4100, 263)]
-SHAPES_GATED = [(5, 2050, 80), (48, 2050, 80), (65, 8200, 528), (1030, 1000, 80), (300, 12300, 144), (200, 16400, 144),
-                (200, 200, 80), (513, 70, 1040), (513, 70, 80), (5, 2050, 263), (17, 2050, 263), (200, 200, 263),
-                (48, 2050, 2063), (128, 2050, 263)]
+# a size or more for each kernel and shape, ungated and gated: a few rows; rows through LDS, with one turn of the ring and
+# several; tiles of 32 to 128 rows, with fewer stages than the ring has and more; rows off 16 bytes
+SHAPES = [(1, 3000, 144), (8, 70, 144), (9, 64, 144), (33, 70, 9008), (100, 2050, 1040), (166, 2739, 16), (256, 4098, 2064),
+          (128, 4098, 4112), (4214, 21, 16), (512, 4098, 1040), (6157, 194, 16), (6201, 917, 16), (6100, 500, 400),
+          (2048, 4098, 1040), (4121, 1234, 880), (6403, 1794, 1728),
+          (5, 4100, 263), (33, 70, 9001), (64, 4098, 4111), (166, 2739, 15), (100, 2050, 1039), (128, 4098, 4113),
+          (4730, 70, 7), (512, 4098, 1037)]
+SHAPES_GATED = [(1, 3000, 144), (8, 70, 144), (9, 64, 144), (33, 70, 9008), (68, 2887, 16), (100, 2050, 1040), (128, 4098, 4112),
+                (64, 4098, 4112), (512, 4098, 1040), (6256, 110, 16), (5244, 518, 16), (4121, 1234, 880), (4507, 1339, 1824),
+                (17, 2050, 263), (64, 2050, 4111), (128, 2050, 2063), (1, 4127, 11), (4374, 42, 7)]
 
 
 @pytest.mark.parametrize("size,act", [(s, "relu") for s in SHAPES] + [(s, "swiglu") for s in SHAPES_GATED])
-def test_unit_and_tile_shapes(size, act):
+def test_kernels_and_shapes(size, act):
     run(*size, act, c="f32", bias=True, residual="bf16", pad=16, seed=sum(size))
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 72, 272), (300, 520, 272), (6100, 512, 272), (40, 72, 271)])
+@pytest.mark.parametrize("c", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("residual", [None, "f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+def test_four_columns_at_once(M, N, K, c, residual, act):
+    """N and the strides multiples of four: every type of the output and of the residual."""
+    run(M, N, K, act=act, c=c, residual=residual, bias=True, pad=16, seed=M)
 
 
 @pytest.mark.parametrize("act", list(EPI))
