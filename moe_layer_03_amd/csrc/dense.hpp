@@ -765,7 +765,8 @@ __device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const 
 #pragma unroll
             for (int i = 0; i < R; ++i) part[i] = f.load(first + g * 16 + mine0 + i * KG * dr + lr, col);
         };
-        if (mine0 < 16) load(0);
+        constexpr bool kAhead = KIND == kI8 || NA < 4;         // 128 float32 sums and 48 of fragments leave no room for it
+        if (kAhead && mine0 < 16) load(0);
 #pragma unroll 1
         for (int g = 0; g < NA * 2; ++g) {
             switch (g) {                               // uniform
@@ -781,9 +782,10 @@ __device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const 
             if constexpr (KG > 1) phase_end_lds();
             if (mine0 < 16) {
                 u32x4 now[R];
+                if constexpr (!kAhead) load(g);
 #pragma unroll
                 for (int i = 0; i < R; ++i) now[i] = part[i];
-                if (g + 1 < NA * 2) load(g + 1);
+                if (kAhead && g + 1 < NA * 2) load(g + 1);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const int r = mine0 + i * KG * dr + lr, x = (r & 4) * 8;

@@ -270,6 +270,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 }
 
 // ---- many rows: two workgroups to a CU -------------------------------------------------------
+// (three of them with tiles of 64 rows and less).
 // A workgroup of 4 waves owns NA * 32 rows x four 64-column pairs, a pair to a wave: NA x 2 tiles of
 // v_mfma_i32_32x32x32.  A stage is 128 k.  The rows reach LDS by direct copies into a ring of four stages (granules XORed
 // by row / 2 % 8, as above: no bank conflicts), one barrier a stage; each weight belongs to one wave and goes straight to
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 // card.  Bound by the matrix unit at the clock that the power limit leaves (1.75 GHz: half of the cycles multiply) and the
 // latency of the weights.
 template <bool VEC, int NA>
-__global__ __launch_bounds__(256, NA == 1 ? 4 : NA == 2 ? 3 : 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+__global__ __launch_bounds__(256, NA == 1 || (NA == 2 && VEC) ? 3 : 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
     constexpr int UM = NA * 32, kStage = UM * 128, kStages = 4;
     __shared__ __attribute__((aligned(16))) uint8_t s_a[kStages * kStage > 16384 ? kStages * kStage : 16384];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(256, NA == 1 ? 4 : NA == 2 ? 3 : 2) void int8_tile_
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k < 3) read(k + 1);
-            __builtin_amdgcn_sched_barrier(0);         // the next fragments are asked for before these are multiplied
+            if constexpr (NA > 2) __builtin_amdgcn_sched_barrier(0);   // the next fragments are asked for before these are multiplied
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
                 acc[i][0] = mfma32d<kI8>(a[k & 1][i], wb[B][k][0], acc[i][0]);
