@@ -541,8 +541,10 @@ int moe_pack_dense_int8(const moe_dense_shape* s, const void* w, const void* w_u
 
 /*
  * moe_dense_gemm_int8 -- the product on packed codes.
- *   a: rows of K codes, lda >= K apart, any alignment (rows that all start on 16
- *       bytes, with K a multiple of 16, take the fast paths); a_scales float32 [M].
+ *   a: rows of K codes, lda >= K apart, any alignment; a_scales float32 [M].
+ *       Rows that all start on 16 bytes take the fast paths (with K a multiple of
+ *       16 all of them; otherwise up to 15 bytes between a row's end and the next
+ *       row may be read, which change nothing).
  *   epilogue, bias, residual, c and their types and strides as in
  *   moe_dense_gemm(): the residual may be c itself.
  */

@@ -88,7 +88,10 @@ __global__ __launch_bounds__(256) void pack_dense_int8_kernel(const ST* __restri
 // (past the caches 9.7 us at 128 x 4096 x 4096, against 7.8).
 // Bound by what a CU reads, some 106 bytes/ns once it has several workgroups and 80 with one: 64 x 4096 x 4096 6.6 us,
 // 128 rows 7.8, 256 rows 10.6, of which a launch is 2.3.
-// ROWS16: rows on 16 bytes and K a multiple of 16, copied directly.  Otherwise they go through registers.
+// ROWS16: rows on 16 bytes, copied directly.  PART: K ends inside a granule.  The codes behind it up to the next 16 bytes
+// come along, from between the rows, and meet zero weights; behind the last row there may be nothing, so that one's
+// end is put there code by code (1000 x 1003 x 1100 on rows 1104 apart 8.6 us, 11.0 through registers; in the other
+// kernels this would cost 3 %).  Rows off 16 bytes go through registers.
 constexpr int kDepth = 2;
 
 // Bytes n .. 15 of v moved down to 0 .., zeros behind them; n uniform, 0 to 15.
@@ -100,7 +103,7 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
                  __builtin_amdgcn_alignbyte(v[3], v[2], b), __builtin_amdgcn_alignbyte(0u, v[3], b)};
 }
 
-template <bool VEC, bool ROWS16, int MT, int CT>
+template <bool VEC, bool ROWS16, bool PART, int MT, int CT>
 __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(DenseArgs p) {
     constexpr int kStep = MT * 16 * 128;               // bytes of the rows' part of a step
     constexpr int D = kDepth, kRing = kNW * D * kStep, kRed = kNW * MT * CT * 1024;
@@ -145,7 +148,13 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
         for (int i = 0; i < MT * 2; ++i) {
             if constexpr (ROWS16) {
                 uint32_t o = off[i];
-                if (last) o = next * 128 + granule(i) * 16 < p.K ? o : kOutOfRange;
+                if (last && !PART) {
+                    o = next * 128 + granule(i) * 16 < p.K ? o : kOutOfRange;
+                } else if (last) {
+                    const int end = p.K - next * 128 - granule(i) * 16;      // codes of the granule that exist
+                    const bool last_row = row0 + i * 8 + (lane >> 3) == p.M - 1;
+                    o = end >= 16 || (end > 0 && !last_row) ? o : kOutOfRange;
+                }
                 copy_to_lds(rows, ring + slot * kStep + i * 1024, static_cast<int>(o), next * 128);
             } else {
                 ra[slot][i] = load_any<kI8>(first + next * 128 + off[i]);
@@ -191,6 +200,13 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
         if constexpr (ROWS16) wait_lgkmcnt0();
         asm volatile("" ::: "memory");
     };
+    // the granule that K ends in, of the last row, and its place in a step
+    u32x4 row_end = {0u, 0u, 0u, 0u};
+    const int end_row = p.M - 1 - row0, end_granule = p.K / 16 % 8;
+    const int end_place = (end_row >> 3) * 1024 + (end_row & 7) * 128 + ((end_granule ^ (end_row >> 1)) & 7) * 16;
+    const bool put_end = PART && end_row < MT * 16 && (nk - 1) % kNW == wave;   // uniform
+    if (put_end && lane == 0)
+        row_end = load_tail<kI8>(first + static_cast<int64_t>(end_row) * p.lda, (nk - 1) * 64 + end_granule * 8, p.K);
     if constexpr (!ROWS16) {
         if (ends_here) {                               // whole granules, and the row's last 16 bytes for the one K ends in
             const uint8_t* start = b;
@@ -228,6 +244,8 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
         if (i + j < steps) {                           // uniform
             if (i + j + D <= steps) landed(IntC<D - 1>{});
             else landed(IntC<0>{});
+            if (put_end && i + j == steps - 1 && lane == 0)
+                *reinterpret_cast<u32x4*>(ring + j % D * kStep + end_place) = row_end;
             multiply(j % D);
             if (j < D && i + j + D < steps) {
                 read();
@@ -468,18 +486,18 @@ Choice rows_choice(const DenseArgs& p, int64_t pairs, bool rows16) {
     return best;
 }
 
-template <bool VEC, bool ROWS16>
+template <bool VEC, bool ROWS16, bool PART>
 int launch_rows(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
     const RowsShape& u = kRowsShapes[shape];
     const dim3 g(static_cast<unsigned>(pairs * (4 / u.ct)), (p.M + u.mt * kRowTile - 1) / (u.mt * kRowTile));
     switch (shape) {
-        case 0: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 1, 2>), g, dim3(kNW * 64), 0, st, p); break;
-        case 1: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 2, 2>), g, dim3(kNW * 64), 0, st, p); break;
-        case 2: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 1, 4>), g, dim3(kNW * 64), 0, st, p); break;
+        case 0: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, PART, 1, 2>), g, dim3(kNW * 64), 0, st, p); break;
+        case 1: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, PART, 2, 2>), g, dim3(kNW * 64), 0, st, p); break;
+        case 2: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, PART, 1, 4>), g, dim3(kNW * 64), 0, st, p); break;
         case 3:
-            if constexpr (ROWS16) hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 2, 4>), g, dim3(kNW * 64), 0, st, p);
+            if constexpr (ROWS16) hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, PART, 2, 4>), g, dim3(kNW * 64), 0, st, p);
             break;
-        default: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, 4, 4>), g, dim3(kNW * 64), 0, st, p); break;
+        default: hipLaunchKernelGGL((int8_rows_kernel<VEC, ROWS16, PART, 4, 4>), g, dim3(kNW * 64), 0, st, p); break;
     }
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -539,10 +557,12 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     p.Kp = k_padded<kI8>(s);
     const int64_t pairs = pairs_of(s);
     if (!rows_near(p)) return launch_any<kI8>(p, pairs, st);
-    const bool rows16 = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda % 16 == 0 && s.K % 16 == 0;
+    const bool rows16 = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda % 16 == 0;
     const Choice rows = rows_choice(p, pairs, rows16);
     if (!rows16)
-        return p.vec ? launch_rows<true, false>(p, pairs, rows.shape, st) : launch_rows<false, false>(p, pairs, rows.shape, st);
+        return p.vec ? launch_rows<true, false, false>(p, pairs, rows.shape, st) : launch_rows<false, false, false>(p, pairs, rows.shape, st);
+    if (s.K % 16 != 0)
+        return p.vec ? launch_rows<true, true, true>(p, pairs, rows.shape, st) : launch_rows<false, true, true>(p, pairs, rows.shape, st);
     // a few rows need no detour through LDS, and units of 16 columns: 1 x 4096 x 1536 3.1 us, 3.5 through LDS
     if (s.M <= kVeryFewRows) {
         if (stream_choice(p, pairs, true).shape == kUnitShape11) return launch_stream_tiles<kI8, true, 1, 1>(p, pairs, st);
@@ -552,7 +572,7 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     const Choice tile = int8_tile_choice(p, pairs);
     if (tile.ns > 0.0 && tile.ns < rows.ns)
         return p.vec ? launch_int8_tiles<true>(p, pairs, tile.shape, st) : launch_int8_tiles<false>(p, pairs, tile.shape, st);
-    return p.vec ? launch_rows<true, true>(p, pairs, rows.shape, st) : launch_rows<false, true>(p, pairs, rows.shape, st);
+    return p.vec ? launch_rows<true, true, false>(p, pairs, rows.shape, st) : launch_rows<false, true, false>(p, pairs, rows.shape, st);
 }
 
 }  // namespace moe

@@ -142,6 +142,23 @@ def test_rows_off_16_bytes(M, K, pad, offset):
     run(M, 70, K, act="swiglu", c="f16", residual="f16", pad=pad, offset=offset, seed=K)
 
 
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 15, 16, 17, 33, 64, 65, 130, 300, 1000])
+@pytest.mark.parametrize("K", [1, 15, 17, 100, 127, 129, 250, 1020, 1100, 2041, 4097])
+def test_rows_on_16_bytes_that_end_off_them(M, K):
+    """K ends inside 16 bytes, the rows start on them: what lies between the rows changes nothing, and behind the last row
+    nothing is read (it ends with its buffer)."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ld, N = (K + 15) // 16 * 16 + 16, 70
+    buf = torch.randint(-128, 128, ((M - 1) * ld + K,), generator=g, device="cuda").to(torch.int8)
+    a = buf.as_strided((M, K), (ld, 1))
+    d = inputs(1, N, K, "swiglu", seed=K)
+    sa = torch.rand(M, generator=g, device="cuda")
+    s = B.DenseShape(M, N, K, gated=True)
+    got = Q.moe_dense_gemm_int8(s, a, sa, pack(s, d), EPI["swiglu"], c_dtype=torch.float32)
+    ref, bound = reference(a, sa, d["w"], d["sw"], None, None, "swiglu", "f32")
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 100, 512, 777])
 @pytest.mark.parametrize("K", [16384, 16385])
 def test_sums_are_exact(M, K):
