@@ -85,9 +85,9 @@ __global__ __launch_bounds__(256) void pack_dense_int8_kernel(const ST* __restri
 // to LDS, eight lanes to a row, 8 accesses for a KiB, into a ring of its own: no barrier until the sums are joined.
 // A granule of 16 bytes lies at its place XOR row / 2 % 8, so that the 16 rows of a fragment read fall into all banks.
 // Two steps are in flight (three and four: no faster, and fewer workgroups fit a CU); weights are loaded as others are
-// (past the caches 9.7 us at 128 x 4096 x 4096, against 7.8).
-// Bound by what a CU reads, some 106 bytes/ns once it has several workgroups and 80 with one: 64 x 4096 x 4096 6.6 us,
-// 128 rows 7.8, 256 rows 10.6, of which a launch is 2.3.
+// (past the caches 9.7 us at 128 x 4096 x 4096, 7.8 on the same card).
+// Bound by what a CU reads, some 106 bytes/ns once it has several workgroups and 80 with one: 64 x 4096 x 4096 6.8 us,
+// 128 rows 8.7, 256 rows 11.3, of which a launch is 2.3.
 // ROWS16: rows on 16 bytes, copied directly.  PART: K ends inside a granule.  The codes behind it up to the next 16 bytes
 // come along, from between the rows, and meet zero weights; behind the last row there may be nothing, so that one's
 // end is put there code by code (1000 x 1003 x 1100 on rows 1104 apart 8.6 us, 11.0 through registers; in the other

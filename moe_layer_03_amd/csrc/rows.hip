@@ -140,9 +140,10 @@ __device__ __forceinline__ uint32_t most_of(const float (&v)[8]) {
 }
 
 // ---- int8 ----------------------------------------------------------------------
-// Eight codes, without the remainder (6000 x 4096 49.9 us, 52.0 with it, before the stores below).  v * inv + 1.5 * 2^23 rounds to the integer next to the product and leaves its two's complement in
-// the low bits; only where some product is next to a half, which one group of 64 x 8 in ten has, the remainder is
-// looked at (int8_code).  |v| <= 127.00001 scale, so no code passes 127.
+// Eight codes, without the remainder (6000 x 4096 49.9 us, 52.0 with it, before the stores went past the caches).
+// v * inv + 1.5 * 2^23 rounds to the integer next to the product and leaves its two's complement in the low bits;
+// only where some product is next to a half, which one group of 64 x 8 in ten has, the remainder is looked at
+// (int8_code).  |v| <= 127.00001 scale, so no code passes 127.
 __device__ __forceinline__ u32x2 int8_codes(const float (&v)[8], float scale, float inv) {
     if (scale != scale) return u32x2{0u, 0u};
     constexpr float kMagic = 12582912.0f;
