@@ -542,9 +542,9 @@ int moe_pack_dense_int8(const moe_dense_shape* s, const void* w, const void* w_u
 /*
  * moe_dense_gemm_int8 -- the product on packed codes.
  *   a: rows of K codes, lda >= K apart, any alignment; a_scales float32 [M].
- *       Rows that all start on 16 bytes take the fast paths (with K a multiple of
- *       16 all of them; otherwise up to 15 bytes between a row's end and the next
- *       row may be read, which change nothing).
+ *       Rows that all start on 16 bytes take the fast paths (where K is no
+ *       multiple of 16, up to 15 bytes between a row's end and the next row may be
+ *       read, which change nothing; nothing behind the last row's end is read).
  *   epilogue, bias, residual, c and their types and strides as in
  *   moe_dense_gemm(): the residual may be c itself.
  */

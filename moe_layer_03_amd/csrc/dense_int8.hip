@@ -294,6 +294,8 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 // by row / 2 % 8, as above: no bank conflicts), one barrier a stage; each weight belongs to one wave and goes straight to
 // its registers, two stages of it.  Two workgroups share a CU, and while one is at its barrier, its loads or its
 // epilogue, which at 6000 x 4096 x 4096 is a seventh of its time, the other multiplies.
+// Where K ends inside a granule the last stage's copies bring what lies behind it, but the last row's end comes code by
+// code, as above (2000 x 4096 x 4090, rows 4096 apart, 42.2 us, 71.3 by int8_rows_kernel; K 4096 42.2).
 // The loop has no branch around a load and the fragments of a step are asked for before the step before is multiplied:
 // 6000 x 4096 x 4096 97.8 us (2060 TOP/s; a library product 101.7), with bias and SiLU 100.1, 107 with such branches;
 // gated, 1536 columns, 77; the 16-bit products' kernel, one workgroup of 8 waves to a CU: 109, 110 and 97 on the same
@@ -326,13 +328,18 @@ __global__ __launch_bounds__(256, NA == 1 || (NA == 2 && VEC) ? 3 : 2) void int8
     const uint8_t* b = reinterpret_cast<const uint8_t*>(p.b) +
                        static_cast<int64_t>(min(pair, pairs - 1)) * (p.Kp / 64) * step_bytes<false>() + lane * 16;
     const int nk = p.Kp / 64;
+    const int end_row = p.M - 1 - row0;                // as in int8_rows_kernel: its end comes code by code
     u32x4 wb[2][4][2];                                 // [stage % 2][32 k][column half]
     auto load_a = [&](int s, auto inside) __attribute__((always_inline)) {
         const bool last = !decltype(inside)::value && s * 64 + 64 > p.Kh;   // uniform: K ends in the stage
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             uint32_t o = off[i];
-            if (last) o = s * 64 + granule[i] * 8 < p.Kh ? o : kOutOfRange;
+            if (last) {
+                const int end = p.K - s * 128 - granule[i] * 16;             // codes of the granule that exist
+                const bool last_row = (wave * NA + i) * 8 + (lane >> 3) == end_row;
+                o = end >= 16 || (end > 0 && !last_row) ? o : kOutOfRange;
+            }
             copy_to_lds(rows, s_a + (s & 3) * kStage + (wave * NA + i) * 1024, static_cast<int>(o), s * 128);
         }
     };
@@ -363,6 +370,16 @@ __global__ __launch_bounds__(256, NA == 1 || (NA == 2 && VEC) ? 3 : 2) void int8
         if (kInside || s + 2 < nk) wait_vmcnt<NA + 8>();
         else if (s + 1 < nk) wait_vmcnt<8>();
         else wait_vmcnt<0>();
+        if constexpr (!kInside) {
+            if (s + 1 == nk && p.K % 16 != 0 && (end_row >> 3) / NA == wave) {     // uniform
+                const int g = p.K / 16 % 8;
+                const uint8_t* row = reinterpret_cast<const uint8_t*>(p.a) + static_cast<int64_t>(p.M - 1) * p.lda;
+                if (lane == 0)
+                    *reinterpret_cast<u32x4*>(s_a + (s & 3) * kStage + (end_row >> 3) * 1024 + (end_row & 7) * 128 +
+                                              ((g ^ (end_row >> 1)) & 7) * 16) = load_tail<kI8>(row, s * 64 + g * 8, p.K);
+                wait_lgkmcnt0();
+            }
+        }
         phase_end();
         if (kInside || s + 3 < nk) load_a(s + 3, inside);
         const uint8_t* at = s_a + (s & 3) * kStage + fr;
@@ -561,10 +578,8 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     const Choice rows = rows_choice(p, pairs, rows16);
     if (!rows16)
         return p.vec ? launch_rows<true, false, false>(p, pairs, rows.shape, st) : launch_rows<false, false, false>(p, pairs, rows.shape, st);
-    if (s.K % 16 != 0)
-        return p.vec ? launch_rows<true, true, true>(p, pairs, rows.shape, st) : launch_rows<false, true, true>(p, pairs, rows.shape, st);
     // a few rows need no detour through LDS, and units of 16 columns: 1 x 4096 x 1536 3.1 us, 3.5 through LDS
-    if (s.M <= kVeryFewRows) {
+    if (s.M <= kVeryFewRows && s.K % 16 == 0) {
         if (stream_choice(p, pairs, true).shape == kUnitShape11) return launch_stream_tiles<kI8, true, 1, 1>(p, pairs, st);
         return launch_stream_tiles<kI8, true, 1, 2>(p, pairs, st);
     }
@@ -572,6 +587,8 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     const Choice tile = int8_tile_choice(p, pairs);
     if (tile.ns > 0.0 && tile.ns < rows.ns)
         return p.vec ? launch_int8_tiles<true>(p, pairs, tile.shape, st) : launch_int8_tiles<false>(p, pairs, tile.shape, st);
+    if (s.K % 16 != 0)
+        return p.vec ? launch_rows<true, true, true>(p, pairs, rows.shape, st) : launch_rows<false, true, true>(p, pairs, rows.shape, st);
     return p.vec ? launch_rows<true, true, false>(p, pairs, rows.shape, st) : launch_rows<false, true, false>(p, pairs, rows.shape, st);
 }
 

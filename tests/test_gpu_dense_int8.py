@@ -159,6 +159,22 @@ def test_rows_on_16_bytes_that_end_off_them(M, K):
     assert ((got.double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("M", [900, 1537, 2047, 3000, 4001])
+@pytest.mark.parametrize("K", [17, 250, 383, 700, 1100, 2041])
+def test_many_rows_on_16_bytes_that_end_off_them(M, K):
+    """The same in tiles; every K of a full last tile and of a tile with a few rows, and integers that float32 holds."""
+    g = torch.Generator(device="cuda").manual_seed(K + M)
+    ld, N = (K + 15) // 16 * 16, 2060
+    buf = torch.randint(-128, 128, ((M - 1) * ld + K,), generator=g, device="cuda").to(torch.int8)
+    a = buf.as_strided((M, K), (ld, 1))
+    w = torch.randint(-127, 128, (K, N), generator=g, device="cuda").to(torch.int8)
+    one = torch.ones(max(M, N), device="cuda")
+    s = B.DenseShape(M, N, K)
+    c = Q.moe_dense_gemm_int8(s, a, one[:M], Q.moe_pack_dense_int8(s, w, scales=one[:N]), 0, c_dtype=torch.float32)
+    exact = a.double() @ w.double()
+    assert torch.equal(c, exact.float())
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 100, 512, 777])
 @pytest.mark.parametrize("K", [16384, 16385])
 def test_sums_are_exact(M, K):
