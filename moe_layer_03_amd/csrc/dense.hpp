@@ -122,12 +122,13 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v)
     else static_cast<uint16_t*>(p)[i] = dtype == MOE_BF16 ? f32_to_bf16_or_nan(v) : f32_to_f16_or_nan(v);
 }
 
-// A sum with its scales.  The int32 sum and two products round once each.  The smaller factor comes first, but for
-// rows whose scale is above one, so that no product over- or underflows where the result does not: up to one,
-// sum * sa lies between sa and 2^31; above, sum * sw overflows only if the result does.
+// A sum with its scales, of either sign.  The int32 sum and two products round once each.  The row's scale comes first
+// where it is at most one in magnitude, the column's else, so that no product overflows where the result does not: up to
+// one, |sum * sa| lies between |sa| and 2^31; above, sum * sw overflows only if the result does.  Nor is a digit lost
+// below the normal numbers: an integer times a subnormal one is a multiple of its last digit.
 __device__ __forceinline__ float scaled(int v, float sa, float sw) {
     const float f = static_cast<float>(v);
-    return sa > 1.0f ? f * sw * sa : f * sa * sw;
+    return fabsf(sa) > 1.0f ? f * sw * sa : f * sa * sw;
 }
 
 // The element (row, col): v is its sum (gated: the gate's, u the up's).  The
@@ -187,8 +188,8 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 // Four sums with their scales, in the order of scaled().
 __device__ __forceinline__ floatx4 scaled4(const intx4& v, float sa, const floatx4& sw) {
     floatx4 f = __builtin_convertvector(v, floatx4);
-    if (__builtin_amdgcn_ballot_w64(sa > 1.0f) == 0) return f * sa * sw;
-    const bool big = sa > 1.0f;
+    const bool big = fabsf(sa) > 1.0f;
+    if (__builtin_amdgcn_ballot_w64(big) == 0) return f * sa * sw;
     const floatx4 all = {sa, sa, sa, sa};
     return f * (big ? sw : all) * (big ? all : sw);
 }
