@@ -194,59 +194,90 @@ __device__ __forceinline__ floatx4 scaled4(const intx4& v, float sa, const float
     return f * (big ? sw : all) * (big ? all : sw);
 }
 
-// C and R from the first row of a tile on, as buffers: the launcher keeps a tile's offsets below the range.
+// C and R from row `first` on, as buffers; the launcher keeps the offsets of the rows reached from there below the range.
+// A tile's epilogue goes on 16 rows at a time, which costs a few scalar instructions: so rows may lie 128 MiB apart (1024 x
+// 4096 x 4096 into rows 8 MiB apart 38 us; with one base for all of a tile's rows such C fell to dense_any_kernel, an
+// element at a time, 72 us).  A lane's row is u, uniform, and its own beyond that: the offset of a part of C or R is a
+// register, a scalar and a constant.
 template <int KIND, bool VEC>
 struct Finisher {
     const DenseArgs& p;
-    __amdgpu_buffer_rsrc_t c, r;
-    int rows;                  // rows of the tile that exist
+    const uint8_t *c_at, *r_at;
+    int c_rows, r_rows;        // rows from there on that exist
     int c_row, r_row;          // bytes of a row
     bool c_wide, r_wide;
+    int own, col;              // the lane's row beyond u, and its first column
+    uint32_t c_off, r_off;
 
-    __device__ __forceinline__ Finisher(const DenseArgs& args, int row0) : p(args) {
+    __device__ __forceinline__ Finisher(const DenseArgs& args, int first, int lane_row, int lane_col)
+        : p(args), own(lane_row), col(lane_col) {
         c_wide = p.c_dtype == MOE_F32;
         r_wide = p.r_dtype == MOE_F32;
         c_row = static_cast<int>(p.ldc) * (c_wide ? 4 : 2);
         r_row = static_cast<int>(p.ldr) * (r_wide ? 4 : 2);
-        auto buffer = [](const void* base, int64_t bytes) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + bytes, 0,
-                                                     kBufferRange, kBufferFlags);
-        };
-        c = buffer(p.c, static_cast<int64_t>(row0) * c_row);
-        r = buffer(p.r, static_cast<int64_t>(row0) * r_row);
-        rows = p.M - row0;
+        c_at = static_cast<const uint8_t*>(p.c) + static_cast<int64_t>(first) * c_row;
+        r_at = static_cast<const uint8_t*>(p.r) + static_cast<int64_t>(first) * r_row;
+        c_rows = r_rows = p.M - first;
+        c_off = own * c_row + col * (c_wide ? 4 : 2);
+        r_off = own * r_row + col * (r_wide ? 4 : 2);
     }
-    // The residual's four elements of a row of the tile: a word each, or (16-bit, VEC) two to a word.
-    __device__ __forceinline__ u32x4 load(int row, int col) const {
+    // The residual is loaded ahead of C: each goes on by itself.
+    __device__ __forceinline__ void next_c(int n) {
+        c_at += static_cast<int64_t>(c_row) * n;
+        c_rows -= n;
+    }
+    __device__ __forceinline__ void next_r(int n) {
+        r_at += static_cast<int64_t>(r_row) * n;
+        r_rows -= n;
+    }
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t buffer(const uint8_t* at) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), 0, kBufferRange, kBufferFlags);
+    }
+    // Offsets of the elements col .. col + 3, but for a constant each, `off` or out of range.  Opaque: the constants belong
+    // into the instructions, and one set of registers is then all that the branches on a type need; where they took some
+    // of their own, which loads of the other branch might be writing, they waited for all that is in flight (6000 x 4095 x
+    // 1024 onto a float32 residual 101 us, 105).
+    __device__ __forceinline__ void each(bool row, uint32_t off, uint32_t (&o)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i] = row && col + i < p.N ? off : kOutOfRange;
+            asm("" : "+v"(o[i]));
+        }
+    }
+    // The residual's four elements of the row: a word each, or (16-bit, VEC) two to a word.
+    __device__ __forceinline__ u32x4 load(int u) const {
         u32x4 q = {0u, 0u, 0u, 0u};
         if (p.r == nullptr) return q;                  // uniform, as the types are
+        const __amdgpu_buffer_rsrc_t r = buffer(r_at);
+        const bool row = own < r_rows - u;
+        const int at = u * r_row;
+        uint32_t o[4];
+        if constexpr (!VEC) each(row, r_off, o);
         if (r_wide) {
-            const uint32_t off = row * r_row + col * 4;
             if constexpr (VEC) {
                 q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  r, row < rows && col < p.N ? off : kOutOfRange, 0, 0));
+                                                  r, row && col < p.N ? r_off : kOutOfRange, at, 0));
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    q[i] = __builtin_amdgcn_raw_buffer_load_b32(r, row < rows && col + i < p.N ? off + 4 * i : kOutOfRange, 0, 0);
+                    q[i] = __builtin_amdgcn_raw_buffer_load_b32(r, o[i] + 4 * i, at, 0);
             }
         } else {
-            const uint32_t off = row * r_row + col * 2;
             if constexpr (VEC) {
                 const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
-                                                                  r, row < rows && col < p.N ? off : kOutOfRange, 0, 0));
+                                                                  r, row && col < p.N ? r_off : kOutOfRange, at, 0));
                 q[0] = v[0];
                 q[1] = v[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    q[i] = __builtin_amdgcn_raw_buffer_load_b16(r, row < rows && col + i < p.N ? off + 2 * i : kOutOfRange, 0, 0);
+                    q[i] = __builtin_amdgcn_raw_buffer_load_b16(r, o[i] + 2 * i, at, 0);
             }
         }
         return q;
     }
     template <int ACT>
-    __device__ __forceinline__ void finish(int row, int col, const typename Sums<KIND>::four& v0,
+    __device__ __forceinline__ void finish(int u_row, const typename Sums<KIND>::four& v0,
                                            const typename Sums<KIND>::four& u0, const Columns& k, float sa,
                                            const u32x4& q) const {
         floatx4 v, u;
@@ -281,16 +312,19 @@ struct Finisher {
                 }
             }
         }
+        const __amdgpu_buffer_rsrc_t c = buffer(c_at);
+        const bool row = own < c_rows - u_row;
+        const int at = u_row * c_row;
+        uint32_t o[4];
+        if constexpr (!VEC) each(row, c_off, o);
         if (c_wide) {
-            const uint32_t off = row * c_row + col * 4;
             if constexpr (VEC) {
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), c,
-                                                       row < rows && col < p.N ? off : kOutOfRange, 0, 0);
+                                                       row && col < p.N ? c_off : kOutOfRange, at, 0);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), c,
-                                                          row < rows && col + i < p.N ? off + 4 * i : kOutOfRange, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), c, o[i] + 4 * i, at, 0);
             }
             return;
         }
@@ -300,14 +334,13 @@ struct Finisher {
         else
             h = u32x2_t{f32_to_f16_or_nan(v[0]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[1])) << 16,
                         f32_to_f16_or_nan(v[2]) | static_cast<uint32_t>(f32_to_f16_or_nan(v[3])) << 16};
-        const uint32_t off = row * c_row + col * 2;
         if constexpr (VEC) {
-            __builtin_amdgcn_raw_buffer_store_b64(h, c, row < rows && col < p.N ? off : kOutOfRange, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(h, c, row && col < p.N ? c_off : kOutOfRange, at, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1))), c,
-                                                      row < rows && col + i < p.N ? off + 2 * i : kOutOfRange, 0, 0);
+                                                      o[i] + 2 * i, at, 0);
         }
     }
 };
@@ -371,7 +404,7 @@ __device__ __forceinline__ typename Sums<KIND>::four mfma16k(const u32x4& a, con
 constexpr int kAnyK = 128;
 constexpr int kAnyLd = kAnyK + 8;                      // LDS row, 16 of them in distinct banks
 constexpr int kAnyOut = 64 + 4;                        // row of sums on the way out
-// Rows of R and C: four elements at once, one at a time, or so far apart that a tile's pass a buffer's range.
+// Rows of R and C: four elements at once, one at a time, or so far apart that 16 of them pass a buffer's range.
 enum OutRows { kByFour = 0, kByOne = 1, kFarRows = 2 };
 
 template <int KIND, int OUT>
@@ -452,11 +485,11 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
                 s_c[(r0 + m * 16 + (lane >> 4) * 4 + i) * kAnyOut + h * 32 + c0 + (lane & 15)] = acc[m][h][i];
     const int lc = p.gated ? (tid & 7) * 4 : (tid & 15) * 4, dr = p.gated ? 32 : 16;
     const int col = pair * (p.gated ? 32 : 64) + lc;
-    int r = p.gated ? tid >> 3 : tid >> 4;
+    const int wr = wave * (p.gated ? 8 : 4), in_wave = p.gated ? lane >> 3 : lane >> 4;   // row wr + in_wave, then each dr-th
     if constexpr (OUT == kFarRows) {
         __syncthreads();
 #pragma unroll 1
-        for (; r < 64; r += dr)
+        for (int r = wr + in_wave; r < 64; r += dr)
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const Sum* e = s_c + r * kAnyOut + lc + i;
@@ -465,23 +498,26 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
         return;
     }
     typedef typename Sums<KIND>::four Sum4;
-    const Finisher<KIND, OUT == kByFour> f(p, row0);
+    typedef Finisher<KIND, OUT == kByFour> Finish;
     const Columns columns = load_columns<KIND>(p, col);
     float sa = 0.0f;                                   // of row tid % 64
     if constexpr (KIND == kI8) sa = p.sa[min(row0 + lane, p.M - 1)];
     __syncthreads();
     with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
-        u32x4 part = f.load(r, col);
+        Finish f(p, row0 + wr, in_wave, col);
+        u32x4 part = f.load(0);
 #pragma unroll 1
-        for (int i = r; i < 64; i += dr) {
+        for (int i = wr; i < 64; i += dr) {            // uniform
             const u32x4 now = part;
-            part = f.load(i + dr, col);
-            const Sum* e = s_c + i * kAnyOut + lc;
+            f.next_r(dr);
+            part = f.load(0);
+            const Sum* e = s_c + (i + in_wave) * kAnyOut + lc;
             Sum4 u = {0, 0, 0, 0};
             if constexpr (ACT == MOE_EPI_SWIGLU) u = *reinterpret_cast<const Sum4*>(e + 32);
-            f.template finish<ACT>(i, col, *reinterpret_cast<const Sum4*>(e), u, columns, KIND == kI8 ? __shfl(sa, i, kWave) : 0.0f,
-                                   now);
+            f.template finish<ACT>(0, *reinterpret_cast<const Sum4*>(e), u, columns,
+                                   KIND == kI8 ? __shfl(sa, i + in_wave, kWave) : 0.0f, now);
+            f.next_c(dr);
         }
     });
 }
@@ -736,15 +772,18 @@ __device__ __forceinline__ void phase_end_lds() {
 // bank conflicts), so that a lane ends up with four columns of a row.  KG waves hold sums of the same rows, added in
 // LDS in their order: `mine` is the wave's place, `parts` the first's, the others' STRIDE places apart.  One copy of the
 // code for all of the registers: rows are loaded and finished in a loop, and only the way to LDS is written out.
+// `first` is the wave's first row.
 template <int KIND, int NA, int KG, int STRIDE, bool VEC>
-__device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const typename Sums<KIND>::sixteen (&acc)[NA][2],
+__device__ __forceinline__ void finish_tile(const DenseArgs& p, const typename Sums<KIND>::sixteen (&acc)[NA][2],
                                             typename Sums<KIND>::one (*mine)[64], const typename Sums<KIND>::one (*parts)[64],
                                             int kg, int first, int col, const Columns& columns,
                                             const float (&sa)[(NA + 1) / 2]) {
     typedef typename Sums<KIND>::one Sum;
     typedef typename Sums<KIND>::four Sum4;
+    typedef Finisher<KIND, VEC> Finish;
     const int lane = threadIdx.x & (kWave - 1);
-    const int lc = f.p.gated ? (lane & 7) * 4 : (lane & 15) * 4, lr = f.p.gated ? lane >> 3 : lane >> 4;
+    const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
+    const int lr = p.gated ? lane >> 3 : lane >> 4;    // of the rows that a wave takes at once
     auto put = [&](auto i, auto hf) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -756,18 +795,20 @@ __device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const 
         // keeps the compiler from making one block of two cases, whose registers would have to lie in memory
         asm volatile("; rows %0" ::"n"(decltype(i)::value * 2 + decltype(hf)::value));
     };
-    with_activation(f.p.act, [&](auto act) __attribute__((always_inline)) {
+    with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         constexpr int dr = ACT == MOE_EPI_SWIGLU ? 8 : 4;      // rows a wave takes at once
         constexpr int R = KG * dr < 16 ? 16 / (KG * dr) : 1;   // times that for its share of 16
         const int mine0 = kg * dr;                             // the first of it; 16 and more: none
         u32x4 part[R];
-        auto load = [&](int g) __attribute__((always_inline)) {
+        Finish f(p, first, lr, col);
+        auto load = [&]() __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) part[i] = f.load(first + g * 16 + mine0 + i * KG * dr + lr, col);
+            for (int i = 0; i < R; ++i) part[i] = f.load(mine0 + i * KG * dr);
+            f.next_r(16);
         };
         constexpr bool kAhead = KIND == kI8 || NA < 4;         // 128 float32 sums and 48 of fragments leave no room for it
-        if (kAhead && mine0 < 16) load(0);
+        if (kAhead && mine0 < 16) load();
 #pragma unroll 1
         for (int g = 0; g < NA * 2; ++g) {
             switch (g) {                               // uniform
@@ -783,28 +824,34 @@ __device__ __forceinline__ void finish_tile(const Finisher<KIND, VEC>& f, const 
             if constexpr (KG > 1) phase_end_lds();
             if (mine0 < 16) {
                 u32x4 now[R];
-                if constexpr (!kAhead) load(g);
+                if constexpr (!kAhead) load();
 #pragma unroll
                 for (int i = 0; i < R; ++i) now[i] = part[i];
-                if (kAhead && g + 1 < NA * 2) load(g + 1);
+                if (kAhead && g + 1 < NA * 2) load();
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const int r = mine0 + i * KG * dr + lr, x = (r & 4) * 8;
-                    Sum4 v = {0, 0, 0, 0}, u = v;
+                    Sum4 v = {0, 0, 0, 0}, u = v, ev[KG], eu[KG];
 #pragma unroll
                     for (int q = 0; q < KG; ++q) {
                         const Sum* e = &parts[q * STRIDE * 16 + r][0];
-                        v += *reinterpret_cast<const Sum4*>(e + (lc ^ x));
-                        if constexpr (ACT == MOE_EPI_SWIGLU) u += *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
+                        ev[q] = *reinterpret_cast<const Sum4*>(e + (lc ^ x));
+                        if constexpr (ACT == MOE_EPI_SWIGLU) eu[q] = *reinterpret_cast<const Sum4*>(e + ((lc + 32) ^ x));
                     }
-                    const int row = g * 16 + r;
+                    if constexpr (KG > 1) __builtin_amdgcn_sched_barrier(0);   // all on their way before the first is added
+#pragma unroll
+                    for (int q = 0; q < KG; ++q) {
+                        v += ev[q];
+                        if constexpr (ACT == MOE_EPI_SWIGLU) u += eu[q];
+                    }
                     float scale = 0.0f;
                     if constexpr (KIND == kI8) {
-                        scale = __shfl(sa[0], row, kWave);
-                        if constexpr (NA > 2) scale = g < 4 ? scale : __shfl(sa[1], row, kWave);
+                        scale = __shfl(sa[0], g * 16 + r, kWave);
+                        if constexpr (NA > 2) scale = g < 4 ? scale : __shfl(sa[1], g * 16 + r, kWave);
                     }
-                    f.template finish<ACT>(first + row, col, v, u, columns, scale, now[i]);
+                    f.template finish<ACT>(mine0 + i * KG * dr, v, u, columns, scale, now[i]);
                 }
+                f.next_c(16);
             }
             if constexpr (KG > 1) phase_end_lds();
         }
@@ -979,8 +1026,7 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         if (!late) phase_end();                        // the late waves' last multiply
 
         if constexpr (NA >= 4) load_scales();
-        const Finisher<KIND, VEC> f(p, m_tile * UM);
-        finish_tile<KIND, NA, KG, MW * NW>(f, acc, s_e[wave], s_e[mh * NW + nq], kg, first, col, columns, sa);
+        finish_tile<KIND, NA, KG, MW * NW, VEC>(p, acc, s_e[wave], s_e[mh * NW + nq], kg, m_tile * UM + first, col, columns, sa);
         if (!more) break;
         tile += G;
         cur = next;
@@ -1097,16 +1143,17 @@ int launch_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t st) {
     }
 }
 
-// Whether the rows of a tile, of A, R and C, lie within a buffer's range.
-inline bool rows_near(const DenseArgs& p) {
+// Whether the rows of a tile, of A, and that many rows of R and C lie within a buffer's range.
+inline bool a_near(const DenseArgs& p) { return p.lda * 256 <= kBufferRange; }
+inline bool out_near(const DenseArgs& p, int rows) {
     const int64_t widest = std::max(p.ldc * (p.c_dtype == MOE_F32 ? 4 : 2), p.r == nullptr ? 0 : p.ldr * (p.r_dtype == MOE_F32 ? 4 : 2));
-    return p.lda * 256 <= kBufferRange && widest * 256 + MOE_DENSE_MAX_COLS * 4 <= kBufferRange;
+    return widest <= (kBufferRange - MOE_DENSE_MAX_COLS * 4) / rows;
 }
 
 template <int KIND>
 int launch_any(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     const dim3 g(static_cast<unsigned>(pairs), (p.M + 63) / 64);
-    if (KIND == kI8 || !rows_near(p))                  // int8 rows within reach take another kernel
+    if (KIND == kI8 || !out_near(p, 16))               // int8 rows within reach take another kernel
         hipLaunchKernelGGL((dense_any_kernel<KIND, kFarRows>), g, dim3(256), 0, st, p);
     else if constexpr (KIND != kI8) {
         if (p.vec) hipLaunchKernelGGL((dense_any_kernel<KIND, kByFour>), g, dim3(256), 0, st, p);
@@ -1124,10 +1171,10 @@ int launch_dense(const DenseArgs& p, int64_t pairs, hipStream_t st) {
     const bool rows16 = reinterpret_cast<uintptr_t>(p.a) % 16 == 0 && p.lda % 16 == 0 && p.K % 8 == 0;
     // byte offsets within a tile of rows stay below the buffer range (streaming finishes an element at a time, at any
     // address of C and R)
-    const bool near = p.lda * 256 <= kBufferRange;
+    const bool near = a_near(p);
     const Choice stream = stream_choice(p, pairs, rows16);
     const bool few = near && p.M <= kStreamRows;
-    if (rows16 && rows_near(p)) {
+    if (rows16 && near && out_near(p, 16)) {
         // 96 x 12288 x 4096: tiles 38.5 us, streaming 64.8; 256 x 1024 x 4096: 19.6 and 13.6
         const Choice tile = tile_choice(p, pairs);
         if (!few || stream.ns > tile.ns)

@@ -266,7 +266,6 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
     with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         constexpr bool kGated = ACT == MOE_EPI_SWIGLU;
-        const Finisher<kI8, VEC> f(p, row0);
         for (int i = tid; i < MT * CT * (kGated ? 32 : 64); i += kNW * 64) {
             const int q = i & 15, v = (i >> 4) & 3, t = i >> 6;        // lanes 4 q .. 4 q + 3
             const int m = kGated ? t / (CT / 2) : t / CT, c = kGated ? t % (CT / 2) * 2 : t % CT;
@@ -274,7 +273,8 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
             const int col = kGated ? pair * 32 + in : pair * 64 + (c & 1) * 32 + in;
             const float sa = p.sa[min(row0 + row, p.M - 1)];
             const Columns columns = load_columns<kI8>(p, col);
-            const u32x4 part = f.load(row, col);
+            const Finisher<kI8, VEC> f(p, row0, row, col);
+            const u32x4 part = f.load(0);
             intx4 s = {0, 0, 0, 0}, u = s;
 #pragma unroll
             for (int w = 0; w < kNW; ++w) {
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
                 s += *reinterpret_cast<const intx4*>(e);
                 if constexpr (kGated) u += *reinterpret_cast<const intx4*>(e + 256);
             }
-            f.template finish<ACT>(row, col, s, u, columns, sa, part);
+            f.template finish<ACT>(0, s, u, columns, sa, part);
         }
     });
 }
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256, NA == 1 || (NA == 2 && VEC) ? 3 : 2) void int8
 #pragma unroll
     for (int i = 0; i < (NA + 1) / 2; ++i) sa[i] = p.sa[min(row0 + i * 64 + lane, p.M - 1)];
     int(*mine)[64] = reinterpret_cast<int(*)[64]>(s_a + wave * 4096);
-    finish_tile<kI8, NA, 1, 1>(Finisher<kI8, VEC>(p, row0), acc, mine, mine, 0, 0, col, columns, sa);
+    finish_tile<kI8, NA, 1, 1, VEC>(p, acc, mine, mine, 0, row0, col, columns, sa);
 }
 
 // Rows of a tile: the least time expected.  Tiles take a launch, and the busiest CU's tiles one after another, each a fixed
@@ -573,7 +573,7 @@ int launch_dense_gemm_int8(const moe_dense_shape& s, const int8_t* a, int64_t ld
     p.Kh = s.K / 2;
     p.Kp = k_padded<kI8>(s);
     const int64_t pairs = pairs_of(s);
-    if (!rows_near(p)) return launch_any<kI8>(p, pairs, st);
+    if (!a_near(p) || !out_near(p, 64)) return launch_any<kI8>(p, pairs, st);   // 64 rows of a unit of int8_rows_kernel
     const bool rows16 = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda % 16 == 0;
     const Choice rows = rows_choice(p, pairs, rows16);
     if (!rows16)
