@@ -438,8 +438,11 @@ int launch_shapes(const RowArgs& p, hipStream_t st) {
     if (groups <= 64) return launch_shape<NORM, XB, RB, PAST, 64, 1>(p, 0, st);
     auto whole = [](int n) { return (n + kWave - 1) / kWave * kWave; };
     const int one = whole(groups), two = whole((groups + 1) / 2);
-    if (groups <= kWholeGroup && (p.rows * (one / kWave) <= kFewWaves || (!NORM && one < 2 * two)))
-        return launch_shape<NORM, XB, RB, PAST, kWholeGroup, 1>(p, one, st);
+    // nine bytes of output an element at most: a norm's few waves write less than the caches hold
+    static_assert(kFewWaves * kWave * 8 * 9 <= kL2Bytes, "");
+    if constexpr (!NORM || !PAST)
+        if (groups <= kWholeGroup && (p.rows * (one / kWave) <= kFewWaves || (!NORM && one < 2 * two)))
+            return launch_shape<NORM, XB, RB, PAST, kWholeGroup, 1>(p, one, st);
     if (groups <= 128) return launch_shape<NORM, XB, RB, PAST, 64, 2>(p, 0, st);
     if (groups <= 2 * kWholeGroup) return launch_shape<NORM, XB, RB, PAST, kWholeGroup, 2>(p, two, st);
     return launch_shape<NORM, XB, RB, PAST, kWholeGroup, 0>(p, kWholeGroup, st);
