@@ -28,8 +28,9 @@ __all__ = ["MOE_I8", "MOE_MXFP8", "moe_add_rmsnorm", "moe_quantize_int8", "moe_p
 
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
 _CODES = {MOE_I8: torch.int8, MOE_MXFP8: torch.uint8}
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# bound once; a torch without a GPU has neither, and no call there gets past the check of its first tensor
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dt(t: torch.Tensor) -> int:
