@@ -2,7 +2,8 @@
 //   C = act(A W + bias) + R,   or, gated,   C = silu(A Wg + bg) * (A Wu + bu) + R,
 // A [M, K] 16-bit, W [K, N] packed once, sums in float32, one rounding to C's type; or
 // A and W in int8 codes, sums in int32, with a scale per row and per column.  The
-// kernels and the choice among them, for dense.hip and dense_int8.hip.
+// kernels of the 16-bit products and the choice among them, and what dense_int8.hip
+// shares: the epilogues, weight streaming for a few rows, the kernel for rows far apart.
 //
 // Packed weights are the grouped GEMMs' fragment blocks of 32 columns x 16 k, K
 // padded to a multiple of 64 and the columns to whole 64-column pairs (gated:
@@ -409,6 +410,7 @@ enum OutRows { kByFour = 0, kByOne = 1, kFarRows = 2 };
 
 template <int KIND, int OUT>
 __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
+    static_assert(KIND != kI8 || OUT == kFarRows, "int8 rows within reach have kernels of their own");
     __shared__ __attribute__((aligned(16))) uint16_t s_a[2][64 * kAnyLd];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -495,31 +497,26 @@ __global__ __launch_bounds__(256) void dense_any_kernel(DenseArgs p) {
                 const Sum* e = s_c + r * kAnyOut + lc + i;
                 finish<KIND>(p, row0 + r, col + i, *e, p.gated ? e[32] : 0);
             }
-        return;
-    }
-    typedef typename Sums<KIND>::four Sum4;
-    typedef Finisher<KIND, OUT == kByFour> Finish;
-    const Columns columns = load_columns<KIND>(p, col);
-    float sa = 0.0f;                                   // of row tid % 64
-    if constexpr (KIND == kI8) sa = p.sa[min(row0 + lane, p.M - 1)];
-    __syncthreads();
-    with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
-        constexpr int ACT = decltype(act)::value;
-        Finish f(p, row0 + wr, in_wave, col);
-        u32x4 part = f.load(0);
+    } else {
+        const Columns columns = load_columns<KIND>(p, col);
+        __syncthreads();
+        with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+            Finisher<KIND, OUT == kByFour> f(p, row0 + wr, in_wave, col);
+            u32x4 part = f.load(0);
 #pragma unroll 1
-        for (int i = wr; i < 64; i += dr) {            // uniform
-            const u32x4 now = part;
-            f.next_r(dr);
-            part = f.load(0);
-            const Sum* e = s_c + (i + in_wave) * kAnyOut + lc;
-            Sum4 u = {0, 0, 0, 0};
-            if constexpr (ACT == MOE_EPI_SWIGLU) u = *reinterpret_cast<const Sum4*>(e + 32);
-            f.template finish<ACT>(0, *reinterpret_cast<const Sum4*>(e), u, columns,
-                                   KIND == kI8 ? __shfl(sa, i + in_wave, kWave) : 0.0f, now);
-            f.next_c(dr);
-        }
-    });
+            for (int i = wr; i < 64; i += dr) {        // uniform
+                const u32x4 now = part;
+                f.next_r(dr);
+                part = f.load(0);
+                const Sum* e = s_c + (i + in_wave) * kAnyOut + lc;
+                floatx4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (ACT == MOE_EPI_SWIGLU) u = *reinterpret_cast<const floatx4*>(e + 32);
+                f.template finish<ACT>(0, *reinterpret_cast<const floatx4*>(e), u, columns, 0.0f, now);
+                f.next_c(dr);
+            }
+        });
+    }
 }
 
 // ---- few rows: weight streaming ------------------------------------------------------
@@ -538,9 +535,10 @@ constexpr int kNW = 8;
 // ROWS16: rows on 16 bytes and K a multiple of 8; rows past M and k past K then
 // load zeros through an out-of-range buffer offset.  Otherwise rows past M load
 // the last row (their results are dropped), and the step that K ends in is done
-// apart, element by element.
+// apart, element by element.  int8: rows on 16 bytes, at most 16 of them (others go through LDS, in dense_int8.hip).
 template <int KIND, bool ROWS16, int MT, int CT>
 struct DenseCursor {
+    static_assert(KIND != kI8 || (ROWS16 && MT == 1), "");
     const uint8_t* b;          // this lane's bytes of the step, first column half of the tile
     __amdgpu_buffer_rsrc_t rows;
     const uint8_t* base;       // the tile's first row
@@ -569,7 +567,7 @@ struct DenseCursor {
                         u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                    rows, k + l * 8 < K ? off[m] + l * 16 : kOutOfRange, 0, 0));
                 else
-                    s.a[m][0][l] = load_any<KIND>(base + off[m] + l * 16);
+                    s.a[m][0][l] = load_any<kBF16>(base + off[m] + l * 16);
             }
         b += kNW * step_bytes<false>();
         k += kNW * 64;
@@ -636,7 +634,7 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
     StepRegs<1, false, MT, CT> ring[MT == 1 ? 4 : 2];
     start_steps(steps, cur, ring);
     run_steps(steps, cur, ring, acc);
-    if (!ROWS16 && p.K % (64 * codes_per_unit<KIND>()) != 0 && wave == nk % kNW) {   // the cursor stands at the last, short step
+    if (!ROWS16 && p.K % 64 != 0 && wave == nk % kNW) {   // the cursor stands at the last, short step
         StepRegs<1, false, MT, CT> last;
         cur.load_b(last);
 #pragma unroll
@@ -644,7 +642,7 @@ __global__ __launch_bounds__(kNW * 64, MT == 4 ? 1 : 2) void dense_stream_kernel
             const int row = min(m * kRowTile + (lane & 15), p.M - 1 - row0);
 #pragma unroll
             for (int l = 0; l < 2; ++l)
-                last.a[m][0][l] = load_tail<KIND>(first + static_cast<int64_t>(row) * p.lda, cur.k + l * 8, p.K);
+                last.a[m][0][l] = load_tail<kBF16>(first + static_cast<int64_t>(row) * p.lda, cur.k + l * 8, p.K);
         }
         acc.add(last);
     }
@@ -860,6 +858,7 @@ __device__ __forceinline__ void finish_tile(const DenseArgs& p, const typename S
 
 template <int KIND, bool VEC, int MW, int NW, int NA, int SL>
 __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+    static_assert(KIND != kI8, "int8 tiles are dense_int8.hip's");
     constexpr int KG = 8 / (MW * NW);                  // wave groups along k
     constexpr int WS = SL * 2 / KG;                    // k-steps of 16 of a wave per stage
     constexpr int UM = MW * NA * 32;                   // rows of the tile
@@ -871,8 +870,7 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     static_assert(BD <= 4 && 4 % BD == 0, "a wave's weight blocks lie in one pair and slice");
     __shared__ __attribute__((aligned(16))) uint16_t s_a[kTileNB][AC * 8 * 16 * kTileBK];   // [slice][row][32]
     __shared__ __attribute__((aligned(16))) uint16_t s_b[kTileNB][SL * NW * 4][512];        // [slice][pair][4]
-    typedef typename Sums<KIND>::one Sum;
-    __shared__ __attribute__((aligned(16))) Sum s_e[8][16][64];     // epilogue: 16 rows of each wave
+    __shared__ __attribute__((aligned(16))) float s_e[8][16][64];     // epilogue: 16 rows of each wave
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool late = wave >= 4;                       // reads in odd phases
@@ -955,21 +953,14 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
     for (;;) {
         const bool more = tile + G < total;            // uniform
         const Source next = source(more ? tile + G : tile);
-        // what the epilogue needs of this tile's columns and rows, loaded ahead where registers are left for it
+        // what the epilogue needs of this tile's columns, loaded ahead where registers are left for it
         int m_tile, n_tile;
         place(tile, m_tile, n_tile);
         const int lc = p.gated ? (lane & 7) * 4 : (lane & 15) * 4;
         const int first = mh * NA * 32, col = (n_tile * NW + nq) * (p.gated ? 32 : 64) + lc;   // of the wave's part
         Columns columns;
-        float sa[(NA + 1) / 2];                        // of the wave's rows lane, lane + 64
-        auto load_scales = [&]() __attribute__((always_inline)) {
-            columns = load_columns<KIND>(p, col);
-#pragma unroll
-            for (int i = 0; i < (NA + 1) / 2; ++i)
-                sa[i] = KIND == kI8 ? p.sa[min(m_tile * UM + first + i * 64 + lane, p.M - 1)] : 0.0f;
-        };
-        if constexpr (NA < 4) load_scales();
-        typename Sums<KIND>::sixteen acc[NA][2];
+        if constexpr (NA < 4) columns = load_columns<KIND>(p, col);
+        floatx16 acc[NA][2];
 #pragma unroll
         for (int i = 0; i < NA; ++i)
 #pragma unroll
@@ -1025,8 +1016,9 @@ __global__ __launch_bounds__(512, 1) void dense_tile_kernel(DenseArgs p, int mti
         }
         if (!late) phase_end();                        // the late waves' last multiply
 
-        if constexpr (NA >= 4) load_scales();
-        finish_tile<KIND, NA, KG, MW * NW, VEC>(p, acc, s_e[wave], s_e[mh * NW + nq], kg, m_tile * UM + first, col, columns, sa);
+        if constexpr (NA >= 4) columns = load_columns<KIND>(p, col);
+        constexpr float no_scales[(NA + 1) / 2] = {};
+        finish_tile<KIND, NA, KG, MW * NW, VEC>(p, acc, s_e[wave], s_e[mh * NW + nq], kg, m_tile * UM + first, col, columns, no_scales);
         if (!more) break;
         tile += G;
         cur = next;
