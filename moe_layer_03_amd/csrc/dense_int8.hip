@@ -302,7 +302,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 // card.  Bound by the matrix unit at the clock that the power limit leaves (1.75 GHz: half of the cycles multiply) and the
 // latency of the weights.
 template <bool VEC, int NA>
-__global__ __launch_bounds__(256, NA == 1 || (NA == 2 && VEC) ? 3 : 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
+__global__ __launch_bounds__(256, NA <= 2 ? 3 : 2) void int8_tile_kernel(DenseArgs p, int mtiles, int ntiles, int pairs) {
     constexpr int UM = NA * 32, kStage = UM * 128, kStages = 4;
     __shared__ __attribute__((aligned(16))) uint8_t s_a[kStages * kStage > 16384 ? kStages * kStage : 16384];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
