@@ -476,6 +476,8 @@ int moe_dense_gemm(const moe_dense_shape* s, const void* a, int a_dtype, int64_t
  *   h = x + residual, a float32 sum rounded to the residual's type; h = x
  *       without one.  h is what is normed and what `sum` receives.
  *   s = 1 / sqrt(mean(h^2) + eps), mean and root in double, s rounded to float32
+ *       (the sum's order is not specified: another one gives the neighbouring
+ *       float32 in fewer than one row of a million; every call gives the same)
  *   v = (h * s) * weight, two float32 products (weight NULL: h * s)
  *   y = v rounded to y_dtype; codes and scales are v's, not y's.
  * x, residual, sum, y: rows of H values, ldx, ldr, lds, ldy >= H elements apart,
@@ -541,7 +543,8 @@ int moe_pack_dense_int8(const moe_dense_shape* s, const void* w, const void* w_u
 
 /*
  * moe_dense_gemm_int8 -- the product on packed codes.
- *   a: rows of K codes, lda >= K apart, any alignment; a_scales float32 [M].
+ *   a: rows of K codes, lda >= K apart, any alignment; a_scales float32 [M], of
+ *       any sign, as the columns' scales are.
  *       Rows that all start on 16 bytes take the fast paths (where K is no
  *       multiple of 16, up to 15 bytes between a row's end and the next row may be
  *       read, which change nothing; nothing behind the last row's end is read).

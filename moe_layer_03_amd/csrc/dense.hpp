@@ -196,10 +196,10 @@ __device__ __forceinline__ floatx4 scaled4(const intx4& v, float sa, const float
 }
 
 // C and R from row `first` on, as buffers; the launcher keeps the offsets of the rows reached from there below the range.
-// A tile's epilogue goes on 16 rows at a time, which costs a few scalar instructions: so rows may lie 128 MiB apart (1024 x
-// 4096 x 4096 into rows 8 MiB apart 38 us; with one base for all of a tile's rows such C fell to dense_any_kernel, an
-// element at a time, 72 us).  A lane's row is u, uniform, and its own beyond that: the offset of a part of C or R is a
-// register, a scalar and a constant.
+// A tile's epilogue goes on 16 rows at a time, which costs a few scalar instructions: so rows may lie some 128 MiB apart
+// (1024 x 4096 x 4096 into rows 8 MiB apart 38 us; with one base for all of a tile's rows such C fell to
+// dense_any_kernel, an element at a time, 72 us).  A lane's row is u, uniform, and its own beyond that: the offset of a
+// part of C or R is a register, a scalar and a constant.
 template <int KIND, bool VEC>
 struct Finisher {
     const DenseArgs& p;

@@ -1,7 +1,7 @@
 // Dense products of int8 codes with a scale per row of A and per column of W:
 //   C = act((sum_k a w) sa sw + bias) + R,   or, gated, with a gate and an up weight.
 // The sums are int32 and exact (K is at most 131071, |a w| at most 2^14), so no order of them matters; the kernels
-// are the 16-bit products' (dense.hpp), whose operands hold sixteen codes in the bytes of eight values.
+// are of the 16-bit products' kind (dense.hpp), with sixteen codes in the bytes of eight values.
 //
 // Packed weights: the 16-bit layout with a code in each byte, blocks of 32 columns x 32 k, K padded to a multiple of
 // 128; then the columns' scales, padded to the packed columns (gated: the gate's, then the up's).
@@ -11,13 +11,14 @@
 namespace moe {
 namespace {
 
-// Scales of 64 columns (int8 rule over K); 16 waves share the k out.
 template <typename ST>
 __device__ __forceinline__ float weight_at(const ST* w, int64_t i, int dtype) {
     if constexpr (sizeof(ST) == 4) return w[i];
     else return dtype == MOE_BF16 ? bf16_to_f32(w[i]) : f16_to_f32(w[i]);
 }
 
+// Scales of 64 columns (int8 rule over K); 16 waves share the k out.  Few workgroups, and the weights are read again for
+// the codes: packing 4096 x 4096 takes 110 us from bf16, 16 from codes, once for a model's weights.
 template <typename ST>
 __global__ __launch_bounds__(1024) void column_scales_kernel(const ST* __restrict__ w, int dtype, int N, int K,
                                                              float* __restrict__ scales) {
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kNW * 64, MT < 4 ? 4 : 2) void int8_rows_kernel(Den
 // Where K ends inside a granule the last stage's copies bring what lies behind it, but the last row's end comes code by
 // code, as above (2000 x 4096 x 4090, rows 4096 apart, 42.2 us, 71.3 by int8_rows_kernel; K 4096 42.2).
 // The loop has no branch around a load and the fragments of a step are asked for before the step before is multiplied:
-// 6000 x 4096 x 4096 97.8 us (2060 TOP/s; a library product 101.7), with bias and SiLU 100.1, 107 with such branches;
+// 6000 x 4096 x 4096 97 us (2080 TOP/s; a library product 101.7), with bias and SiLU 99.7, 107 with such branches;
 // gated, 1536 columns, 77; the 16-bit products' kernel, one workgroup of 8 waves to a CU: 109, 110 and 97 on the same
 // card.  Bound by the matrix unit at the clock that the power limit leaves (1.75 GHz: half of the cycles multiply) and the
 // latency of the weights.
@@ -436,8 +437,8 @@ __global__ __launch_bounds__(256, NA <= 2 ? 3 : 2) void int8_tile_kernel(DenseAr
 }
 
 // Rows of a tile: the least time expected.  Tiles take a launch, and the busiest CU's tiles one after another, each a fixed
-// part and a part by the reduction (ns, of 4096 k); a CU's only tile waits for its loads a little longer.  Within 12 % of
-// measured times from 18 to 480 us.
+// part and a part by the reduction (ns, of 4096 k); a CU's only tile waits for its loads a little longer.  Measured with N
+// a multiple of four and K of sixteen: there within 13 % in nine of ten, 17 % at most, from 16 to 97 us.
 struct TileCost {
     double ends, whole;
 };
@@ -478,8 +479,10 @@ int launch_int8_tiles(const DenseArgs& p, int64_t pairs, int shape, hipStream_t 
 // Unit shapes of int8_rows_kernel, and the time expected of each: a launch, what the shape takes at the ends (ns), and
 // what the busiest CU reads (bytes/ns), its first unit and then the others at the rate they reach together, but no less
 // than a unit takes anyhow; rows off 16 bytes pass through registers, more slowly (32 rows x 64 columns then leave room
-// for one workgroup on a CU: not taken).  Mostly within 15 % of measured times from 3.5 to 60 us, and the shape chosen
-// within 8 % of the best.
+// for one workgroup on a CU: not taken).  Measured with N a multiple of four: within 16 % from 3.5 to 25 us (19 % at 512 x
+// 512, 3000 rows and more), and the kernel and shape chosen within 4 % of the best but for three sizes of 72 (15 to 31 %).
+// Stores of an element each, where N is none, and K's end are in no figure: 2000 x 2050 x 1000 is expected to take 13.7
+// us here and takes 23.4, 17.3 in tiles.
 struct RowsShape {
     int mt, ct;
     double ends, rate, rate_any, least;

@@ -2,10 +2,13 @@
 //   h = x + residual (rounded to the residual's type),   s = 1 / sqrt(mean(h^2) + eps),   v = (h s) w,
 // and the codes of v, or of rows given, in 8 bits: int8 with a scale per row, MXFP8 with one per 32.
 //
-// The mean and s are computed in double and s is rounded to float32; v takes two float32 products.  A double sum
-// differs by 2^-50 or so from one order of summation to another, which moves the rounded s once in millions of
-// rows; so v, and the codes, which turn on which side of a half a quotient lies, do not depend on the order, nor on
-// the kernel's shape.  The conversion and the double fma of an element cost what two float32 operations do.
+// The mean and s are computed in double and s is rounded to float32; v takes two float32 products.  A thread adds up n
+// squares, at most 16 for H to 2^14 and 8 ceil(H / 8192) beyond, before ten steps join the threads, so an order of
+// summation is off by (n + 10) 2^-53 of the sum at most and by half of that in s, whose double steps add 2^-52.  That moves
+// the rounded s to its neighbour where s lies that close to the middle of two: in fewer than one row of ten million, of a
+// million for the longest.  In all others v, and the codes, which turn on which side of a half a quotient lies, depend
+// neither on the order nor on the kernel's shape.  The conversion and the double fma of an element cost what two float32
+// operations do.
 //
 // Bound by memory: 6000 x 4096, bf16 in, sum and out with int8 codes, moves 221 MB in 42.8 us, 5.2 TB/s, a large copy's
 // rate; 16384 x 1536 quantised 75 MB in 17.4 us (4.3 TB/s, two rounds of rows and a launch).  Few rows are bound by the

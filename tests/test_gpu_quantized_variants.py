@@ -75,8 +75,8 @@ def id_of(v):
 @pytest.mark.parametrize("case", list(sizes.norms()), ids=id_of)
 def test_norms(case):
     """Rows a few elements apart, at odd places where H is odd: what lies between them stays.  A double's sum in another
-    order moves a row's s by a step of float32 once in 2^20 rows or so, of which there are some million here: such a row is
-    compared with the neighbouring s."""
+    order may move a row's s by a step of float32, in fewer than one row of a million: such a row is compared with the
+    neighbouring s."""
     rows, H, xt, rt, yt, want_codes = case
     x, r, w = rows_inputs(rows, H, xt, rt, rows + H)
     pad = 3 if H % 2 else 8
