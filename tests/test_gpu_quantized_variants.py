@@ -153,3 +153,51 @@ def test_quantisers(case):
     _, scales = Q.moe_quantize_int8(x, codes=codes)
     check_int8(x.float(), codes, scales)
     assert untouched(buf, codes, 99)
+
+
+# ---- the largest calls ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,K,gated", [(8, 48, False), (6, 41, True), (196, 48, False), (100, 48, True)])
+def test_most_rows_of_a_product(N, K, gated):
+    M = 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(N)
+    d = inputs(1, N, K, "swiglu" if gated else "none", seed=N)
+    a = torch.randint(-128, 128, (M, (K + 15) // 16 * 16), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+    sa = torch.rand(M, generator=g, device="cuda")
+    s = B.DenseShape(M, N, K, gated=gated)
+    act = "swiglu" if gated else "none"
+    got = Q.moe_dense_gemm_int8(s, a, sa, pack(s, d), EPI[act], c_dtype=torch.float32)
+    ref, bound = reference(a, sa, d["w"], d["sw"], None, None, act, "f32")
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("K", [48, 41])
+@pytest.mark.parametrize("gated", [False, True])
+def test_most_columns_of_a_product(M, K, gated):
+    N = 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(M)
+    w = [torch.randint(-128, 128, (K, N), generator=g, device="cuda", dtype=torch.int8) for _ in range(1 + gated)]
+    sw = [torch.rand(N, generator=g, device="cuda") * 1e-3 for _ in w]
+    a = torch.randint(-128, 128, (M, 48), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+    sa = torch.rand(M, generator=g, device="cuda")
+    s = B.DenseShape(M, N, K, gated=gated)
+    act = "swiglu" if gated else "none"
+    packed = Q.moe_pack_dense_int8(s, *w, scales=sw[0], up_scales=sw[1] if gated else None)
+    got = Q.moe_dense_gemm_int8(s, a, sa, packed, EPI[act], c_dtype=torch.float32)
+    ref, bound = reference(a, sa, w, sw, None, None, act, "f32")
+    assert ((got.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("H", [8, 136, 520, 1032])
+def test_most_rows_of_a_quantiser_and_a_norm(H):
+    rows = 1 << 21
+    x, _, w = rows_inputs(rows, H, "bf16", None, H)
+    codes, scales = Q.moe_quantize_int8(x)
+    some = torch.cat([torch.arange(0, rows, 4099), torch.arange(rows - 70, rows)]).cuda()
+    check_int8(x[some].float(), codes[some], scales[some])
+    del codes, scales
+    _, y, codes, scales = Q.moe_add_rmsnorm(x, w, eps=EPS, y_dtype=torch.bfloat16, q_dtype=Q.MOE_I8)
+    _, v = normed(x[some], None, w)
+    check_int8(v, codes[some], scales[some])
+    assert torch.equal(y[some], to_type(v, torch.bfloat16))
